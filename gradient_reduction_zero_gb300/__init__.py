@@ -12,7 +12,9 @@ import importlib
 _BINDING = {"AdamWCfg", "DpzError", "dp_allgather", "dp_allreduce_avg", "dp_grad_global_norm",
             "dp_grad_global_norm_static", "dp_reduce_scatter_avg", "dp_reduce_scatter_avg_range",
             "dp_reduce_scatter_avg_bucket", "dp_grad_norm_finalize", "dp_zero1_step",
-            "dp_zero1_update", "dp_zero2_update", "make_cfg", "workspace", "zero1_adamw_step"}
+            "dp_zero1_update", "dp_zero2_update", "make_cfg", "workspace", "zero1_adamw_step",
+            "lm_embedding", "lm_embedding_grad", "lm_embedding_workspace", "lm_logprobs",
+            "lm_logprobs_grad", "lm_distill", "lm_distill_grad", "lm_distill_step"}
 
 
 def __getattr__(name):

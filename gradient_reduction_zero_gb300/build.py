@@ -20,8 +20,10 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdpz.so")
 
-SOURCES = ["api.cpp", "reduce.cu", "adamw.cu", "staged.cu", "norm_static.cu"]
-HEADERS = [os.path.join(CSRC, h) for h in ("internal.h", "device.cuh", "bulk.cuh")] + \
+SOURCES = ["api.cpp", "reduce.cu", "adamw.cu", "staged.cu", "norm_static.cu", "lm_api.cpp",
+           "lm_embed.cu", "lm_logits.cu"]
+HEADERS = [os.path.join(CSRC, h) for h in ("internal.h", "api_util.h", "lm.h", "device.cuh",
+                                          "bulk.cuh")] + \
     [os.path.join(INCLUDE, "dpz.h")]
 
 NVCC_FLAGS = [

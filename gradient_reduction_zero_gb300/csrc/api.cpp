@@ -15,14 +15,14 @@
 #include <string>
 #include <vector>
 
+#include "api_util.h"
 #include "internal.h"
 
-using namespace dpz;
+namespace dpz {
 
-namespace {
-
-thread_local std::string g_err;
+static thread_local std::string g_err;
 std::atomic<int64_t> g_launches{0};
+Profiler g_prof;
 
 int fail(int code, const char* fmt, ...)
 {
@@ -41,7 +41,13 @@ int ok()
     return DPZ_OK;
 }
 
-int elem_bytes(int dt) { return dt == DPZ_F32 ? 4 : 2; }
+static const char* last_error() { return g_err.c_str(); }
+
+}  // namespace dpz
+
+using namespace dpz;
+
+namespace {
 
 // ------------------------------------------------------------ validation
 
@@ -83,45 +89,6 @@ int check_ptr(const void* p, const char* what, int dt = DPZ_BF16)
     return DPZ_OK;
 }
 
-struct Range {
-    const char* name;
-    uintptr_t lo, hi;
-};
-
-Range range(const char* name, const void* p, int64_t bytes)
-{
-    uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return {name, lo, lo + static_cast<uintptr_t>(bytes)};
-}
-
-// The byte ranges of one call's buffers, held on the stack (no allocation on
-// the launch path).  A NULL buffer is not added.  No call has more than seven
-// buffers; one past kMax would be dropped, never written out of bounds.
-struct Ranges {
-    static constexpr int kMax = 8;
-    Range r[kMax];
-    int n = 0;
-    Ranges(std::initializer_list<Range> rs)
-    {
-        for (const Range& x : rs)
-            if (n < kMax) r[n++] = x;
-    }
-    void add(const char* name, const void* p, int64_t bytes)
-    {
-        if (p != nullptr && n < kMax) r[n++] = range(name, p, bytes);
-    }
-};
-
-int check_disjoint(const Ranges& rs)
-{
-    for (int i = 0; i < rs.n; ++i)
-        for (int j = i + 1; j < rs.n; ++j)
-            if (rs.r[i].lo < rs.r[j].hi && rs.r[j].lo < rs.r[i].hi)
-                return fail(DPZ_ERR_INVALID_ARG, "buffers %s and %s overlap", rs.r[i].name,
-                            rs.r[j].name);
-    return DPZ_OK;
-}
-
 int check_cfg(const dpz_adamw_cfg* cfg)
 {
     if (cfg == nullptr) return fail(DPZ_ERR_INVALID_ARG, "cfg is NULL");
@@ -129,12 +96,6 @@ int check_cfg(const dpz_adamw_cfg* cfg)
         return fail(DPZ_ERR_INVALID_ARG, "step = %lld must be >= 1", (long long)cfg->step);
     return DPZ_OK;
 }
-
-#define DPZ_TRY(x)                     \
-    do {                               \
-        int rc_ = (x);                 \
-        if (rc_ != DPZ_OK) return rc_; \
-    } while (0)
 
 Arena make_arena(int64_t P, int N, int gdt, int wdt)
 {
@@ -168,43 +129,6 @@ AdamArgs make_adam(const dpz_adamw_cfg* cfg)
     return h;
 }
 
-// ------------------------------------------------------------ profiling
-
-struct Profiler {
-    std::mutex mu;
-    std::atomic<bool> on{false};     // read without the lock on every launch
-    int cap = 0;
-    int used = 0;
-    std::vector<cudaEvent_t> ev;
-    std::vector<std::string> names;
-};
-Profiler g_prof;
-
-template <class F>
-int launch(cudaStream_t s, F&& f)
-{
-    int slot = -1;
-    if (g_prof.on.load(std::memory_order_acquire)) {
-        std::lock_guard<std::mutex> lk(g_prof.mu);
-        if (g_prof.on.load(std::memory_order_relaxed) && g_prof.used < g_prof.cap)
-            slot = g_prof.used++;
-    }
-    if (slot >= 0) cudaEventRecord(g_prof.ev[2 * slot], s);
-    cudaError_t e = f();
-    const char* name = last_kernel_name();
-    if (slot >= 0) {
-        cudaEventRecord(g_prof.ev[2 * slot + 1], s);
-        std::lock_guard<std::mutex> lk(g_prof.mu);
-        g_prof.names[slot] = name;
-    }
-    if (e != cudaSuccess)
-        return fail(DPZ_ERR_CUDA, "launch of %s failed: %s", name, cudaGetErrorString(e));
-    g_launches.fetch_add(1, std::memory_order_relaxed);
-    return DPZ_OK;
-}
-
-cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
-
 }  // namespace
 
 // ====================================================================== ABI
@@ -217,7 +141,7 @@ DPZ_API size_t dpz_workspace_bytes(int64_t P, int N)
     return ws_bytes_for(P, N);
 }
 
-DPZ_API const char* dpz_last_error(void) { return g_err.c_str(); }
+DPZ_API const char* dpz_last_error(void) { return last_error(); }
 
 DPZ_API const char* dpz_version(void) { return "dpz 0.2 (sm_103a)"; }
 

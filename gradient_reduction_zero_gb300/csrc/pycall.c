@@ -22,10 +22,11 @@ typedef union {
     void* p;
     int64_t l;
     int i;
+    float f;
 } Arg;
 
 /* fmt: one character per argument, 'p' pointer (int or None), 'l' int64,
- * 'i' int.  Sets a Python exception and returns -1 on a bad argument. */
+ * 'i' int, 'f' float.  Sets a Python exception and returns -1 on a bad argument. */
 static int parse(PyObject* const* a, Py_ssize_t n, const char* fmt, Arg* out)
 {
     const Py_ssize_t k = (Py_ssize_t)strlen(fmt);
@@ -46,6 +47,10 @@ static int parse(PyObject* const* a, Py_ssize_t n, const char* fmt, Arg* out)
             const long long v = PyLong_AsLongLong(o);
             if (v == -1 && PyErr_Occurred()) return -1;
             out[j].l = (int64_t)v;
+        } else if (fmt[j] == 'f') {
+            const double v = PyFloat_AsDouble(o);
+            if (v == -1.0 && PyErr_Occurred()) return -1;
+            out[j].f = (float)v;
         } else {
             const long v = PyLong_AsLong(o);
             if (v == -1 && PyErr_Occurred()) return -1;
@@ -97,6 +102,27 @@ CALL(dp_zero1_update, "pppppliiippp", 12,
 CALL(dp_zero2_update, "pppppliiippp", 12,
      dp_zero2_update(s[0].p, F(1), F(2), F(3), s[4].p, s[5].l, s[6].i, s[7].i, s[8].i, CFG(9),
                      s[10].p, s[11].p))
+CALL(lm_embedding, "plllipilfplip", 13,
+     lm_embedding(s[0].p, s[1].l, s[2].l, s[3].l, s[4].i, s[5].p, s[6].i, s[7].l, s[8].f, s[9].p,
+                  s[10].l, s[11].i, s[12].p))
+CALL(lm_embedding_grad, "plipilfplplillpp", 16,
+     lm_embedding_grad(s[0].p, s[1].l, s[2].i, s[3].p, s[4].i, s[5].l, s[6].f, s[7].p, s[8].l,
+                       s[9].p, s[10].l, s[11].i, s[12].l, s[13].l, s[14].p, s[15].p))
+CALL(lm_logprobs, "plllifpipppippp", 15,
+     lm_logprobs(s[0].p, s[1].l, s[2].l, s[3].l, s[4].i, s[5].f, s[6].p, s[7].i, F(8), F(9), F(10),
+                 s[11].i, s[12].p, F(13), s[14].p))
+CALL(lm_logprobs_grad, "plllifpippppplp", 15,
+     lm_logprobs_grad(s[0].p, s[1].l, s[2].l, s[3].l, s[4].i, s[5].f, s[6].p, s[7].i, F(8), F(9),
+                      F(10), F(11), s[12].p, s[13].l, s[14].p))
+CALL(lm_distill, "plllipipiifppp", 14,
+     lm_distill(s[0].p, s[1].l, s[2].l, s[3].l, s[4].i, s[5].p, s[6].i, s[7].p, s[8].i, s[9].i,
+                s[10].f, F(11), F(12), s[13].p))
+CALL(lm_distill_grad, "plllipipiifppplp", 16,
+     lm_distill_grad(s[0].p, s[1].l, s[2].l, s[3].l, s[4].i, s[5].p, s[6].i, s[7].p, s[8].i,
+                     s[9].i, s[10].f, F(11), F(12), s[13].p, s[14].l, s[15].p))
+CALL(lm_distill_step, "plllipipiifpppplp", 17,
+     lm_distill_step(s[0].p, s[1].l, s[2].l, s[3].l, s[4].i, s[5].p, s[6].i, s[7].p, s[8].i,
+                     s[9].i, s[10].f, F(11), F(12), F(13), s[14].p, s[15].l, s[16].p))
 
 #define ENTRY(name) {#name, (PyCFunction)(void (*)(void))py_##name, METH_FASTCALL, NULL}
 
@@ -113,6 +139,13 @@ static PyMethodDef methods[] = {
     ENTRY(dp_grad_norm_finalize),
     ENTRY(dp_zero1_update),
     ENTRY(dp_zero2_update),
+    ENTRY(lm_embedding),
+    ENTRY(lm_embedding_grad),
+    ENTRY(lm_logprobs),
+    ENTRY(lm_logprobs_grad),
+    ENTRY(lm_distill),
+    ENTRY(lm_distill_grad),
+    ENTRY(lm_distill_step),
     {NULL, NULL, 0, NULL},
 };
 

@@ -16,6 +16,8 @@ LIB_PATH = os.path.join(_PKG, "libdpz.so")
 HEADER = os.path.join(os.path.dirname(_PKG), "include", "dpz.h")
 
 F32, BF16, BF16_ACC32 = 0, 1, 2
+I32, I64 = 16, 17
+LM_MAX_TOP, LM_MAX_TEACHER = 32, 256
 OK, ERR_INVALID_ARG, ERR_ALIGN, ERR_CUDA = 0, 1, 2, 3
 MAX_RANKS = 64
 # the per-call status word of a workspace (include/dpz.h)
@@ -43,6 +45,7 @@ class KernelStat(ctypes.Structure):
 
 _VP = ctypes.c_void_p
 _FP = ctypes.c_void_p     # float* (device)
+_L, _I, _F = ctypes.c_int64, ctypes.c_int, ctypes.c_float
 
 _SIGS = {
     "dpz_workspace_bytes": ([ctypes.c_int64, ctypes.c_int], ctypes.c_size_t),
@@ -68,6 +71,18 @@ _SIGS = {
                          ctypes.c_int, _VP, _VP, _VP], ctypes.c_int),
     "dp_zero2_update": ([_VP, _FP, _FP, _FP, _VP, ctypes.c_int64, ctypes.c_int, ctypes.c_int,
                          ctypes.c_int, _VP, _VP, _VP], ctypes.c_int),
+    "lm_embedding": ([_VP, _L, _L, _L, _I, _VP, _I, _L, _F, _VP, _L, _I, _VP], _I),
+    "lm_embedding_workspace_bytes": ([_L, _L, _L], ctypes.c_size_t),
+    "lm_embedding_grad": ([_VP, _L, _I, _VP, _I, _L, _F, _VP, _L, _VP, _L, _I, _L, _L, _VP, _VP],
+                          _I),
+    "lm_logprobs": ([_VP, _L, _L, _L, _I, _F, _VP, _I, _FP, _FP, _FP, _I, _VP, _FP, _VP], _I),
+    "lm_logprobs_grad": ([_VP, _L, _L, _L, _I, _F, _VP, _I, _FP, _FP, _FP, _FP, _VP, _L, _VP],
+                         _I),
+    "lm_distill": ([_VP, _L, _L, _L, _I, _VP, _I, _VP, _I, _I, _F, _FP, _FP, _VP], _I),
+    "lm_distill_grad": ([_VP, _L, _L, _L, _I, _VP, _I, _VP, _I, _I, _F, _FP, _FP, _VP, _L, _VP],
+                        _I),
+    "lm_distill_step": ([_VP, _L, _L, _L, _I, _VP, _I, _VP, _I, _I, _F, _FP, _FP, _FP, _VP, _L,
+                         _VP], _I),
     "dpz_last_error": ([], ctypes.c_char_p),
     "dpz_version": ([], ctypes.c_char_p),
     "dpz_launch_count": ([], ctypes.c_int64),
@@ -254,6 +269,190 @@ def dp_zero2_update(shards, master, m, v, weights, N: int, cfg: AdamWCfg, ws=Non
     _check(_C.dp_zero2_update(_ptr(shards), _ptr(master), _ptr(m), _ptr(v), _ptr(weights),
                                shards.numel(), N, dtype_code(shards), dtype_code(weights),
                                ctypes.addressof(cfg), _ptr(ws), _stream_handle(stream)))
+
+
+# ------------------------------------------------------------ vocabulary-sized ends
+#
+# Shapes, strides, types and devices are checked here (the C call sees
+# addresses only); sizes, alignment and overlaps by the library.
+
+def _id_code(t) -> int:
+    torch = _torch()
+    if t.dtype == torch.int64:
+        return I64
+    if t.dtype == torch.int32:
+        return I32
+    raise TypeError(f"token ids must be int32 or int64, not {t.dtype}")
+
+
+def _mat(t, what: str, rows: int = -1, cols: int = -1) -> int:
+    """The row stride of a 2-D matrix of unit column stride on a GPU."""
+    if t.dim() != 2 or (rows >= 0 and t.shape[0] != rows) or (cols >= 0 and t.shape[1] != cols):
+        raise ValueError(f"{what} must be a matrix"
+                         + (f" [{rows}, {cols}]" if rows >= 0 and cols >= 0 else "")
+                         + f", not {list(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    r, c = t.shape
+    ld, step = t.stride()
+    if step != 1 and c > 1:
+        raise ValueError(f"{what} must have unit column stride")
+    return ld if r > 1 else max(ld, c)
+
+
+def _dense(t, what: str, shape: tuple, dtype=None):
+    """None, or a dense GPU tensor of the given shape (fp32 unless dtype)."""
+    if t is None:
+        return None
+    want = dtype or _torch().float32
+    if t.dtype != want:
+        raise TypeError(f"{what} must be {want}, not {t.dtype}")
+    if tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{what} must be a dense CUDA tensor of shape {list(shape)}, "
+                         f"not {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _tokens(t, what: str, shape: tuple) -> tuple:
+    code = _id_code(t)
+    return _dense(t, what, shape, t.dtype), code
+
+
+def lm_embedding(table, ids, out, scale: float = 1.0, stream=None) -> None:
+    """out[t] = scale * table[ids[t]] (a row of zeros where ids[t] is outside
+    the table).  table [V, D] and out [T, D], bf16 or fp32 with any row
+    stride; ids [T], int32 or int64."""
+    T = ids.numel()
+    ldt = _mat(table, "table")
+    V, D = table.shape
+    ldo = _mat(out, "out", T, D)
+    p, it = _tokens(ids, "ids", (T,))
+    _check(_C.lm_embedding(table.data_ptr(), ldt, V, D, dtype_code(table), p, it, T, scale,
+                           out.data_ptr(), ldo, dtype_code(out), _stream_handle(stream)))
+
+
+def lm_embedding_workspace(T: int, V: int, D: int, device=None):
+    """A device tensor of lm_embedding_workspace_bytes(T, V, D) bytes."""
+    nb = lib.lm_embedding_workspace_bytes(T, V, D)
+    if nb == 0:
+        raise DpzError(ERR_INVALID_ARG, lib.dpz_last_error().decode())
+    return _torch().empty(nb, dtype=_torch().uint8, device=device or "cuda")
+
+
+def lm_embedding_grad(dout, ids, dtable, ws, base=None, scale: float = 1.0, stream=None) -> None:
+    """dtable[v] = base[v] + scale * (sum of the rows dout[t] with ids[t] = v),
+    base None: zeros; base may be dtable itself (rows of absent tokens are
+    then left as they are).  dout [T, D], dtable and base [V, D]; ws:
+    lm_embedding_workspace(T, V, D) or larger."""
+    T = ids.numel()
+    ldg = _mat(dtable, "dtable")
+    V, D = dtable.shape
+    ldd = _mat(dout, "dout", T, D)
+    p, it = _tokens(ids, "ids", (T,))
+    ldb, pb = 0, None
+    if base is not None:
+        ldb, pb = _mat(base, "base", V, D), base.data_ptr()
+        if base.dtype != dtable.dtype:
+            raise TypeError("base and dtable must have one dtype")
+    need = lib.lm_embedding_workspace_bytes(T, V, D)
+    if not ws.is_cuda or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
+        raise ValueError(f"ws must be a dense CUDA tensor of at least {need} bytes")
+    _check(_C.lm_embedding_grad(dout.data_ptr(), ldd, dtype_code(dout), p, it, T, scale, pb, ldb,
+                                dtable.data_ptr(), ldg, dtype_code(dtable), V, D, ws.data_ptr(),
+                                _stream_handle(stream)))
+
+
+def lm_logprobs(logits, targets, logprob, lse=None, entropy=None, top_ids=None,
+                top_logprobs=None, scale: float = 1.0, stream=None) -> None:
+    """Log probabilities of `targets` [T] under softmax(scale * logits), into
+    logprob [T]; lse [T], entropy [T], and the K largest logits' ids (of
+    targets' dtype) and log probabilities, top_ids and top_logprobs [T, K],
+    where given.  logits [T, V], bf16 or fp32 with any row stride."""
+    ld = _mat(logits, "logits")
+    T, V = logits.shape
+    p, it = _tokens(targets, "targets", (T,))
+    K, pt = 0, None
+    if top_ids is not None:
+        if top_ids.dim() != 2 or top_logprobs is None:
+            raise ValueError("top_ids must be [T, K] and come with top_logprobs")
+        K = top_ids.shape[1]
+        pt = _dense(top_ids, "top_ids", (T, K), targets.dtype)
+    elif top_logprobs is not None:
+        raise ValueError("top_logprobs comes with top_ids")
+    _check(_C.lm_logprobs(logits.data_ptr(), ld, T, V, dtype_code(logits), scale, p, it,
+                          _dense(logprob, "logprob", (T,)), _dense(lse, "lse", (T,)),
+                          _dense(entropy, "entropy", (T,)), K, pt,
+                          _dense(top_logprobs, "top_logprobs", (T, K)), _stream_handle(stream)))
+
+
+def lm_logprobs_grad(logits, targets, lse, dlogprob, dlogits, entropy=None, dentropy=None,
+                     scale: float = 1.0, stream=None) -> None:
+    """The gradient of lm_logprobs' logprob (weighted by dlogprob [T]) and
+    entropy (by dentropy [T], with the entropy it gave) with respect to the
+    logits, into dlogits, which may be logits itself."""
+    ld = _mat(logits, "logits")
+    T, V = logits.shape
+    ldd = _mat(dlogits, "dlogits", T, V)
+    if dlogits.dtype != logits.dtype:
+        raise TypeError("logits and dlogits must have one dtype")
+    p, it = _tokens(targets, "targets", (T,))
+    _check(_C.lm_logprobs_grad(logits.data_ptr(), ld, T, V, dtype_code(logits), scale, p, it,
+                               _dense(lse, "lse", (T,)), _dense(entropy, "entropy", (T,)),
+                               _dense(dlogprob, "dlogprob", (T,)),
+                               _dense(dentropy, "dentropy", (T,)), dlogits.data_ptr(), ldd,
+                               _stream_handle(stream)))
+
+
+def _distill_args(logits, teacher_ids, teacher_logits, temperature) -> tuple:
+    ld = _mat(logits, "logits")
+    T, V = logits.shape
+    if teacher_ids.dim() != 2:
+        raise ValueError(f"teacher_ids must be [T, K], not {list(teacher_ids.shape)}")
+    K = teacher_ids.shape[1]
+    p, it = _tokens(teacher_ids, "teacher_ids", (T, K))
+    return (logits.data_ptr(), ld, T, V, dtype_code(logits), p, it,
+            _dense(teacher_logits, "teacher_logits", (T, K), teacher_logits.dtype),
+            dtype_code(teacher_logits), K, temperature)
+
+
+def _dlogits_args(logits, dlogits) -> tuple:
+    ldd = _mat(dlogits, "dlogits", *logits.shape)
+    if dlogits.dtype != logits.dtype:
+        raise TypeError("logits and dlogits must have one dtype")
+    return dlogits.data_ptr(), ldd
+
+
+def lm_distill(logits, teacher_ids, teacher_logits, loss, lse=None, temperature: float = 1.0,
+               stream=None) -> None:
+    """Per-row distillation loss from a teacher's top logits: teacher_ids
+    [T, K] (int32 or int64) and teacher_logits [T, K] (bf16 or fp32), softmax
+    over the K entries at the given temperature, against softmax(logits /
+    temperature) over the whole vocabulary.  loss and lse: [T]."""
+    T = logits.shape[0]
+    _check(_C.lm_distill(*_distill_args(logits, teacher_ids, teacher_logits, temperature),
+                         _dense(loss, "loss", (T,)), _dense(lse, "lse", (T,)),
+                         _stream_handle(stream)))
+
+
+def lm_distill_grad(logits, teacher_ids, teacher_logits, lse, dloss, dlogits,
+                    temperature: float = 1.0, stream=None) -> None:
+    """The gradient of sum(dloss * loss) of lm_distill with respect to the
+    logits, from its lse, into dlogits, which may be logits itself."""
+    T = logits.shape[0]
+    _check(_C.lm_distill_grad(*_distill_args(logits, teacher_ids, teacher_logits, temperature),
+                              _dense(lse, "lse", (T,)), _dense(dloss, "dloss", (T,)),
+                              *_dlogits_args(logits, dlogits), _stream_handle(stream)))
+
+
+def lm_distill_step(logits, teacher_ids, teacher_logits, dloss, loss, dlogits, lse=None,
+                    temperature: float = 1.0, stream=None) -> None:
+    """lm_distill and lm_distill_grad in one pass over the logits, for weights
+    dloss [T] known beforehand; dlogits may be logits itself."""
+    T = logits.shape[0]
+    _check(_C.lm_distill_step(*_distill_args(logits, teacher_ids, teacher_logits, temperature),
+                              _dense(dloss, "dloss", (T,)), _dense(loss, "loss", (T,)),
+                              _dense(lse, "lse", (T,)), *_dlogits_args(logits, dlogits),
+                              _stream_handle(stream)))
 
 
 class PreparedCall:

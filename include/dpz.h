@@ -316,6 +316,132 @@ DPZ_API int dp_zero2_update(const void* shards, float* master, float* m, float* 
 DPZ_API int dp_grad_global_norm_static(const void* grads, int64_t P, int N,
                                        int gdtype, float* norm_out, void* stream);
 
+/* ---------------------------------------------------------------------
+ * The two ends of a language model's training step
+ *
+ * The arena calls above take over once every gradient slab is filled.  These
+ * calls sit at the other end of a replica's forward and backward pass, where
+ * it meets the vocabulary: the embedding lookup that reads a table in a
+ * weight slab, the loss that reads the logits, the gradient of the logits,
+ * and the table's gradient in a gradient slab.  They have no counterpart on
+ * the pages (which start from filled gradients), run on one replica's
+ * buffers, and keep the library's rules: asynchronous on `stream`, nothing
+ * allocated, and the same bits from every run, because no sum's order depends
+ * on the launch or on the order of atomics.
+ *
+ *   T   tokens (rows), 0 <= T < 2^31;   V  vocabulary, 1 <= V < 2^30
+ *   D   width of an embedding row, 1 <= D < 2^24
+ *   Matrices are row-major with a row stride in elements (ld_*, at least the
+ *   row's length), so that a table inside an arena or logits with padded rows
+ *   need no copy.  Any stride and any element-aligned address is accepted;
+ *   the fastest accesses need the alignment each call states.
+ *   Ids are DPZ_I32 or DPZ_I64; an id outside [0, V) names no token.
+ *   Element types are DPZ_F32 or DPZ_BF16; arithmetic is fp32, with one
+ *   rounding to the output's type at the end.
+ *   A call with T = 0 writes no row (lm_embedding_grad still writes dtable).
+ *   Errors are as above: DPZ_ERR_INVALID_ARG for a NULL pointer, a size out
+ *   of range, a stride below the row length, an unknown type, a scale or
+ *   temperature that is not finite (or not positive where it scales logits)
+ *   or buffers that overlap except where a call allows it; DPZ_ERR_ALIGN for
+ *   an address that is not a multiple of its element.
+ * ------------------------------------------------------------------- */
+
+/* id types */
+#define DPZ_I32 16
+#define DPZ_I64 17
+
+#define DPZ_LM_MAX_TOP 32       /* most alternatives of lm_logprobs */
+#define DPZ_LM_MAX_TEACHER 256  /* most teacher logits per row of lm_distill* */
+
+/* Embedding lookup: out[t, :] = R(scale * table[ids[t], :]), a row of zeros
+ * where ids[t] names no token.  table [V][D] (wdtype), out [T][D] (odtype).
+ * Fastest with 32-byte aligned fp32 (16-byte bf16) rows and D % 8 == 0. */
+DPZ_API int lm_embedding(const void* table, int64_t ld_table, int64_t V, int64_t D, int wdtype,
+                         const void* ids, int itype, int64_t T, float scale, void* out,
+                         int64_t ld_out, int odtype, void* stream);
+
+/* Bytes of device workspace of lm_embedding_grad; 0 for invalid sizes. */
+DPZ_API size_t lm_embedding_workspace_bytes(int64_t T, int64_t V, int64_t D);
+
+/* Gradient of lm_embedding with respect to the table, added to `base`:
+ *     dtable[v, :] = R(base[v, :] + scale * sum over t with ids[t] = v of dout[t, :])
+ * dout [T][D] (ddtype); base and dtable [V][D] (gdtype).  base NULL: zeros,
+ * so that every row of dtable is written.  base may be dtable itself (same
+ * address and stride): rows whose token does not occur are then left
+ * untouched, which is how a tied output layer's gradient in the slab gets the
+ * lookup's part.  The tokens are sorted first and each row is summed in fp32
+ * in the order of t (rows of very frequent tokens in pieces of fixed length,
+ * joined in order), so the result does not depend on the launch.  Tokens
+ * whose id names none contribute nothing.  ws: lm_embedding_workspace_bytes
+ * bytes, 16-byte aligned. */
+DPZ_API int lm_embedding_grad(const void* dout, int64_t ld_dout, int ddtype, const void* ids,
+                              int itype, int64_t T, float scale, const void* base,
+                              int64_t ld_base, void* dtable, int64_t ld_dtable, int gdtype,
+                              int64_t V, int64_t D, void* ws, void* stream);
+
+/* Log probabilities of given tokens.  With z = scale * logits[t, :] (scale:
+ * the inverse temperature, > 0) and lse = log sum_j exp(z_j):
+ *     logprob[t] = z[targets[t]] - lse          (0 where the id names no token)
+ *     lse[t], and entropy[t] = lse - sum_j p_j z_j,  p = exp(z - lse)
+ *     top_ids[t, k], top_logprobs[t, k]: the K largest logits in descending
+ *     order, the lowest id first among equal ones (+0 equals -0, NaN counts
+ *     as the largest), and their log probabilities
+ * logits [T][V] (dtype); targets and top_ids of type itype; logprob, lse,
+ * entropy and top_logprobs fp32; top_ids and top_logprobs [T][K], densely.
+ * lse and entropy may be NULL; with K = 0 (at most DPZ_LM_MAX_TOP and V) the
+ * top pointers are not used.  logprob may be NULL with targets NULL.
+ * A logit of -inf is masked: p = 0.  A row of -inf alone gives lse -inf,
+ * log probabilities -inf and entropy 0; a row that holds NaN or +inf gives
+ * NaN for all of them. */
+DPZ_API int lm_logprobs(const void* logits, int64_t ld, int64_t T, int64_t V, int dtype,
+                        float scale, const void* targets, int itype, float* logprob, float* lse,
+                        float* entropy, int K, void* top_ids, float* top_logprobs, void* stream);
+
+/* Gradient of lm_logprobs with respect to the logits, from the lse and the
+ * entropy that it gave and the gradients of its outputs:
+ *     dlogits[t, j] = R(scale * (dlogprob[t] * (1[j = targets[t]] - p_j)
+ *                                - dentropy[t] * p_j * (log p_j + entropy[t])))
+ * dentropy may be NULL (zero; entropy is then not read).  Where the id names
+ * no token, dlogprob counts as 0.  A row whose two gradients are 0, or whose
+ * lse is -inf, is zeros (its logits are not read).  dlogits [T][V] (dtype)
+ * may be logits itself (same address and stride). */
+DPZ_API int lm_logprobs_grad(const void* logits, int64_t ld, int64_t T, int64_t V, int dtype,
+                             float scale, const void* targets, int itype, const float* lse,
+                             const float* entropy, const float* dlogprob, const float* dentropy,
+                             void* dlogits, int64_t ld_dlogits, void* stream);
+
+/* Distillation from a teacher's top logits.  Row t has K teacher entries:
+ * token teacher_ids[t, k] with logit teacher_logits[t, k] ([T][K], densely,
+ * tdtype).  With tau = temperature, z = logits / tau, p = softmax(z) over the
+ * vocabulary and q = softmax(teacher_logits / tau) over the row's entries:
+ *     loss[t] = sum_k q_k * (log q_k - log p[teacher_ids[t, k]])
+ * An entry whose id names no token, or whose logit is -inf, is absent; a row
+ * without entries has loss 0.  Entries that name one token twice each count.
+ * lse[t] = log sum_j exp(z_j) (may be NULL).  q_k > 0 on a token of p = 0
+ * gives loss +inf; rows with NaN or +inf among the logits give NaN. */
+DPZ_API int lm_distill(const void* logits, int64_t ld, int64_t T, int64_t V, int dtype,
+                       const void* teacher_ids, int itype, const void* teacher_logits,
+                       int tdtype, int K, float temperature, float* loss, float* lse,
+                       void* stream);
+
+/* Gradient of sum_t dloss[t] * loss[t] with respect to the logits, from lse:
+ *     dlogits[t, j] = R(dloss[t] / tau * (p_j - sum over k with id j of q_k))
+ * Rows with dloss 0, without entries or with lse -inf are zeros.  dlogits
+ * [T][V] (dtype) may be logits itself (same address and stride). */
+DPZ_API int lm_distill_grad(const void* logits, int64_t ld, int64_t T, int64_t V, int dtype,
+                            const void* teacher_ids, int itype, const void* teacher_logits,
+                            int tdtype, int K, float temperature, const float* lse,
+                            const float* dloss, void* dlogits, int64_t ld_dlogits, void* stream);
+
+/* lm_distill and lm_distill_grad in one pass, for a training step that knows
+ * its rows' weights dloss beforehand (1 / tokens, or 0 for padding): the
+ * logits are read from memory once.  Here a row with dloss 0 still gets its
+ * loss and lse. */
+DPZ_API int lm_distill_step(const void* logits, int64_t ld, int64_t T, int64_t V, int dtype,
+                            const void* teacher_ids, int itype, const void* teacher_logits,
+                            int tdtype, int K, float temperature, const float* dloss, float* loss,
+                            float* lse, void* dlogits, int64_t ld_dlogits, void* stream);
+
 /* The calling thread's last error message ("" if none). */
 DPZ_API const char* dpz_last_error(void);
 
