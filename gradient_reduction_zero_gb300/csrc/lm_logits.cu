@@ -126,43 +126,116 @@ __device__ __forceinline__ RowSpan row_span(const char* p, int64_t V)
     return s;
 }
 
-// Calls f(x, j) for each element x of index j that belongs to this thread.
+// ------------------------------------------------------------ a row in slices
+//
+// A row is taken by a thread-block cluster of C blocks (C = 1: a plain
+// block), each with an equal share of the body's vectors; the first block has
+// the head too and the last one the tail.  Thread i of a block has the
+// vectors lo + i, lo + i + kRowThreads, ...
+
+__device__ __forceinline__ unsigned cluster_rank()
+{
+    unsigned r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ unsigned cluster_size()
+{
+    unsigned n;
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+    return n;
+}
+
+__device__ __forceinline__ uint32_t addr_of_rank(const void* p, unsigned rank)
+{
+    uint32_t remote;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;"
+        : "=r"(remote)
+        : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    return remote;
+}
+
+__device__ __forceinline__ void store_rank_f32(float* p, unsigned rank, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr_of_rank(p, rank)), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ void store_rank_u64(uint64_t* p, unsigned rank, uint64_t v)
+{
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr_of_rank(p, rank)), "l"(v) : "memory");
+}
+
+constexpr int kMaxCluster = 8;
+
+struct Slice {
+    int head, lo, hi, tail;   // single elements, vectors [lo, hi), single elements
+    int vec0, tail0;          // index of the body's first element, of the tail's first
+};
+
+template <int DT>
+__device__ __forceinline__ Slice row_slice(const char* p, int64_t V, unsigned rank, unsigned n)
+{
+    const RowSpan r = row_span<DT>(p, V);
+    Slice s;
+    s.head = rank == 0 ? r.head : 0;
+    s.tail = rank == n - 1 ? r.tail : 0;
+    s.lo = (int)((int64_t)r.nvec * rank / n);
+    s.hi = (int)((int64_t)r.nvec * (rank + 1) / n);
+    s.vec0 = r.head;
+    s.tail0 = r.head + r.nvec * El<DT>::kVec;
+    return s;
+}
+
+// Calls f(x, j) for each element x of index j that thread `t` of the block
+// has.  part, parts: only every parts-th of its vectors, from part (and the
+// single elements with part 0), for threads that share the work of one.
 template <int DT, class F>
-__device__ __forceinline__ void for_elements(const char* row, const RowSpan& s, F&& f)
+__device__ __forceinline__ void for_elements(const char* row, const Slice& s, int t, int part,
+                                             int parts, F&& f)
 {
     constexpr int kB = El<DT>::kBytes, kV = El<DT>::kVec;
-    const int t = threadIdx.x;
-    if (t < s.head) f(El<DT>::load(row + t * kB), t);
-    const char* body = row + s.head * kB;
-    for (int i = t; i < s.nvec; i += kRowThreads) {
+    const char* body = row + s.vec0 * kB;
+    for (int64_t i = s.lo + t + (int64_t)part * kRowThreads; i < s.hi;
+         i += (int64_t)parts * kRowThreads) {
         float x[kV];
-        El<DT>::unpack(ld16(body + (int64_t)i * 16), x);
+        El<DT>::unpack(ld16(body + i * 16), x);
 #pragma unroll
-        for (int j = 0; j < kV; ++j) f(x[j], s.head + i * kV + j);
+        for (int j = 0; j < kV; ++j) f(x[j], s.vec0 + (int)i * kV + j);
     }
-    if (t < s.tail) {
-        const int j = s.head + s.nvec * kV + t;
-        f(El<DT>::load(row + (int64_t)j * kB), j);
-    }
+    if (part != 0) return;
+    if (t < s.head) f(El<DT>::load(row + t * kB), t);
+    if (t < s.tail) f(El<DT>::load(row + (int64_t)(s.tail0 + t) * kB), s.tail0 + t);
 }
 
 // ------------------------------------------------------------ softmax statistics
 //
 // Running maximum m, S = sum 2^u and U = sum u 2^u over a part of a row, with
-// u = (x - m) c and c = scale * log2(e).  The difference is taken before the
-// product, so a maximum of the type's lowest value does not overflow.  A
-// masked element (-inf) has 2^u = 0; its u is held at a finite value so that
-// 0 * u is 0.
+// u = (x - m) c and c = scale * log2(e): one pass over the logits, whatever
+// comes after the maximum being rescaled when a larger one turns up.  u is
+// computed as x c - (m c) in one fused operation; m c is rounded once and the
+// same value is used wherever m is, so its rounding cancels.  Where m is below
+// -1e37 (the type's lowest value throughout, or nothing but -inf so far) m c
+// could overflow, and u is (x - m) c instead.  A masked element (-inf) has
+// 2^u = 0; its u is held at a finite value so that 0 * u is 0.
 struct Stat {
     float m, S, U;
 };
 
 constexpr float kMinExp = -16384.0f;
+constexpr float kLowMax = -1e37f;
+
+// (a - m) c for the maxima a <= m of two parts.
+__device__ __forceinline__ float max_step(float a, float m, float c)
+{
+    const float d = m < kLowMax ? (a - m) * c : a * c - m * c;
+    return fmaxf(d, kMinExp);
+}
 
 __device__ __forceinline__ void stat_rebase(Stat& s, float m, float c)
 {
-    // 2^((x - m) c) = 2^((x - s.m) c) * 2^d with d = (s.m - m) c
-    const float d = fmaxf((s.m - m) * c, kMinExp);
+    // u against the new maximum is u + d, so 2^u gets the factor 2^d
+    const float d = max_step(s.m, m, c);
     const float f = ex2(d);
     s.U = f * __fmaf_rn(d, s.S, s.U);
     s.S *= f;
@@ -178,6 +251,62 @@ __device__ __forceinline__ Stat stat_join(Stat a, Stat b, float c)
     return {m, a.S + b.S, a.U + b.U};
 }
 
+// Adds n elements with maximum vm.
+template <int N>
+__device__ __forceinline__ void stat_add(Stat& s, const float (&x)[N], float vm, float c)
+{
+    if (!(vm <= s.m)) stat_rebase(s, max_nan(s.m, vm), c);
+    if (s.m < kLowMax) {
+        for (int j = 0; j < N; ++j) {
+            const float u = x[j] == -INFINITY ? kMinExp : fmaxf((x[j] - s.m) * c, kMinExp);
+            const float e = ex2(u);
+            s.S += e;
+            s.U = __fmaf_rn(e, u, s.U);
+        }
+        return;
+    }
+    const float b = -(s.m * c);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const float u = fmaxf(__fmaf_rn(x[j], c, b), kMinExp);
+        const float e = ex2(u);
+        s.S += e;
+        s.U = __fmaf_rn(e, u, s.U);
+    }
+}
+
+// The statistics of this thread's elements of a slice.
+template <int DT>
+__device__ __forceinline__ Stat thread_stat(const char* row, const Slice& s, float c)
+{
+    constexpr int kB = El<DT>::kBytes, kV = El<DT>::kVec, kLoads = 4;
+    const int t = threadIdx.x;
+    Stat st{-INFINITY, 0.0f, 0.0f};
+    const char* body = row + s.vec0 * kB;
+    for (int64_t i = s.lo + t; i < s.hi; i += kLoads * kRowThreads) {
+        uint4 w[kLoads];
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k)
+            if (i + k * kRowThreads < s.hi) w[k] = ld16(body + (i + k * kRowThreads) * 16);
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k)
+            if (i + k * kRowThreads < s.hi) {
+                float x[kV];
+                El<DT>::unpack(w[k], x);
+                stat_add(st, x, El<DT>::vec_max(w[k]), c);
+            }
+    }
+    if (t < s.head) {
+        const float x[1] = {El<DT>::load(row + t * kB)};
+        stat_add(st, x, x[0], c);
+    }
+    if (t < s.tail) {
+        const float x[1] = {El<DT>::load(row + (int64_t)(s.tail0 + t) * kB)};
+        stat_add(st, x, x[0], c);
+    }
+    return st;
+}
+
 __device__ __forceinline__ Stat warp_stat(Stat s, float c)
 {
 #pragma unroll
@@ -189,26 +318,44 @@ __device__ __forceinline__ Stat warp_stat(Stat s, float c)
     return s;
 }
 
-// The statistics of a whole row, in every thread.
-template <int DT>
-__device__ __forceinline__ Stat row_stat(const char* row, const RowSpan& span, float c)
+struct StatShared {
+    Stat warp[kRowWarps];
+    Stat block[kMaxCluster];   // by cluster rank
+};
+
+// The statistics of the whole row, in every thread, from each thread's own.
+// In a cluster every block must have announced itself with
+// cluster_arrive_relaxed before.  Contains barriers.
+__device__ __forceinline__ Stat row_stat(Stat s, float c, StatShared& sh, unsigned rank, unsigned n)
 {
-    __shared__ Stat warp_part[kRowWarps];
-    Stat s{-INFINITY, 0.0f, 0.0f};
-    for_elements<DT>(row, span, [&](float x, int) {
-        const float m = max_nan(s.m, x);
-        if (m != s.m) stat_rebase(s, m, c);
-        const float u = x == -INFINITY ? kMinExp : fmaxf((x - m) * c, kMinExp);
-        const float e = ex2(u);
-        s.S += e;
-        s.U = __fmaf_rn(e, u, s.U);
-    });
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     s = warp_stat(s, c);
-    if ((threadIdx.x & 31) == 0) warp_part[threadIdx.x >> 5] = s;
+    if (lane == 0) sh.warp[wid] = s;
     __syncthreads();
-    const int lane = threadIdx.x & 31;
-    s = lane < kRowWarps ? warp_part[lane] : Stat{-INFINITY, 0.0f, 0.0f};
-    return warp_stat(s, c);
+    if (wid == 0) {
+        s = warp_stat(lane < kRowWarps ? sh.warp[lane] : Stat{-INFINITY, 0.0f, 0.0f}, c);
+        if (n == 1) {
+            if (lane == 0) sh.block[0] = s;
+        } else {
+            cluster_wait();
+            if (lane < (int)n) {
+                store_rank_f32(&sh.block[rank].m, lane, s.m);
+                store_rank_f32(&sh.block[rank].S, lane, s.S);
+                store_rank_f32(&sh.block[rank].U, lane, s.U);
+            }
+        }
+    } else if (n > 1) {
+        cluster_wait();
+    }
+    if (n == 1) {
+        __syncthreads();
+        return sh.block[0];
+    }
+    cluster_arrive_release();
+    cluster_wait();
+    s = sh.block[0];
+    for (unsigned r = 1; r < n; ++r) s = stat_join(s, sh.block[r], c);
+    return s;
 }
 
 // lse and entropy of a row's statistics; m NaN or +inf: NaN, m -inf: -inf and 0.
@@ -217,13 +364,16 @@ struct RowResult {
     bool empty, bad;
 };
 
-__device__ __forceinline__ RowResult row_result(const Stat& s, float scale)
+__device__ __forceinline__ RowResult row_result(const Stat& s, float scale, float c)
 {
     RowResult r;
     r.empty = s.m == -INFINITY;
     r.bad = !(s.m < INFINITY);
     r.log2S = log2f(s.S);
-    r.lse = r.bad ? quiet_nan() : r.empty ? -INFINITY : __fmaf_rn(s.m, scale, r.log2S * kLn2);
+    r.lse = r.bad ? quiet_nan()
+            : r.empty ? -INFINITY
+            : s.m < kLowMax ? __fmaf_rn(s.m, scale, r.log2S * kLn2)
+                            : (s.m * c + r.log2S) * kLn2;
     r.entropy = r.bad ? quiet_nan() : r.empty ? 0.0f : (r.log2S - s.U / s.S) * kLn2;
     return r;
 }
@@ -241,12 +391,23 @@ __device__ __forceinline__ float logprob_of(float x, const Stat& s, const RowRes
 // the complement of its index in the lower, so that the largest key is the
 // largest value of the lowest index.  0 is below every key.
 
-__device__ __forceinline__ uint64_t rank_key(float x, int j)
+__device__ __forceinline__ uint32_t value_order(float x)
 {
     const uint32_t b = __float_as_uint(x + 0.0f);   // -0 becomes +0
-    uint32_t o = b & 0x80000000u ? ~b : b | 0x80000000u;
-    if (x != x) o = 0xffffff00u;
-    return (uint64_t)o << 32 | (0xffffffffu - (uint32_t)j);
+    return x != x ? 0xffffff00u : b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+constexpr uint32_t kOrderMasked = 0x007fffffu;      // value_order(-inf)
+
+__device__ __forceinline__ float value_of_order(uint32_t o)
+{
+    return o == 0xffffff00u ? quiet_nan()
+                            : __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
+
+__device__ __forceinline__ uint64_t rank_key(uint32_t order, int j)
+{
+    return (uint64_t)order << 32 | (0xffffffffu - (uint32_t)j);
 }
 
 __device__ __forceinline__ uint64_t warp_max64(uint64_t k)
@@ -259,55 +420,176 @@ __device__ __forceinline__ uint64_t warp_max64(uint64_t k)
     return k;
 }
 
-// ------------------------------------------------------------ log probabilities
+constexpr int kTopCap = 512;                        // candidates a block can hold
+constexpr int kTopGroup = kRowThreads / 32;         // threads per group, 32 groups
 
+struct TopShared {
+    uint64_t cand[kTopCap];
+    uint64_t merged[kMaxCluster * DPZ_LM_MAX_TOP];  // a cluster's first block: every block's best
+    uint64_t best[kRowWarps];
+    uint32_t group[32];
+    uint32_t threshold;
+    int n;
+};
+
+// The block's K largest keys of its slice into out[0..K) of shared memory (0
+// where it has fewer elements), for K <= 32.  thread_max: the order of the
+// thread's largest element (0 without one).
+//
+// The K-th largest of 32 groups' maxima is a threshold that at least K
+// elements reach, and few more do: a random row of any length has
+// 32 (H(32) - H(32 - K)) of them, 9 for K = 8, 31 for K = 20 and 130 for
+// K = 32 (H: harmonic numbers).  Only threads whose own maximum reaches it
+// look at their elements again, 32 lanes sharing each one's vectors, and the
+// candidates are ranked against each other.  If more than kTopCap elements
+// reach it (rows of few distinct values), K rounds of a block-wide maximum
+// are run instead.  If only masked elements are left below the threshold
+// (fewer than K groups have any other), the unmasked ones are candidates and
+// the masked ones of lowest index, which are ties, fill up.
 template <int DT>
-__global__ void __launch_bounds__(kRowThreads) k_logprobs(LogprobArgs a)
+__device__ __forceinline__ void block_top(const char* row, const Slice& s, uint32_t thread_max,
+                                          int K, TopShared& sh, uint64_t* out)
 {
-    __shared__ uint64_t warp_best[kRowWarps];
-    pdl_enter();
-    const int64_t t = blockIdx.x;
-    const char* row = a.x.p + t * a.x.ld * El<DT>::kBytes;
-    const RowSpan span = row_span<DT>(row, a.V);
-    const float c = a.scale * kLog2e;
-    const Stat s = row_stat<DT>(row, span, c);
-    const RowResult r = row_result(s, a.scale);
-    if (threadIdx.x == 0) {
-        if (a.logprob != nullptr) {
-            const int y = load_token(a.targets, t, a.V);
-            a.logprob[t] =
-                y < 0 ? 0.0f : logprob_of(El<DT>::load(row + (int64_t)y * El<DT>::kBytes), s, r, a.scale);
+    constexpr int kB = El<DT>::kBytes;
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    uint32_t g = thread_max;
+#pragma unroll
+    for (int o = 1; o < kTopGroup; o <<= 1) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
+    if (threadIdx.x % kTopGroup == 0) sh.group[threadIdx.x / kTopGroup] = g;
+    if (threadIdx.x < K) out[threadIdx.x] = 0;
+    __syncthreads();
+    if (wid == 0) {
+        const uint32_t v = sh.group[lane];
+        int above = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const uint32_t w = __shfl_sync(0xffffffffu, v, i);
+            above += w > v || (w == v && i < lane);
         }
-        if (a.lse != nullptr) a.lse[t] = r.lse;
-        if (a.entropy != nullptr) a.entropy[t] = r.entropy;
+        if (above == K - 1) sh.threshold = v;
+        if (lane == 0) sh.n = 0;
+    }
+    __syncthreads();
+    const uint32_t th = max(sh.threshold, 1u);
+    const bool fill = th <= kOrderMasked;
+    const uint32_t floor_ = fill ? kOrderMasked + 1 : th;
+    unsigned m = __ballot_sync(0xffffffffu, thread_max >= floor_);
+    while (m != 0) {
+        const int owner = (wid << 5) + __ffs(m) - 1;
+        m &= m - 1;
+        for_elements<DT>(row, s, owner, lane, 32, [&](float x, int j) {
+            const uint32_t o = value_order(x);
+            if (o >= floor_) {
+                const int at = atomicAdd(&sh.n, 1);
+                if (at < kTopCap) sh.cand[at] = rank_key(o, j);
+            }
+        });
+    }
+    __syncthreads();
+    int n = sh.n;
+    if (fill && n < K) {
+        // masked elements among the slice's first K + n hold the lowest indices
+        __syncthreads();
+        const int first = s.head > 0 ? 0 : s.vec0 + s.lo * El<DT>::kVec;
+        const int last = s.tail > 0 ? s.tail0 + s.tail : s.vec0 + s.hi * El<DT>::kVec;
+        const int j = first + threadIdx.x;
+        if ((int)threadIdx.x < K + n && j < last &&
+            value_order(El<DT>::load(row + (int64_t)j * kB)) == kOrderMasked)
+            sh.cand[atomicAdd(&sh.n, 1)] = rank_key(kOrderMasked, j);
+        __syncthreads();
+        n = sh.n;
+    }
+    if (n <= kTopCap) {
+        for (int i = threadIdx.x; i < n; i += kRowThreads) {
+            const uint64_t key = sh.cand[i];
+            int above = 0;
+            for (int q = 0; q < n; ++q) above += sh.cand[q] > key;
+            if (above < K) out[above] = key;
+        }
+        return;
     }
     // K rounds: the largest key below the last one.  Each thread keeps its own
     // best and looks for the next one only when its best was taken.
     uint64_t prev = ~uint64_t(0), best = 0;
     bool stale = true;
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    for (int k = 0; k < a.K; ++k) {
+    for (int k = 0; k < K && prev != 0; ++k) {
         if (stale) {
             best = 0;
-            for_elements<DT>(row, span, [&](float x, int j) {
-                const uint64_t key = rank_key(x, j);
+            for_elements<DT>(row, s, threadIdx.x, 0, 1, [&](float x, int j) {
+                const uint64_t key = rank_key(value_order(x), j);
                 if (key < prev && key > best) best = key;
             });
         }
         const uint64_t wb = warp_max64(best);
-        if (lane == 0) warp_best[wid] = wb;
+        if (lane == 0) sh.best[wid] = wb;
         __syncthreads();
-        prev = warp_max64(lane < kRowWarps ? warp_best[lane] : 0);
+        prev = warp_max64(lane < kRowWarps ? sh.best[lane] : 0);
         __syncthreads();
         stale = best == prev;
-        if (threadIdx.x == 0) {
-            const int j = (int)(0xffffffffu - (uint32_t)prev);
-            const float x = El<DT>::load(row + (int64_t)j * El<DT>::kBytes);
-            const int64_t at = t * a.K + k;
-            if (a.targets.it == DPZ_I64) static_cast<int64_t*>(a.top_ids)[at] = j;
-            else static_cast<int*>(a.top_ids)[at] = j;
-            a.top_logprobs[at] = logprob_of(x, s, r, a.scale);
+        if (threadIdx.x == 0) out[k] = prev;
+    }
+}
+
+// ------------------------------------------------------------ log probabilities
+
+template <int DT>
+__global__ void __launch_bounds__(kRowThreads, 3) k_logprobs(LogprobArgs a)
+{
+    __shared__ StatShared ssh;
+    __shared__ TopShared tsh;
+    const unsigned rank = cluster_rank(), n = cluster_size();
+    if (n > 1) cluster_arrive_relaxed();
+    pdl_enter();
+    const int64_t t = blockIdx.x / n;
+    const char* row = a.x.p + t * a.x.ld * El<DT>::kBytes;
+    float target = 0.0f;
+    int y = -1;
+    if (rank == 0 && threadIdx.x == 0 && a.targets.p != nullptr) {
+        y = load_token(a.targets, t, a.V);
+        if (y >= 0) target = El<DT>::load(row + (int64_t)y * El<DT>::kBytes);
+    }
+    const Slice sl = row_slice<DT>(row, a.V, rank, n);
+    const float c = a.scale * kLog2e;
+    const Stat own = thread_stat<DT>(row, sl, c);
+    const Stat s = row_stat(own, c, ssh, rank, n);
+    const RowResult r = row_result(s, a.scale, c);
+    if (rank == 0 && threadIdx.x == 0) {
+        if (a.logprob != nullptr)
+            a.logprob[t] = y < 0 ? 0.0f : logprob_of(target, s, r, a.scale);
+        if (a.lse != nullptr) a.lse[t] = r.lse;
+        if (a.entropy != nullptr) a.entropy[t] = r.entropy;
+    }
+    if (a.K == 0) return;
+    const bool any = (int)threadIdx.x < max(sl.hi - sl.lo, max(sl.head, sl.tail));
+    uint64_t* top = tsh.merged;
+    block_top<DT>(row, sl, any ? value_order(own.m) : 0u, a.K, tsh, top);
+    __syncthreads();
+    if (n > 1) {
+        // every block's best to the first block, which ranks them
+        uint64_t key = 0;
+        if ((int)threadIdx.x < a.K) key = top[threadIdx.x];
+        cluster_arrive_release();
+        cluster_wait();
+        if ((int)threadIdx.x < a.K) store_rank_u64(&tsh.merged[rank * a.K + threadIdx.x], 0, key);
+        cluster_arrive_release();
+        cluster_wait();
+        if (rank != 0) return;
+        if (threadIdx.x < n * a.K) {
+            const uint64_t mine = tsh.merged[threadIdx.x];
+            int above = 0;
+            for (unsigned q = 0; q < n * a.K; ++q) above += tsh.merged[q] > mine;
+            if (mine != 0 && above < a.K) tsh.cand[above] = mine;
         }
+        __syncthreads();
+        top = tsh.cand;
+    }
+    if ((int)threadIdx.x < a.K) {
+        const uint64_t key = top[threadIdx.x];
+        const int j = (int)(0xffffffffu - (uint32_t)key);
+        const int64_t at = t * a.K + threadIdx.x;
+        if (a.targets.it == DPZ_I64) static_cast<int64_t*>(a.top_ids)[at] = j;
+        else static_cast<int*>(a.top_ids)[at] = j;
+        a.top_logprobs[at] = logprob_of(value_of_order((uint32_t)(key >> 32)), s, r, a.scale);
     }
 }
 
@@ -444,6 +726,7 @@ template <int DT, bool LOSS, bool GRAD>
 __global__ void __launch_bounds__(kRowThreads) k_distill(DistillArgs a)
 {
     __shared__ Teacher w;
+    __shared__ StatShared ssh;
     pdl_enter();
     const int64_t t = blockIdx.x;
     const char* row = a.x.p + t * a.x.ld * El<DT>::kBytes;
@@ -458,8 +741,9 @@ __global__ void __launch_bounds__(kRowThreads) k_distill(DistillArgs a)
     if (threadIdx.x < 32) load_teacher<DT>(a, t, row, w);
     float lse;
     if (LOSS) {
-        const Stat s = row_stat<DT>(row, span, c);
-        const RowResult r = row_result(s, a.inv_tau);
+        const Slice sl = row_slice<DT>(row, a.V, 0, 1);
+        const Stat s = row_stat(thread_stat<DT>(row, sl, c), c, ssh, 0, 1);
+        const RowResult r = row_result(s, a.inv_tau, c);
         lse = r.lse;
         if (threadIdx.x < 32) {
             float sum = 0.0f;
@@ -502,13 +786,25 @@ __global__ void __launch_bounds__(kRowThreads) k_distill(DistillArgs a)
     }
 }
 
+// Blocks per row: as many as keep one wave of blocks on the GPU when there are
+// few rows, at most 8, each with at least one vector per thread.
+unsigned row_cluster(int64_t T, int64_t V, int dt)
+{
+    const int64_t nvec = V * (dt == DPZ_F32 ? 4 : 2) / 16;
+    unsigned n = 1;
+    while (n < kMaxCluster && T * n * 2 <= 304 && nvec >= 2 * n * kRowThreads) n *= 2;
+    return n;
+}
+
 }  // namespace
 
 cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t s)
 {
     set_last_kernel_name("lm_logprobs");
     auto fn = a.x.dt == DPZ_BF16 ? k_logprobs<DPZ_BF16> : k_logprobs<DPZ_F32>;
-    return launch_kernel(fn, dim3((unsigned)a.T), dim3(kRowThreads), 0, s, true, 0u, a);
+    const unsigned n = row_cluster(a.T, a.V, a.x.dt);
+    return launch_kernel(fn, dim3((unsigned)a.T * n), dim3(kRowThreads), 0, s, true, n > 1 ? n : 0u,
+                         a);
 }
 
 cudaError_t launch_logprobs_grad(const LogprobGradArgs& a, cudaStream_t s)
