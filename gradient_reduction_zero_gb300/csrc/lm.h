@@ -84,7 +84,8 @@ cudaError_t launch_emb_join(const EmbGrad& g, cudaStream_t s);
 
 struct LogprobArgs {
     Mat x;
-    int64_t T, V;
+    int64_t T;
+    int V;
     float scale;
     Ids targets;       // p NULL: no logprob
     float *logprob, *lse, *entropy;
@@ -96,7 +97,8 @@ cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t s);
 
 struct LogprobGradArgs {
     Mat x, dx;
-    int64_t T, V;
+    int64_t T;
+    int V;
     float scale;
     Ids targets;
     const float *lse, *entropy, *dlogprob, *dentropy;
@@ -105,7 +107,8 @@ cudaError_t launch_logprobs_grad(const LogprobGradArgs& a, cudaStream_t s);
 
 struct DistillArgs {
     Mat x, dx;          // dx.p NULL: no gradient
-    int64_t T, V;
+    int64_t T;
+    int V;
     float inv_tau;
     Ids ids;
     Mat teacher;

@@ -212,7 +212,7 @@ DPZ_API int lm_logprobs(const void* logits, int64_t ld, int64_t T, int64_t V, in
                           vec_block("top_ids", top_ids, T * K * id_bytes(itype), true),
                           vec_block("top_logprobs", top_logprobs, T * K * 4, true)}));
     if (T == 0) return ok();
-    const LogprobArgs a{mat(logits, ld, dtype), T, V, scale, Ids{logprob ? targets : nullptr, itype},
+    const LogprobArgs a{mat(logits, ld, dtype), T, (int)V, scale, Ids{logprob ? targets : nullptr, itype},
                         logprob, lse, entropy, K, top_ids, top_logprobs};
     cudaStream_t s = as_stream(stream);
     DPZ_TRY(launch(s, [&] { return launch_logprobs(a, s); }));
@@ -246,7 +246,7 @@ DPZ_API int lm_logprobs_grad(const void* logits, int64_t ld, int64_t T, int64_t 
                           vec_block("dentropy", dentropy, T * 4, false),
                           mat_block("dlogits", dlogits, ld_dlogits, T, V, dtype, true)}));
     if (T == 0) return ok();
-    const LogprobGradArgs a{mat(logits, ld, dtype), mat(dlogits, ld_dlogits, dtype), T, V, scale,
+    const LogprobGradArgs a{mat(logits, ld, dtype), mat(dlogits, ld_dlogits, dtype), T, (int)V, scale,
                             Ids{targets, itype}, lse, entropy, dlogprob, dentropy};
     cudaStream_t s = as_stream(stream);
     DPZ_TRY(launch(s, [&] { return launch_logprobs_grad(a, s); }));
@@ -286,7 +286,7 @@ static int distill_common(const void* logits, int64_t ld, int64_t T, int64_t V, 
          vec_block("loss", loss, T * 4, true), vec_block("lse", lse, T * 4, true),
          mat_block("dlogits", dlogits, ld_dlogits, T, V, dtype, true)}));
     if (T == 0) return ok();
-    const DistillArgs a{mat(logits, ld, dtype), mat(dlogits, ld_dlogits, dtype), T, V, inv_tau,
+    const DistillArgs a{mat(logits, ld, dtype), mat(dlogits, ld_dlogits, dtype), T, (int)V, inv_tau,
                         Ids{teacher_ids, itype}, mat(teacher_logits, K, tdtype), K, dloss, loss,
                         lse, lse_in};
     cudaStream_t s = as_stream(stream);
