@@ -1,5 +1,5 @@
 // Internal interface between the entry points of lm_api.cpp and the kernels
-// of lm_embed.cu and lm_logits.cu.
+// of lm_embed.cu, lm_logprobs.cu and lm_distill.cu.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -1,0 +1,539 @@
+// Distillation from a teacher's top logits: loss, gradient, and both in one
+// pass over the student's logits.
+#include "lm_rows.cuh"
+
+namespace dpz {
+
+namespace {
+
+// The teacher's entries of one row in shared memory: tokens (-1: absent), the
+// student's logits there, probabilities and their logarithms.
+struct Teacher {
+    int id[DPZ_LM_MAX_TEACHER];
+    float x[DPZ_LM_MAX_TEACHER], q[DPZ_LM_MAX_TEACHER], logq[DPZ_LM_MAX_TEACHER];
+    int any, repeats;   // whether there is an entry; whether two name one token
+};
+
+// Hashed sets of tokens, zero between uses, to find repeats without comparing
+// every pair of entries.
+struct TokenHash {
+    uint32_t seen[256], twice[256];
+    static __device__ __forceinline__ uint32_t of(int id) { return (uint32_t)id * 2654435761u >> 19; }
+};
+
+__device__ __forceinline__ float warp_max_nan(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+__device__ __forceinline__ float warp_sum_all(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Whether two of the entries name one token, by one warp: entries whose hash
+// another entry has too are compared with all of them.
+__device__ __forceinline__ bool find_repeats(const int* id, int K, TokenHash& h)
+{
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+    for (int k = lane; k < K; k += 32)
+        if (id[k] >= 0) {
+            const uint32_t b = TokenHash::of(id[k]), bit = 1u << (b & 31);
+            if (atomicOr(&h.seen[b >> 5], bit) & bit) atomicOr(&h.twice[b >> 5], bit);
+        }
+    __syncwarp();
+    bool found = false;
+    for (int k0 = 0; k0 < K; k0 += 32) {
+        const int v = k0 + lane < K ? id[k0 + lane] : -1;
+        const uint32_t b = TokenHash::of(v);
+        unsigned m = __ballot_sync(0xffffffffu, v >= 0 && (h.twice[b >> 5] >> (b & 31) & 1));
+        while (m != 0) {
+            const int u = __shfl_sync(0xffffffffu, v, __ffs(m) - 1);
+            m &= m - 1;
+            int same = 0;
+            for (int i = lane; i < K; i += 32) same += id[i] == u;
+            found |= __reduce_add_sync(0xffffffffu, same) > 1;
+        }
+    }
+    __syncwarp();
+    for (int k = lane; k < K; k += 32)
+        if (id[k] >= 0) h.seen[TokenHash::of(id[k]) >> 5] = h.twice[TokenHash::of(id[k]) >> 5] = 0;
+    __syncwarp();
+    return found;
+}
+
+__device__ __forceinline__ void clear_hash(TokenHash& h)
+{
+    for (int i = threadIdx.x & 31; i < 256; i += 32) h.seen[i] = h.twice[i] = 0;
+}
+
+// One warp loads a row's entries and their softmax; the student's logits of
+// those in [lo, hi).
+template <int DT>
+__device__ __forceinline__ void load_teacher(const DistillArgs& a, int64_t t, const char* row,
+                                             int lo, int hi, Teacher& w)
+{
+    const int lane = threadIdx.x & 31;
+    float m = -INFINITY;
+    for (int k = lane; k < a.K; k += 32) {
+        const int64_t at = t * a.K + k;
+        int id = load_token(a.ids, at, a.V);
+        float v = a.teacher.dt == DPZ_F32 ? El<DPZ_F32>::load(a.teacher.p + at * 4)
+                                          : El<DPZ_BF16>::load(a.teacher.p + at * 2);
+        if (v == -INFINITY) id = -1;
+        if (id < 0) v = -INFINITY;
+        w.id[k] = id;
+        w.x[k] = id < lo || id >= hi ? 0.0f : El<DT>::load(row + (int64_t)id * El<DT>::kBytes);
+        w.logq[k] = v;
+        m = max_nan(m, v);
+    }
+    m = warp_max_nan(m);
+    float S = 0.0f;
+    for (int k = lane; k < a.K; k += 32) {
+        // the difference before the product: the type's lowest value stays finite
+        const float v = w.id[k] < 0 ? -INFINITY : (w.logq[k] - m) * a.inv_tau;
+        w.logq[k] = v;
+        S += w.id[k] < 0 ? 0.0f : expf(v);
+    }
+    S = warp_sum_all(S);
+    const float logS = logf(S);
+    for (int k = lane; k < a.K; k += 32) {
+        const float v = w.logq[k] - logS;
+        w.logq[k] = v;
+        w.q[k] = w.id[k] < 0 ? 0.0f : expf(v);
+    }
+    if (lane == 0) w.any = m != -INFINITY;
+    __syncwarp();
+}
+
+// By one warp: sum_k q_k (log q_k - log p_k), in a fixed order; lane 0 writes.
+__device__ __forceinline__ void write_loss(const DistillArgs& a, int64_t t, const Teacher& w,
+                                           const Stat& s, const RowResult& r, const StatScale& k)
+{
+    const int lane = threadIdx.x & 31;
+    float sum = 0.0f;
+    for (int i = lane; i < a.K; i += 32)
+        if (w.q[i] != 0.0f) sum += w.q[i] * (w.logq[i] - logprob_of(w.x[i], s, r, a.inv_tau, k));
+    sum = warp_sum_all(sum);
+    if (lane == 0) {
+        a.loss[t] = w.any ? sum : 0.0f;
+        if (a.lse != nullptr) a.lse[t] = r.lse;
+    }
+}
+
+// The gradient without the teacher's part: (w / tau) p, in pairs.
+struct StudentGrad {
+    F2 it, l, e, ws;
+    __device__ __forceinline__ StudentGrad(float inv_tau, float lse, float weight)
+        : it(pack2(inv_tau, inv_tau)), l(pack2(-lse, -lse)), e(pack2(kLog2e, kLog2e)),
+          ws(pack2(weight, weight))
+    {
+    }
+    __device__ __forceinline__ F2 p(F2 x) const { return ex2x2(mul2(fma2(x, it, l), e)); }
+    __device__ __forceinline__ F2 operator()(F2 x) const { return mul2(ws, p(x)); }
+};
+
+// The same for a bf16 result with w > 0 and an ordinary lse, with everything in
+// one exponent: 2^(x log2(e) / tau + log2(w / tau) - lse log2(e)).  The
+// constant's rounding, 2^-24 of a few tens, is far below the result's.
+struct StudentGradExp {
+    F2 c, b;
+    __device__ __forceinline__ StudentGradExp(float inv_tau, float lse, float weight)
+    {
+        const float cc = inv_tau * kLog2e, bb = __fmaf_rn(-lse, kLog2e, log2f(weight));
+        c = pack2(cc, cc);
+        b = pack2(bb, bb);
+    }
+    static __device__ __forceinline__ bool holds(int DT, float lse, float weight)
+    {
+        return DT == DPZ_BF16 && weight > 0.0f && fabsf(lse) < 1e6f;
+    }
+    __device__ __forceinline__ F2 operator()(F2 x) const { return ex2x2(fma2(x, c, b)); }
+};
+
+// The elements of the teacher's tokens in a slice again, now with their q, by
+// one warp.  An entry that repeats an earlier one's token leaves it to that one.
+template <int DT>
+__device__ __forceinline__ void write_teacher_part(const DistillArgs& a, const Teacher& w,
+                                                   const Slice& s, const StudentGrad& f, char* out)
+{
+    for (int i = threadIdx.x & 31; i < a.K; i += 32) {
+        const int id = w.id[i];
+        if (id < s.first || id >= s.last) continue;
+        float q = w.q[i];
+        bool once = true;
+        if (w.repeats) {
+            q = 0.0f;
+            for (int j = 0; j < a.K; ++j)
+                if (w.id[j] == id) {
+                    if (j < i) once = false;
+                    q += w.q[j];
+                }
+        }
+        if (once)
+            El<DT>::store(out + (int64_t)id * El<DT>::kBytes,
+                          lo2(f.ws) * (lo2(f.p(pack2(w.x[i], 0.0f))) - q));
+    }
+}
+
+// ------------------------------------------------------------ loss alone
+
+template <int DT, int NT>
+__global__ void __launch_bounds__(NT, (DT == DPZ_F32 ? 7 : 6) * kRowThreads / NT)
+    k_distill(DistillArgs a)
+{
+    __shared__ Teacher w;
+    __shared__ StatShared<NT> ssh;
+    const unsigned rank = cluster_rank(), n = cluster_size();
+    if (n > 1) cluster_arrive_relaxed();
+    pdl_enter();
+    const int64_t t = blockIdx.x >> (31 - __clz(n));
+    const char* row = a.x.p + t * a.x.ld * El<DT>::kBytes;
+    const Slice sl = row_slice<DT>(row, a.V, rank, n);
+    const StatScale k(a.inv_tau);
+    if (rank == 0 && threadIdx.x >= NT - 32) load_teacher<DT>(a, t, row, 0, a.V, w);
+    RefStat<DT> rs;
+    thread_rows<DT, NT>(rs, row, sl, sl.lo + threadIdx.x, k);
+    Stat own = rs.get();
+    if (!rs.good(k)) {
+        ThreadStat<DT, NT, false, false> ts;
+        thread_rows<DT, NT>(ts, row, sl, sl.lo + threadIdx.x, k);
+        own = ts.get();
+    }
+    const Stat s = row_stat<NT>(thread_rest<DT>(own, row, sl, k), k, ssh, rank, n, [] {});
+    if (rank == 0 && threadIdx.x < 32) write_loss(a, t, w, s, row_result(s, a.inv_tau, k), k);
+}
+
+// ------------------------------------------------------------ gradient alone
+
+template <int DT, int NT>
+__global__ void __launch_bounds__(NT, 8 * kRowThreads / NT) k_distill_grad(DistillArgs a)
+{
+    __shared__ Teacher w;
+    __shared__ TokenHash hash;
+    pdl_enter();
+    const unsigned rank = blockIdx.y, n = gridDim.y;
+    const int64_t t = blockIdx.x;
+    const char* row = a.x.p + t * a.x.ld * El<DT>::kBytes;
+    char* out = a.dx.p + t * a.dx.ld * El<DT>::kBytes;
+    const float wt = a.dloss[t], lse = a.lse_in[t];
+    if (wt == 0.0f || lse == -INFINITY) {
+        zero_row<DT, NT>(out, a.V, rank, n);
+        return;
+    }
+    const Slice sl = row_slice<DT>(row, a.V, rank, n);
+    // in place, other blocks' slices may be overwritten already
+    if (threadIdx.x >= NT - 32) {
+        clear_hash(hash);
+        load_teacher<DT>(a, t, row, sl.first, sl.last, w);
+        const bool repeats = find_repeats(w.id, a.K, hash);
+        if (threadIdx.x == NT - 32) w.repeats = repeats;
+    }
+    __syncthreads();
+    if (!w.any) {
+        zero_row<DT, NT>(out, a.V, rank, n);
+        return;
+    }
+    const StudentGrad f(a.inv_tau, lse, wt * a.inv_tau);
+    map_row<DT, NT>(row, out, sl, sl.lo + threadIdx.x, f);
+    __syncthreads();
+    if (threadIdx.x >= NT - 32) write_teacher_part<DT>(a, w, sl, f, out);
+}
+
+// ------------------------------------------------------------ both in one pass
+//
+// The row (or the slice of a cluster's block) stays in shared memory between
+// the statistics and the gradient, so the logits are read from memory once.
+// Each thread copies its own vectors asynchronously and is the only one to use
+// them, so nothing but its own copies is waited for.  What does not fit is
+// read again, from L2 as a rule.
+//
+// Blocks are persistent and take every gridDim-th row.  As a vector's gradient
+// is written, the copy of the next row's vector into its place begins, so
+// loads go on while the block computes and writes.  One more warp, the
+// teacher's, works beside the NT threads: it loads the next row's entries
+// while the others are at this one, computes the loss, and writes the teacher's
+// tokens' gradients once the others have written theirs.
+constexpr int kStageGroups = 4;    // copies are waited for in this many parts
+
+__device__ __forceinline__ void copy_async16(void* sdst, const void* gsrc)
+{
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(smem_addr(sdst)), "l"(gsrc)
+                 : "memory");
+}
+
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int LEFT>
+__device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// Barriers of the block: 0 (__syncthreads) once per row, when the threads'
+// statistics and the teacher's entries are there; kRowWritten when the
+// gradient is written but for the teacher's tokens, which only the teacher's
+// warp waits for.
+constexpr int kRowWritten = 1;
+
+template <int N>
+__device__ __forceinline__ void barrier_arrive()
+{
+    __threadfence_block();
+    asm volatile("barrier.cta.arrive %0, %1;" ::"n"(kRowWritten), "n"(N) : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void barrier_wait()
+{
+    asm volatile("barrier.cta.sync %0, %1;" ::"n"(kRowWritten), "n"(N) : "memory");
+}
+
+// A row's statistics from the warps' (and in a cluster the blocks') parts; by
+// whole warps, every thread of the block and cluster taking part.
+template <int NT>
+__device__ __forceinline__ Stat step_stat(const StatScale& k, StatShared<NT>& sh, unsigned rank,
+                                          unsigned n)
+{
+    const int lane = threadIdx.x & 31;
+    Stat s = warp_stat(lane < NT / 32 ? sh.warp[lane] : Stat{-INFINITY, 0.0f, 0.0f}, k);
+    if (n == 1) return s;
+    if (threadIdx.x < n) {
+        store_rank_f32(&sh.block[rank].m, threadIdx.x, s.m);
+        store_rank_f32(&sh.block[rank].S, threadIdx.x, s.S);
+        store_rank_f32(&sh.block[rank].U, threadIdx.x, s.U);
+    }
+    __syncwarp();
+    cluster_arrive_release();
+    cluster_wait();
+    s = sh.block[0];
+    for (unsigned r = 1; r < n; ++r) s = stat_join(s, sh.block[r], k);
+    return s;
+}
+
+template <int DT, int NT>
+__global__ void __launch_bounds__(NT + 32, kStepBlocks<NT>) k_distill_step(DistillArgs a, int stage)
+{
+    extern __shared__ uint4 staged[];           // [stage][NT]
+    __shared__ Teacher w[2];                    // this row's and the next one's
+    __shared__ StatShared<NT> ssh[2];           // a warp may be one row ahead
+    __shared__ TokenHash hash;
+    constexpr int kB = El<DT>::kBytes;
+    const unsigned rank = cluster_rank(), n = cluster_size();
+    if (n > 1) cluster_arrive_relaxed();
+    pdl_enter();
+    if (n > 1) cluster_wait();
+    const int log_n = 31 - __clz(n);
+    const int64_t step = gridDim.x >> log_n;
+    int64_t t = blockIdx.x >> log_n;
+    const StatScale k(a.inv_tau);
+    const auto row_of = [&](int64_t r) { return a.x.p + r * a.x.ld * kB; };
+    int b = 0;
+
+    if (threadIdx.x >= NT) {                    // the teacher's warp
+        clear_hash(hash);
+        const auto load = [&](int64_t r, Teacher& e) {
+            load_teacher<DT>(a, r, row_of(r), 0, a.V, e);
+            const bool repeats = find_repeats(e.id, a.K, hash);
+            if (threadIdx.x == NT) e.repeats = repeats;
+            __syncwarp();
+        };
+        load(t, w[0]);
+        for (; t < a.T; t += step, b ^= 1) {
+            __syncthreads();
+            const Stat s = step_stat<NT>(k, ssh[b], rank, n);
+            const RowResult r = row_result(s, a.inv_tau, k);
+            if (rank == 0) write_loss(a, t, w[b], s, r, k);
+            if (t + step < a.T) load(t + step, w[b ^ 1]);
+            const float wt = a.dloss[t];
+            barrier_wait<NT + 32>();
+            if (wt == 0.0f || !w[b].any || r.lse == -INFINITY) continue;
+            write_teacher_part<DT>(a, w[b], row_slice<DT>(row_of(t), a.V, rank, n),
+                                   StudentGrad(a.inv_tau, r.lse, wt * a.inv_tau),
+                                   a.dx.p + t * a.dx.ld * kB);
+        }
+        return;
+    }
+
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    const int per = (stage + kStageGroups - 1) / kStageGroups;
+    uint4* own = staged + threadIdx.x;
+    // the row at hand: its slice, this thread's first vector, and how many of
+    // its vectors are staged
+    const char* row = row_of(t);
+    Slice sl = row_slice<DT>(row, a.V, rank, n);
+    const auto first_of = [&](const Slice& s) { return s.lo + (int)threadIdx.x; };
+    const auto staged_of = [&](const Slice& s) {
+        return min(stage, max(0, (s.hi - first_of(s) + NT - 1) / NT));
+    };
+    {
+        const int have = staged_of(sl);
+        const char* p = row + sl.vec0 * kB + (int64_t)first_of(sl) * 16;
+        for (int g = 0; g < kStageGroups; ++g) {
+            for (int i = g * per; i < min((g + 1) * per, have); ++i)
+                copy_async16(own + i * NT, p + i * (NT * 16));
+            copy_commit();
+        }
+    }
+    for (; t < a.T; t += step, b ^= 1) {
+        const float wt = a.dloss[t];
+        const int first = first_of(sl), have = staged_of(sl);
+        RefStat<DT> rs;
+        const auto add_group = [&](int g) {
+            int i = g * per;
+            const int end = min((g + 1) * per, have);
+            for (; i + 3 < end; i += 4) {
+                const uint4 v[4] = {own[i * NT], own[(i + 1) * NT], own[(i + 2) * NT],
+                                    own[(i + 3) * NT]};
+                rs.add(v, 0, k, nullptr);
+            }
+#pragma unroll 1
+            for (; i < end; ++i) {
+                const uint4 v[1] = {own[i * NT]};
+                rs.add(v, 0, k, nullptr);
+            }
+        };
+#pragma unroll 1
+        for (int g = 0; g < kStageGroups; ++g) {
+            if (g == 0) copy_wait<3>();
+            else if (g == 1) copy_wait<2>();
+            else if (g == 2) copy_wait<1>();
+            else copy_wait<0>();
+            add_group(g);
+        }
+        thread_rows<DT, NT>(rs, row, sl, first + have * NT, k);
+        Stat mine = rs.get();
+        if (!rs.good(k)) {
+            ThreadStat<DT, NT, false, false> ts;
+#pragma unroll 1
+            for (int i = 0; i < have; ++i) {
+                const uint4 v[1] = {own[i * NT]};
+                ts.add(v, 0, k, nullptr);
+            }
+            thread_rows<DT, NT>(ts, row, sl, first + have * NT, k);
+            mine = ts.get();
+        }
+        mine = warp_stat(thread_rest<DT>(mine, row, sl, k), k);
+        if (lane == 0) ssh[b].warp[wid] = mine;
+        __syncthreads();
+        const Stat s = step_stat<NT>(k, ssh[b], rank, n);
+        const float lse = row_result(s, a.inv_tau, k).lse;
+        char* out = a.dx.p + t * a.dx.ld * kB;
+        const bool same = same_alignment(row, out);
+        const bool zero = wt == 0.0f || !w[b].any || lse == -INFINITY;
+        const StudentGrad f(a.inv_tau, lse, wt * a.inv_tau);
+        char* q = out + sl.vec0 * kB + (int64_t)first * 16;
+        // the next row's copies take the places as they become free
+        const bool more = t + step < a.T;
+        const char* next = more ? row_of(t + step) : row;
+        const Slice ns = row_slice<DT>(next, a.V, rank, n);
+        const int will = more ? staged_of(ns) : 0;
+        const char* np = next + ns.vec0 * kB + (int64_t)first_of(ns) * 16;
+        const int both = same && !zero && StudentGradExp::holds(DT, lse, wt * a.inv_tau)
+                             ? min(have, will) : 0;
+        const StudentGradExp fe(a.inv_tau, lse, wt * a.inv_tau);
+#pragma unroll 1
+        for (int g = 0; g < kStageGroups; ++g) {
+            int i = g * per;
+            const int end = min(i + per, max(have, will));
+#pragma unroll 4
+            for (; i < min(end, both); ++i) {
+                map_vector<DT, NT>(own[i * NT], q + i * (NT * 16), true, fe);
+                copy_async16(own + i * NT, np + i * (NT * 16));
+            }
+#pragma unroll 1
+            for (; i < end; ++i) {
+                if (i < have && !zero)
+                    map_vector<DT, NT>(own[i * NT], q + i * (NT * 16), same, f);
+                if (i < will) copy_async16(own + i * NT, np + i * (NT * 16));
+            }
+            copy_commit();
+        }
+        if (zero) zero_row<DT, NT>(out, a.V, rank, n);
+        else map_row<DT, NT>(row, out, sl, first + have * NT, f);
+        barrier_arrive<NT + 32>();
+        row = next;
+        sl = ns;
+    }
+}
+
+// Blocks of a persistent kernel that fit on the GPU together, by the vectors
+// each thread stages; asked for once.
+template <int DT, int NT>
+cudaError_t resident_blocks(int stage, int* blocks)
+{
+    constexpr int kMost = kStageMax / (NT * 16);
+    static std::atomic<int> known[kMost + 1];
+    int got = known[stage].load(std::memory_order_relaxed);
+    if (got == 0) {
+        int dev = 0, sms = 0, per_sm = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess)
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_distill_step<DT, NT>, NT + 32,
+                                                              (size_t)stage * NT * 16);
+        if (e != cudaSuccess) return e;
+        got = std::max(1, sms * per_sm);
+        known[stage].store(got, std::memory_order_relaxed);
+    }
+    *blocks = got;
+    return cudaSuccess;
+}
+
+template <int DT, int NT>
+cudaError_t launch_step(const DistillArgs& a, cudaStream_t s)
+{
+    static SmemRaised raised;
+    const int64_t bytes = row_bytes(a.V, DT);
+    const unsigned n = row_cluster(a.T, bytes, NT);
+    const int64_t vecs = (bytes / 16 + n - 1) / n + 1;
+    const int stage = (int)std::min<int64_t>((vecs + NT - 1) / NT, kStageMax / (NT * 16));
+    cudaError_t e =
+        allow_smem(raised, reinterpret_cast<const void*>(k_distill_step<DT, NT>), kStageMax);
+    int blocks = 0;
+    if (e == cudaSuccess) e = resident_blocks<DT, NT>(stage, &blocks);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = n > 1 ? (unsigned)a.T * n : (unsigned)std::min<int64_t>(a.T, blocks);
+    return launch_kernel(k_distill_step<DT, NT>, dim3(grid), dim3(NT + 32), (size_t)stage * NT * 16, s,
+                         true, n > 1 ? n : 0u, a, stage);
+}
+
+template <int DT>
+cudaError_t step_typed(const DistillArgs& a, cudaStream_t s)
+{
+    return row_bytes(a.V, DT) <= kShortRow ? launch_step<DT, kShortThreads>(a, s)
+                                           : launch_step<DT, kStepThreads>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_distill(const DistillArgs& a, cudaStream_t s)
+{
+    const bool b = a.x.dt == DPZ_BF16;
+    if (a.loss != nullptr && a.dx.p != nullptr) {
+        set_last_kernel_name("lm_distill_step");
+        return b ? step_typed<DPZ_BF16>(a, s) : step_typed<DPZ_F32>(a, s);
+    }
+    const int64_t bytes = row_bytes(a.V, a.x.dt);
+    const bool small = bytes <= kShortRow;
+    const int nt = small ? kShortThreads : kRowThreads;
+    if (a.loss != nullptr) {
+        set_last_kernel_name("lm_distill");
+        const unsigned n = row_cluster(a.T, bytes, nt);
+        auto fn = small ? (b ? k_distill<DPZ_BF16, kShortThreads> : k_distill<DPZ_F32, kShortThreads>)
+                        : (b ? k_distill<DPZ_BF16, kRowThreads> : k_distill<DPZ_F32, kRowThreads>);
+        return launch_kernel(fn, dim3((unsigned)a.T * n), dim3(nt), 0, s, true, n > 1 ? n : 0u, a);
+    }
+    set_last_kernel_name("lm_distill_grad");
+    const unsigned n = row_cluster(a.T, bytes, nt);
+    auto fn = small ? (b ? k_distill_grad<DPZ_BF16, kShortThreads> : k_distill_grad<DPZ_F32, kShortThreads>)
+                    : (b ? k_distill_grad<DPZ_BF16, kRowThreads> : k_distill_grad<DPZ_F32, kRowThreads>);
+    return launch_kernel(fn, dim3((unsigned)a.T, n), dim3(nt), 0, s, true, 0u, a);
+}
+
+}  // namespace dpz

@@ -1,0 +1,689 @@
+// Rows of logits over a vocabulary, shared by lm_logprobs.cu and
+// lm_distill.cu: how a row's elements are read and split between blocks, the
+// running softmax statistics, and the writing of a row of gradients.  Kernels
+// are compiled for blocks of NT threads.
+#pragma once
+
+#include <algorithm>
+#include <atomic>
+#include <cfloat>
+#include <cmath>
+
+#include "bulk.cuh"
+#include "device.cuh"
+#include "internal.h"
+#include "lm.h"
+
+namespace dpz {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kRowLoads = 4;         // vectors a thread loads at once (then 2, then 1)
+
+__device__ __forceinline__ int load_token(const Ids& ids, int64_t i, int64_t V)
+{
+    const int64_t v = ids.it == DPZ_I64 ? static_cast<const int64_t*>(ids.p)[i]
+                                        : (int64_t) static_cast<const int*>(ids.p)[i];
+    return v >= 0 && v < V ? (int)v : -1;
+}
+
+// 2^u by the hardware's instruction: at most 2 units in the last place off,
+// which is below the rounding of the exponent that it is given here.
+__device__ __forceinline__ float ex2(float u)
+{
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(u));
+    return e;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+
+// fp32 values as integers of the same order: -0 equals +0, NaN is highest, and
+// 0 is below every value's.
+__device__ __forceinline__ uint32_t value_order(float x)
+{
+    const uint32_t b = __float_as_uint(x + 0.0f);   // -0 becomes +0
+    return x != x ? 0xffffff00u : b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// Two floats in one register pair, for the paired fp32 operations (sm_100 and
+// later): each half is rounded as the single operation rounds it, and one
+// instruction is issued instead of two.
+using F2 = uint64_t;
+
+__device__ __forceinline__ F2 pack2(float lo, float hi)
+{
+    F2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+
+__device__ __forceinline__ float lo2(F2 a) { return __uint_as_float((uint32_t)a); }
+__device__ __forceinline__ float hi2(F2 a) { return __uint_as_float((uint32_t)(a >> 32)); }
+
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+__device__ __forceinline__ F2 add2(F2 a, F2 b)
+{
+    F2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ F2 mul2(F2 a, F2 b)
+{
+    F2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ F2 ex2x2(F2 u) { return pack2(ex2(lo2(u)), ex2(hi2(u))); }
+
+__device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fc00000); }
+
+// ------------------------------------------------------------ a row's elements
+//
+// A row may begin at any element (a vocabulary of 50,257 shifts each row), so
+// it is a head of single elements up to the first 16-byte boundary, a body of
+// 16-byte vectors, and a tail.
+
+template <int DT>
+struct El;
+
+template <>
+struct El<DPZ_F32> {
+    static constexpr int kBytes = 4, kVec = 4;
+    static __device__ __forceinline__ float load(const char* p)
+    {
+        return *reinterpret_cast<const float*>(p);
+    }
+    // the same, not to be moved to where its value is used
+    static __device__ __forceinline__ float load_now(const char* p)
+    {
+        float x;
+        asm volatile("ld.global.f32 %0, [%1];" : "=f"(x) : "l"(p));
+        return x;
+    }
+    static __device__ __forceinline__ void store(char* p, float x)
+    {
+        *reinterpret_cast<float*>(p) = x;
+    }
+    static __device__ __forceinline__ void unpack(const uint4& w, float x[kVec])
+    {
+        x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y);
+        x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
+    }
+    static __device__ __forceinline__ void pairs(const uint4& w, F2 (&x)[kVec / 2])
+    {
+        x[0] = (F2)w.y << 32 | w.x;
+        x[1] = (F2)w.w << 32 | w.z;
+    }
+    static __device__ __forceinline__ uint4 pack(const F2 (&x)[kVec / 2])
+    {
+        return make_uint4((uint32_t)x[0], (uint32_t)(x[0] >> 32), (uint32_t)x[1],
+                          (uint32_t)(x[1] >> 32));
+    }
+    // The largest of N vectors, NaN if any is.
+    template <int N>
+    static __device__ __forceinline__ float vec_max(const uint4 (&w)[N])
+    {
+        float m = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            float x[kVec];
+            unpack(w[k], x);
+            m = max_nan(m, max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3])));
+        }
+        return m;
+    }
+    // Pairs of elements, none below `low`.
+    static __device__ __forceinline__ void pairs_above(const uint4& w, float low, F2 (&x)[kVec / 2])
+    {
+        const auto at = [&](uint32_t u) { return fmaxf(__uint_as_float(u), low); };
+        x[0] = pack2(at(w.x), at(w.y));
+        x[1] = pack2(at(w.z), at(w.w));
+    }
+};
+
+template <>
+struct El<DPZ_BF16> {
+    static constexpr int kBytes = 2, kVec = 8;
+    static __device__ __forceinline__ float load(const char* p)
+    {
+        return __uint_as_float((uint32_t)*reinterpret_cast<const unsigned short*>(p) << 16);
+    }
+    static __device__ __forceinline__ float load_now(const char* p)
+    {
+        unsigned short u;
+        asm volatile("ld.global.u16 %0, [%1];" : "=h"(u) : "l"(p));
+        return __uint_as_float((uint32_t)u << 16);
+    }
+    static __device__ __forceinline__ void store(char* p, float x)
+    {
+        *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(x);
+    }
+    static __device__ __forceinline__ void unpack(const uint4& w, float x[kVec])
+    {
+        Group<1>::unpack({w}, x);
+    }
+    static __device__ __forceinline__ void pairs(const uint4& w, F2 (&x)[kVec / 2])
+    {
+        x[0] = pack2(bf16_lo(w.x), bf16_hi(w.x));
+        x[1] = pack2(bf16_lo(w.y), bf16_hi(w.y));
+        x[2] = pack2(bf16_lo(w.z), bf16_hi(w.z));
+        x[3] = pack2(bf16_lo(w.w), bf16_hi(w.w));
+    }
+    static __device__ __forceinline__ uint4 pack(const F2 (&x)[kVec / 2])
+    {
+        return make_uint4(pack_bf16x2(lo2(x[0]), hi2(x[0])), pack_bf16x2(lo2(x[1]), hi2(x[1])),
+                          pack_bf16x2(lo2(x[2]), hi2(x[2])), pack_bf16x2(lo2(x[3]), hi2(x[3])));
+    }
+    static __device__ __forceinline__ __nv_bfloat162 pair(uint32_t u)
+    {
+        return *reinterpret_cast<const __nv_bfloat162*>(&u);
+    }
+    // The largest of N vectors, NaN if any is (paired bf16 comparisons).
+    template <int N>
+    static __device__ __forceinline__ float vec_max(const uint4 (&w)[N])
+    {
+        __nv_bfloat162 m = pair(0xff80ff80u);   // -inf
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            m = __hmax2_nan(m, __hmax2_nan(__hmax2_nan(pair(w[k].x), pair(w[k].y)),
+                                           __hmax2_nan(pair(w[k].z), pair(w[k].w))));
+        return max_nan(__low2float(m), __high2float(m));
+    }
+    // Pairs of elements, none below `low`.
+    static __device__ __forceinline__ void pairs_above(const uint4& w, float low, F2 (&x)[kVec / 2])
+    {
+        const __nv_bfloat162 l = __float2bfloat162_rn(low);
+        const auto at = [&](uint32_t u) {
+            const __nv_bfloat162 m = __hmax2(pair(u), l);
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(&m);
+            return pack2(bf16_lo(v), bf16_hi(v));
+        };
+        x[0] = at(w.x);
+        x[1] = at(w.y);
+        x[2] = at(w.z);
+        x[3] = at(w.w);
+    }
+};
+
+struct RowSpan {
+    int head;      // elements before the first 16-byte boundary
+    int nvec;      // 16-byte vectors
+    int tail;      // elements after the last
+};
+
+template <int DT>
+__device__ __forceinline__ RowSpan row_span(const char* p, int V)
+{
+    constexpr int kB = El<DT>::kBytes, kV = El<DT>::kVec;
+    const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15);
+    RowSpan s;
+    s.head = min(V, ((16 - off) & 15) / kB);
+    s.nvec = (V - s.head) / kV;
+    s.tail = V - s.head - s.nvec * kV;
+    return s;
+}
+
+// ------------------------------------------------------------ a row in slices
+//
+// A row is taken by a thread-block cluster of C blocks (C = 1: a plain
+// block), each with an equal share of the body's vectors; the first block has
+// the head too and the last one the tail.  Thread i of a block has the
+// vectors lo + i, lo + i + NT, ...
+
+__device__ __forceinline__ unsigned cluster_rank()
+{
+    unsigned r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ unsigned cluster_size()
+{
+    unsigned n;
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+    return n;
+}
+
+__device__ __forceinline__ uint32_t addr_of_rank(const void* p, unsigned rank)
+{
+    uint32_t remote;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;"
+        : "=r"(remote)
+        : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    return remote;
+}
+
+__device__ __forceinline__ void store_rank_f32(float* p, unsigned rank, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr_of_rank(p, rank)), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ void store_rank_u64(uint64_t* p, unsigned rank, uint64_t v)
+{
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr_of_rank(p, rank)), "l"(v) : "memory");
+}
+
+constexpr int kMaxCluster = 8;
+
+struct Slice {
+    int head, lo, hi, tail;   // single elements, vectors [lo, hi), single elements
+    int vec0, tail0;          // index of the body's first element, of the tail's first
+    int first, last;          // the slice's elements: [first, last)
+};
+
+template <int DT>
+__device__ __forceinline__ Slice row_slice(const char* p, int V, unsigned rank, unsigned n)
+{
+    const RowSpan r = row_span<DT>(p, V);
+    const int log_n = 31 - __clz(n);   // n is a power of two, at most kMaxCluster
+    Slice s;
+    s.head = rank == 0 ? r.head : 0;
+    s.tail = rank == n - 1 ? r.tail : 0;
+    s.lo = (int)((unsigned)r.nvec * rank >> log_n);          // nvec < 2^28
+    s.hi = (int)((unsigned)r.nvec * (rank + 1) >> log_n);
+    s.vec0 = r.head;
+    s.tail0 = r.head + r.nvec * El<DT>::kVec;
+    s.first = rank == 0 ? 0 : s.vec0 + s.lo * El<DT>::kVec;
+    s.last = rank == n - 1 ? V : s.vec0 + s.hi * El<DT>::kVec;
+    return s;
+}
+
+// ------------------------------------------------------------ softmax statistics
+//
+// Running maximum m, S = sum 2^u and U = sum u 2^u (where ENT) over a part of
+// a row, with u = (x - m) c and c = scale * log2(e): one pass over the logits,
+// whatever came before a larger maximum being rescaled.  u is computed as
+// x c - (m c) in one fused operation; m c is rounded once and the same value
+// is used wherever m is, so its rounding cancels.  Elements below kLowest
+// count as kLowest there, whose 2^u is 0, so that a masked element (-inf) gives
+// 0 * u = 0 to U.  That needs a maximum well above kLowest and an ordinary
+// scale; otherwise (a row of the type's lowest value, or nothing but -inf so
+// far) u is (x - m) c and -inf is left out.
+struct Stat {
+    float m, S, U;
+};
+
+constexpr float kMinExp = -16384.0f;
+constexpr float kLowest = -1e20f;
+
+// c, and the smallest maximum for which the fused form holds.
+struct StatScale {
+    float c, low_max;
+    __device__ __forceinline__ explicit StatScale(float scale)
+        : c(scale * kLog2e), low_max(c > 1e-15f && c < 1e17f ? -1e19f : INFINITY)
+    {
+    }
+};
+
+// (a - m) c for the maxima a <= m of two parts.
+__device__ __forceinline__ float max_step(float a, float m, const StatScale& k)
+{
+    const float d = m < k.low_max ? (a - m) * k.c : a * k.c - m * k.c;
+    return fmaxf(d, kMinExp);
+}
+
+__device__ __forceinline__ void stat_rebase(Stat& s, float m, const StatScale& k)
+{
+    // u against the new maximum is u + d, so 2^u gets the factor 2^d
+    const float d = max_step(s.m, m, k);
+    const float f = ex2(d);
+    s.U = f * __fmaf_rn(d, s.S, s.U);
+    s.S *= f;
+    s.m = m;
+}
+
+__device__ __forceinline__ Stat stat_join(Stat a, Stat b, const StatScale& k)
+{
+    const float m = max_nan(a.m, b.m);
+    if (m == -INFINITY) return a;             // nothing in either
+    stat_rebase(a, m, k);
+    stat_rebase(b, m, k);
+    return {m, a.S + b.S, a.U + b.U};
+}
+
+// One element.
+__device__ __forceinline__ void stat_add(Stat& s, float x, const StatScale& k)
+{
+    if (!(x <= s.m)) stat_rebase(s, max_nan(s.m, x), k);
+    if (x == -INFINITY) return;
+    const float u = fmaxf(s.m < k.low_max ? (x - s.m) * k.c : __fmaf_rn(x, k.c, -(s.m * k.c)), kMinExp);
+    const float e = ex2(u);
+    s.S += e;
+    s.U = __fmaf_rn(e, u, s.U);
+}
+
+// A thread's running statistics, S and U in two halves.  With TOP also the
+// first of the vectors that were added together with the largest element, a
+// copy of these in `kept` (shared memory), and the largest element elsewhere.
+template <int DT, int NT, bool ENT, bool TOP>
+struct ThreadStat {
+    float m = -INFINITY;
+    F2 S = 0, U = 0;
+    int best = 0;
+    float second = -INFINITY;
+
+    // N vectors at once, the first of them number i.
+    template <int N>
+    __device__ __forceinline__ void add(const uint4 (&w)[N], int i, const StatScale& k, uint4* kept)
+    {
+        constexpr int kV = El<DT>::kVec;
+        const float vm = El<DT>::vec_max(w);
+        if (TOP && vm <= m) second = max_nan(second, vm);
+        if (!(vm <= m)) {
+            if (TOP) {
+                second = m;
+                best = i;
+#pragma unroll
+                for (int l = 0; l < N; ++l) kept[l * NT + threadIdx.x] = w[l];
+            }
+            const float mm = max_nan(m, vm);
+            const float d = max_step(m, mm, k);
+            const F2 f = pack2(ex2(d), ex2(d));
+            if (ENT) U = fma2(f, fma2(pack2(d, d), S, U), 0);
+            S = fma2(f, S, 0);
+            m = mm;
+        }
+        if (m < k.low_max) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                float x[kV];
+                El<DT>::unpack(w[i], x);
+                Stat s{m, 0.0f, 0.0f};
+                for (int j = 0; j < kV; ++j) stat_add(s, x[j], k);
+                S = add2(S, pack2(s.S, 0.0f));
+                U = add2(U, pack2(s.U, 0.0f));
+            }
+            return;
+        }
+        const F2 c2 = pack2(k.c, k.c), b2 = pack2(-(m * k.c), -(m * k.c));
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            F2 x[kV / 2];
+            El<DT>::pairs_above(w[i], kLowest, x);
+#pragma unroll
+            for (int j = 0; j < kV / 2; ++j) {
+                const F2 u = fma2(x[j], c2, b2);
+                const F2 e = pack2(ex2(lo2(u)), ex2(hi2(u)));
+                S = add2(S, e);
+                if (ENT) U = fma2(e, u, U);
+            }
+        }
+    }
+
+    __device__ __forceinline__ Stat get() const
+    {
+        return {m, lo2(S) + hi2(S), ENT ? lo2(U) + hi2(U) : 0.0f};
+    }
+};
+
+// A thread's S alone (U is left out), against the largest element of its first
+// vectors instead of the running maximum: the reference cancels in the result,
+// and nothing has to be compared or rescaled, a third fewer instructions.
+// Elements so far above the reference that S overflows, NaN, +inf and a
+// reference too low for the fused exponent show in good(); the thread's
+// vectors then go through ThreadStat.
+template <int DT>
+struct RefStat {
+    float ref = -INFINITY;
+    F2 S = 0;
+
+    template <int N>
+    __device__ __forceinline__ void add(const uint4 (&w)[N], int, const StatScale& k, uint4*)
+    {
+        constexpr int kV = El<DT>::kVec;
+        if (ref == -INFINITY) {
+            ref = El<DT>::vec_max(w);
+            if (ref == -INFINITY) return;     // nothing but masked elements so far
+        }
+        const F2 c2 = pack2(k.c, k.c), b2 = pack2(-(ref * k.c), -(ref * k.c));
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            F2 x[kV / 2];
+            El<DT>::pairs(w[i], x);
+#pragma unroll
+            for (int j = 0; j < kV / 2; ++j) S = add2(S, ex2x2(fma2(x[j], c2, b2)));
+        }
+    }
+
+    __device__ __forceinline__ bool good(const StatScale& k) const
+    {
+        return ref == -INFINITY || (ref >= k.low_max && lo2(S) + hi2(S) < FLT_MAX);
+    }
+
+    __device__ __forceinline__ Stat get() const { return {ref, lo2(S) + hi2(S), 0.0f}; }
+};
+
+// Adds this thread's vectors of a slice from number i on.
+template <int DT, int NT, class TS>
+__device__ __forceinline__ void thread_rows(TS& ts, const char* row, const Slice& s, int i,
+                                            const StatScale& k, uint4* kept = nullptr)
+{
+    const char* body = row + s.vec0 * El<DT>::kBytes;
+    for (; i < s.hi - (kRowLoads - 1) * NT; i += kRowLoads * NT) {
+        uint4 w[kRowLoads];
+#pragma unroll
+        for (int l = 0; l < kRowLoads; ++l) w[l] = ld16(body + (int64_t)(i + l * NT) * 16);
+        ts.add(w, i, k, kept);
+    }
+    if (i < s.hi - NT) {
+        const uint4 w[2] = {ld16(body + (int64_t)i * 16), ld16(body + (int64_t)(i + NT) * 16)};
+        ts.add(w, i, k, kept);
+        i += 2 * NT;
+    }
+    if (i < s.hi) {
+        const uint4 w[1] = {ld16(body + (int64_t)i * 16)};
+        ts.add(w, i, k, kept);
+    }
+}
+
+// And its single elements.
+template <int DT>
+__device__ __forceinline__ Stat thread_rest(Stat st, const char* row, const Slice& s,
+                                            const StatScale& k)
+{
+    constexpr int kB = El<DT>::kBytes;
+    const int t = threadIdx.x;
+    if (t < s.head) stat_add(st, El<DT>::load(row + t * kB), k);
+    if (t < s.tail) stat_add(st, El<DT>::load(row + (int64_t)(s.tail0 + t) * kB), k);
+    return st;
+}
+
+// The statistics of a warp's lanes together: the maximum first, then sums of
+// the parts rebased to it.
+__device__ __forceinline__ Stat warp_stat(Stat s, const StatScale& k)
+{
+    float m = s.m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (m != -INFINITY) stat_rebase(s, m, k);   // (also NaN)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        s.S += __shfl_xor_sync(0xffffffffu, s.S, o);
+        s.U += __shfl_xor_sync(0xffffffffu, s.U, o);
+    }
+    return s;
+}
+
+template <int NT>
+struct StatShared {
+    Stat warp[NT / 32];
+    Stat block[kMaxCluster];   // by cluster rank
+};
+
+// The statistics of the whole row, in every thread, from each thread's own.
+// In a cluster every block must have announced itself with
+// cluster_arrive_relaxed before.  The block's barriers are two __syncthreads,
+// or one and the cluster's: what a thread stores to shared memory before the
+// call is visible to other(), which one other warp runs while the first joins
+// the warps' parts, and what other() stores is visible after the call.
+template <int NT, class F>
+__device__ __forceinline__ Stat row_stat(Stat s, const StatScale& k, StatShared<NT>& sh,
+                                         unsigned rank, unsigned n, F&& other)
+{
+    constexpr int kWarps = NT / 32;
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    s = warp_stat(s, k);
+    if (lane == 0) sh.warp[wid] = s;
+    __syncthreads();
+    if (n > 1) cluster_wait();
+    if (wid == 0) {
+        s = warp_stat(lane < kWarps ? sh.warp[lane] : Stat{-INFINITY, 0.0f, 0.0f}, k);
+        if (n == 1) {
+            if (lane == 0) sh.block[0] = s;
+        } else if (lane < (int)n) {
+            store_rank_f32(&sh.block[rank].m, lane, s.m);
+            store_rank_f32(&sh.block[rank].S, lane, s.S);
+            store_rank_f32(&sh.block[rank].U, lane, s.U);
+        }
+    }
+    if (wid == kWarps - 1) other();
+    if (n == 1) {
+        __syncthreads();
+        return sh.block[0];
+    }
+    cluster_arrive_release();
+    cluster_wait();
+    s = sh.block[0];
+    for (unsigned r = 1; r < n; ++r) s = stat_join(s, sh.block[r], k);
+    return s;
+}
+
+// lse and entropy of a row's statistics; m NaN or +inf: NaN, m -inf: -inf and 0.
+struct RowResult {
+    float lse, log2S, entropy;
+    bool empty, bad;
+};
+
+__device__ __forceinline__ RowResult row_result(const Stat& s, float scale, const StatScale& k)
+{
+    RowResult r;
+    r.empty = s.m == -INFINITY;
+    r.bad = !(s.m < INFINITY);
+    r.log2S = log2f(s.S);
+    r.lse = r.bad ? quiet_nan()
+            : r.empty ? -INFINITY
+            : s.m < k.low_max ? __fmaf_rn(s.m, scale, r.log2S * kLn2)
+                              : (s.m * k.c + r.log2S) * kLn2;
+    r.entropy = r.bad ? quiet_nan() : r.empty ? 0.0f : (r.log2S - s.U / s.S) * kLn2;
+    return r;
+}
+
+__device__ __forceinline__ float logprob_of(float x, const Stat& s, const RowResult& r, float scale,
+                                            const StatScale& k)
+{
+    if (r.bad) return quiet_nan();
+    if (r.empty) return -INFINITY;
+    if (s.m < k.low_max || x < kLowest) return __fmaf_rn(x - s.m, scale, -r.log2S * kLn2);
+    return (__fmaf_rn(x, k.c, -(s.m * k.c)) - r.log2S) * kLn2;
+}
+
+// ------------------------------------------------------------ gradients
+//
+// map_row writes f(x) for the elements of a slice, where f takes and gives
+// pairs.  An element is read and written by the same thread, so the output
+// may be the input.
+template <int DT, int NT, class F>
+__device__ __forceinline__ void map_vector(const uint4& w, char* q, bool same, F&& f)
+{
+    constexpr int kB = El<DT>::kBytes, kV = El<DT>::kVec;
+    F2 x[kV / 2];
+    El<DT>::pairs(w, x);
+#pragma unroll
+    for (int j = 0; j < kV / 2; ++j) x[j] = f(x[j]);
+    if (same) {
+        st16(q, El<DT>::pack(x));
+    } else {
+#pragma unroll
+        for (int j = 0; j < kV / 2; ++j) {
+            El<DT>::store(q + 2 * j * kB, lo2(x[j]));
+            El<DT>::store(q + (2 * j + 1) * kB, hi2(x[j]));
+        }
+    }
+}
+
+// Whether the output's rows are aligned as the input's are.
+__device__ __forceinline__ bool same_alignment(const char* row, const char* out)
+{
+    return ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
+}
+
+// The vectors from number i on, then the slice's single elements.
+template <int DT, int NT, class F>
+__device__ __forceinline__ void map_row(const char* row, char* out, const Slice& s, int i, F&& f)
+{
+    constexpr int kB = El<DT>::kBytes;
+    const int t = threadIdx.x;
+    const bool same = same_alignment(row, out);
+    const int body = s.vec0 * kB;
+    for (; i < s.hi - (kRowLoads - 1) * NT; i += kRowLoads * NT) {
+        uint4 w[kRowLoads];
+#pragma unroll
+        for (int l = 0; l < kRowLoads; ++l) w[l] = ld16(row + body + (int64_t)(i + l * NT) * 16);
+#pragma unroll
+        for (int l = 0; l < kRowLoads; ++l)
+            map_vector<DT, NT>(w[l], out + body + (int64_t)(i + l * NT) * 16, same, f);
+    }
+    for (; i < s.hi; i += NT)
+        map_vector<DT, NT>(ld16(row + body + (int64_t)i * 16), out + body + (int64_t)i * 16, same, f);
+    if (t < s.head) El<DT>::store(out + t * kB, lo2(f(pack2(El<DT>::load(row + t * kB), 0.0f))));
+    if (t < s.tail) {
+        const int64_t at = (int64_t)(s.tail0 + t) * kB;
+        El<DT>::store(out + at, lo2(f(pack2(El<DT>::load(row + at), 0.0f))));
+    }
+}
+
+// Zeros in this block's part of a row.
+template <int DT, int NT>
+__device__ __forceinline__ void zero_row(char* out, int V, unsigned rank, unsigned n)
+{
+    const Slice s = row_slice<DT>(out, V, rank, n);
+    constexpr int kB = El<DT>::kBytes;
+    const int t = threadIdx.x;
+    for (int i = s.lo + t; i < s.hi; i += NT)
+        st16(out + s.vec0 * kB + (int64_t)i * 16, make_uint4(0, 0, 0, 0));
+    if (t < s.head) El<DT>::store(out + t * kB, 0.0f);
+    if (t < s.tail) El<DT>::store(out + (int64_t)(s.tail0 + t) * kB, 0.0f);
+}
+
+// ------------------------------------------------------------ launch shapes
+
+// Threads per block for rows of this many bytes.
+constexpr int kRowThreads = 256, kShortThreads = 64;
+constexpr int64_t kShortRow = 8192;
+
+// The distillation step's blocks and the most shared memory each stages.
+constexpr int kStepThreads = 256;
+constexpr int kStageMax = 100 * 1024;
+template <int NT>
+constexpr int kStepBlocks = NT == kStepThreads ? 2 : 8;   // on an SM, at least
+
+inline int64_t row_bytes(int V, int dt) { return (int64_t)V * (dt == DPZ_F32 ? 4 : 2); }
+
+// Blocks per row: as many as keep one wave of blocks on the GPU when there are
+// few rows, at most 8, each with at least one vector per thread.
+inline unsigned row_cluster(int64_t T, int64_t bytes, int threads)
+{
+    unsigned n = 1;
+    while (n < kMaxCluster && T * n * 2 <= 304 && bytes >= (int64_t)2 * n * threads * 16) n *= 2;
+    return n;
+}
+
+}  // namespace
+
+}  // namespace dpz
