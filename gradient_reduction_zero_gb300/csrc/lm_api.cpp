@@ -179,8 +179,8 @@ DPZ_API int lm_embedding_grad(const void* dout, int64_t ld_dout, int ddtype, con
     cudaStream_t s = as_stream(stream);
     DPZ_TRY(launch(s, [&] { return launch_emb_sort(g, s); }));
     DPZ_TRY(launch(s, [&] { return launch_emb_rows(g, s); }));
-    // runs longer than one piece can only occur among more tokens than that
-    if (T > kEmbPiece) DPZ_TRY(launch(s, [&] { return launch_emb_join(g, s); }));
+    // without enough tokens for a run longer than one piece there is none to join
+    if (g.ws.pieces > 0) DPZ_TRY(launch(s, [&] { return launch_emb_join(g, s); }));
     return ok();
 }
 

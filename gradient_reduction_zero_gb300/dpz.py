@@ -138,9 +138,15 @@ def _check(rc: int) -> None:
 
 # ------------------------------------------------------------ tensor helpers
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 _CODES: dict = {}
@@ -274,61 +280,88 @@ def dp_zero2_update(shards, master, m, v, weights, N: int, cfg: AdamWCfg, ws=Non
 # ------------------------------------------------------------ vocabulary-sized ends
 #
 # Shapes, strides, types and devices are checked here (the C call sees
-# addresses only); sizes, alignment and overlaps by the library.
+# addresses only); sizes, alignment and overlaps by the library.  The checks
+# ask a tensor for few things, because on a small call they are most of it.
 
-def _id_code(t) -> int:
-    torch = _torch()
-    if t.dtype == torch.int64:
-        return I64
-    if t.dtype == torch.int32:
-        return I32
-    raise TypeError(f"token ids must be int32 or int64, not {t.dtype}")
+_ID_CODES: dict = {}
 
 
-def _mat(t, what: str, rows: int = -1, cols: int = -1) -> int:
-    """The row stride of a 2-D matrix of unit column stride on a GPU."""
-    if t.dim() != 2 or (rows >= 0 and t.shape[0] != rows) or (cols >= 0 and t.shape[1] != cols):
-        raise ValueError(f"{what} must be a matrix"
-                         + (f" [{rows}, {cols}]" if rows >= 0 and cols >= 0 else "")
-                         + f", not {list(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
-    r, c = t.shape
-    ld, step = t.stride()
-    if step != 1 and c > 1:
-        raise ValueError(f"{what} must have unit column stride")
-    return ld if r > 1 else max(ld, c)
+def _dtypes() -> dict:
+    """Element and id type codes by torch dtype."""
+    if not _ID_CODES:
+        torch = _torch()
+        _ID_CODES.update({torch.int32: I32, torch.int64: I64})
+        _CODES.update({torch.bfloat16: BF16, torch.float32: F32})
+    return _CODES
 
 
-def _dense(t, what: str, shape: tuple, dtype=None):
-    """None, or a dense GPU tensor of the given shape (fp32 unless dtype)."""
+def _current_stream(t, stream) -> int:
+    """The handle of `stream`, or of the current stream of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _bad_mat(t, what, rows, cols):
+    if t.dtype not in _dtypes():
+        raise TypeError(f"{what}: unsupported dtype {t.dtype}")
+    want = f" [{rows}, {cols}]" if rows >= 0 and cols >= 0 else ""
+    raise ValueError(f"{what} must be a CUDA matrix{want} of unit column stride, not "
+                     f"{list(t.shape)} with strides {list(t.stride())} on {t.device}")
+
+
+def _mat(t, what: str, rows: int = -1, cols: int = -1) -> tuple:
+    """(address, row stride, dtype code, rows, columns) of a 2-D matrix of unit
+    column stride on a GPU."""
+    shape, strides = t.shape, t.stride()
+    code = _dtypes().get(t.dtype)
+    if code is None or len(shape) != 2 or t.get_device() < 0:
+        _bad_mat(t, what, rows, cols)
+    r, c = shape
+    ld, step = strides
+    if (rows >= 0 and (r != rows or c != cols)) or (step != 1 and c > 1):
+        _bad_mat(t, what, rows, cols)
+    if r < 2 and ld < c:
+        ld = c
+    return t.data_ptr(), ld, code, r, c
+
+
+def _dense(t, what: str, n: int, k: int = 0, dtype=None):
+    """The address of a dense GPU tensor [n] ([n, k] with k) of fp32 (or dtype);
+    None for None."""
     if t is None:
         return None
+    shape = t.shape
     want = dtype or _torch().float32
     if t.dtype != want:
         raise TypeError(f"{what} must be {want}, not {t.dtype}")
-    if tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{what} must be a dense CUDA tensor of shape {list(shape)}, "
-                         f"not {list(t.shape)}")
+    ok = len(shape) == 1 and shape[0] == n if not k else \
+        len(shape) == 2 and shape[0] == n and shape[1] == k
+    if not ok or not t.is_contiguous() or t.get_device() < 0:
+        raise ValueError(f"{what} must be a dense CUDA tensor of shape "
+                         f"{[n, k] if k else [n]}, not {list(shape)}")
     return t.data_ptr()
 
 
-def _tokens(t, what: str, shape: tuple) -> tuple:
-    code = _id_code(t)
-    return _dense(t, what, shape, t.dtype), code
+def _tokens(t, what: str, n: int, k: int = 0) -> tuple:
+    """(address, id type code) of token ids [n] or [n, k]."""
+    _dtypes()
+    code = _ID_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{what} must be int32 or int64, not {t.dtype}")
+    return _dense(t, what, n, k, t.dtype), code
 
 
 def lm_embedding(table, ids, out, scale: float = 1.0, stream=None) -> None:
     """out[t] = scale * table[ids[t]] (a row of zeros where ids[t] is outside
     the table).  table [V, D] and out [T, D], bf16 or fp32 with any row
     stride; ids [T], int32 or int64."""
+    pt, ldt, tc, V, D = _mat(table, "table")
     T = ids.numel()
-    ldt = _mat(table, "table")
-    V, D = table.shape
-    ldo = _mat(out, "out", T, D)
-    p, it = _tokens(ids, "ids", (T,))
-    _check(_C.lm_embedding(table.data_ptr(), ldt, V, D, dtype_code(table), p, it, T, scale,
-                           out.data_ptr(), ldo, dtype_code(out), _stream_handle(stream)))
+    po, ldo, oc, _, _ = _mat(out, "out", T, D)
+    p, it = _tokens(ids, "ids", T)
+    _check(_C.lm_embedding(pt, ldt, V, D, tc, p, it, T, scale, po, ldo, oc,
+                           _current_stream(out, stream)))
 
 
 def lm_embedding_workspace(T: int, V: int, D: int, device=None):
@@ -344,22 +377,20 @@ def lm_embedding_grad(dout, ids, dtable, ws, base=None, scale: float = 1.0, stre
     base None: zeros; base may be dtable itself (rows of absent tokens are
     then left as they are).  dout [T, D], dtable and base [V, D]; ws:
     lm_embedding_workspace(T, V, D) or larger."""
+    pg, ldg, gc, V, D = _mat(dtable, "dtable")
     T = ids.numel()
-    ldg = _mat(dtable, "dtable")
-    V, D = dtable.shape
-    ldd = _mat(dout, "dout", T, D)
-    p, it = _tokens(ids, "ids", (T,))
-    ldb, pb = 0, None
+    pd, ldd, dc, _, _ = _mat(dout, "dout", T, D)
+    p, it = _tokens(ids, "ids", T)
+    pb, ldb = None, 0
     if base is not None:
-        ldb, pb = _mat(base, "base", V, D), base.data_ptr()
-        if base.dtype != dtable.dtype:
+        pb, ldb, bc, _, _ = _mat(base, "base", V, D)
+        if bc != gc:
             raise TypeError("base and dtable must have one dtype")
     need = lib.lm_embedding_workspace_bytes(T, V, D)
-    if not ws.is_cuda or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
+    if ws.get_device() < 0 or not ws.is_contiguous() or ws.nbytes < need:
         raise ValueError(f"ws must be a dense CUDA tensor of at least {need} bytes")
-    _check(_C.lm_embedding_grad(dout.data_ptr(), ldd, dtype_code(dout), p, it, T, scale, pb, ldb,
-                                dtable.data_ptr(), ldg, dtype_code(dtable), V, D, ws.data_ptr(),
-                                _stream_handle(stream)))
+    _check(_C.lm_embedding_grad(pd, ldd, dc, p, it, T, scale, pb, ldb, pg, ldg, gc, V, D,
+                                ws.data_ptr(), _current_stream(dtable, stream)))
 
 
 def lm_logprobs(logits, targets, logprob, lse=None, entropy=None, top_ids=None,
@@ -368,21 +399,20 @@ def lm_logprobs(logits, targets, logprob, lse=None, entropy=None, top_ids=None,
     logprob [T]; lse [T], entropy [T], and the K largest logits' ids (of
     targets' dtype) and log probabilities, top_ids and top_logprobs [T, K],
     where given.  logits [T, V], bf16 or fp32 with any row stride."""
-    ld = _mat(logits, "logits")
-    T, V = logits.shape
-    p, it = _tokens(targets, "targets", (T,))
-    K, pt = 0, None
+    px, ld, xc, T, V = _mat(logits, "logits")
+    p, it = _tokens(targets, "targets", T)
+    K, pt, pl = 0, None, None
     if top_ids is not None:
         if top_ids.dim() != 2 or top_logprobs is None:
             raise ValueError("top_ids must be [T, K] and come with top_logprobs")
         K = top_ids.shape[1]
-        pt = _dense(top_ids, "top_ids", (T, K), targets.dtype)
+        pt = _dense(top_ids, "top_ids", T, K, targets.dtype)
+        pl = _dense(top_logprobs, "top_logprobs", T, K)
     elif top_logprobs is not None:
         raise ValueError("top_logprobs comes with top_ids")
-    _check(_C.lm_logprobs(logits.data_ptr(), ld, T, V, dtype_code(logits), scale, p, it,
-                          _dense(logprob, "logprob", (T,)), _dense(lse, "lse", (T,)),
-                          _dense(entropy, "entropy", (T,)), K, pt,
-                          _dense(top_logprobs, "top_logprobs", (T, K)), _stream_handle(stream)))
+    _check(_C.lm_logprobs(px, ld, T, V, xc, scale, p, it, _dense(logprob, "logprob", T),
+                          _dense(lse, "lse", T), _dense(entropy, "entropy", T), K, pt, pl,
+                          _current_stream(logits, stream)))
 
 
 def lm_logprobs_grad(logits, targets, lse, dlogprob, dlogits, entropy=None, dentropy=None,
@@ -390,36 +420,31 @@ def lm_logprobs_grad(logits, targets, lse, dlogprob, dlogits, entropy=None, dent
     """The gradient of lm_logprobs' logprob (weighted by dlogprob [T]) and
     entropy (by dentropy [T], with the entropy it gave) with respect to the
     logits, into dlogits, which may be logits itself."""
-    ld = _mat(logits, "logits")
-    T, V = logits.shape
-    ldd = _mat(dlogits, "dlogits", T, V)
-    if dlogits.dtype != logits.dtype:
+    px, ld, xc, T, V = _mat(logits, "logits")
+    pd, ldd, dc, _, _ = _mat(dlogits, "dlogits", T, V)
+    if dc != xc:
         raise TypeError("logits and dlogits must have one dtype")
-    p, it = _tokens(targets, "targets", (T,))
-    _check(_C.lm_logprobs_grad(logits.data_ptr(), ld, T, V, dtype_code(logits), scale, p, it,
-                               _dense(lse, "lse", (T,)), _dense(entropy, "entropy", (T,)),
-                               _dense(dlogprob, "dlogprob", (T,)),
-                               _dense(dentropy, "dentropy", (T,)), dlogits.data_ptr(), ldd,
-                               _stream_handle(stream)))
+    p, it = _tokens(targets, "targets", T)
+    _check(_C.lm_logprobs_grad(px, ld, T, V, xc, scale, p, it, _dense(lse, "lse", T),
+                               _dense(entropy, "entropy", T), _dense(dlogprob, "dlogprob", T),
+                               _dense(dentropy, "dentropy", T), pd, ldd,
+                               _current_stream(logits, stream)))
 
 
 def _distill_args(logits, teacher_ids, teacher_logits, temperature) -> tuple:
-    ld = _mat(logits, "logits")
-    T, V = logits.shape
+    px, ld, xc, T, V = _mat(logits, "logits")
     if teacher_ids.dim() != 2:
         raise ValueError(f"teacher_ids must be [T, K], not {list(teacher_ids.shape)}")
     K = teacher_ids.shape[1]
-    p, it = _tokens(teacher_ids, "teacher_ids", (T, K))
-    return (logits.data_ptr(), ld, T, V, dtype_code(logits), p, it,
-            _dense(teacher_logits, "teacher_logits", (T, K), teacher_logits.dtype),
-            dtype_code(teacher_logits), K, temperature)
-
-
-def _dlogits_args(logits, dlogits) -> tuple:
-    ldd = _mat(dlogits, "dlogits", *logits.shape)
-    if dlogits.dtype != logits.dtype:
-        raise TypeError("logits and dlogits must have one dtype")
-    return dlogits.data_ptr(), ldd
+    if K == 0:
+        raise ValueError("teacher_ids must have at least one column")
+    p, it = _tokens(teacher_ids, "teacher_ids", T, K)
+    tc = _dtypes().get(teacher_logits.dtype)
+    if tc is None:
+        raise TypeError(f"teacher_logits: unsupported dtype {teacher_logits.dtype}")
+    return (px, ld, T, V, xc, p, it,
+            _dense(teacher_logits, "teacher_logits", T, K, teacher_logits.dtype), tc, K,
+            temperature)
 
 
 def lm_distill(logits, teacher_ids, teacher_logits, loss, lse=None, temperature: float = 1.0,
@@ -428,31 +453,36 @@ def lm_distill(logits, teacher_ids, teacher_logits, loss, lse=None, temperature:
     [T, K] (int32 or int64) and teacher_logits [T, K] (bf16 or fp32), softmax
     over the K entries at the given temperature, against softmax(logits /
     temperature) over the whole vocabulary.  loss and lse: [T]."""
-    T = logits.shape[0]
-    _check(_C.lm_distill(*_distill_args(logits, teacher_ids, teacher_logits, temperature),
-                         _dense(loss, "loss", (T,)), _dense(lse, "lse", (T,)),
-                         _stream_handle(stream)))
+    args = _distill_args(logits, teacher_ids, teacher_logits, temperature)
+    T = args[2]
+    _check(_C.lm_distill(*args, _dense(loss, "loss", T), _dense(lse, "lse", T),
+                         _current_stream(logits, stream)))
 
 
 def lm_distill_grad(logits, teacher_ids, teacher_logits, lse, dloss, dlogits,
                     temperature: float = 1.0, stream=None) -> None:
     """The gradient of sum(dloss * loss) of lm_distill with respect to the
     logits, from its lse, into dlogits, which may be logits itself."""
-    T = logits.shape[0]
-    _check(_C.lm_distill_grad(*_distill_args(logits, teacher_ids, teacher_logits, temperature),
-                              _dense(lse, "lse", (T,)), _dense(dloss, "dloss", (T,)),
-                              *_dlogits_args(logits, dlogits), _stream_handle(stream)))
+    args = _distill_args(logits, teacher_ids, teacher_logits, temperature)
+    T, V = args[2], args[3]
+    pd, ldd, dc, _, _ = _mat(dlogits, "dlogits", T, V)
+    if dc != args[4]:
+        raise TypeError("logits and dlogits must have one dtype")
+    _check(_C.lm_distill_grad(*args, _dense(lse, "lse", T), _dense(dloss, "dloss", T), pd, ldd,
+                              _current_stream(logits, stream)))
 
 
 def lm_distill_step(logits, teacher_ids, teacher_logits, dloss, loss, dlogits, lse=None,
                     temperature: float = 1.0, stream=None) -> None:
     """lm_distill and lm_distill_grad in one pass over the logits, for weights
     dloss [T] known beforehand; dlogits may be logits itself."""
-    T = logits.shape[0]
-    _check(_C.lm_distill_step(*_distill_args(logits, teacher_ids, teacher_logits, temperature),
-                              _dense(dloss, "dloss", (T,)), _dense(loss, "loss", (T,)),
-                              _dense(lse, "lse", (T,)), *_dlogits_args(logits, dlogits),
-                              _stream_handle(stream)))
+    args = _distill_args(logits, teacher_ids, teacher_logits, temperature)
+    T, V = args[2], args[3]
+    pd, ldd, dc, _, _ = _mat(dlogits, "dlogits", T, V)
+    if dc != args[4]:
+        raise TypeError("logits and dlogits must have one dtype")
+    _check(_C.lm_distill_step(*args, _dense(dloss, "dloss", T), _dense(loss, "loss", T),
+                              _dense(lse, "lse", T), pd, ldd, _current_stream(logits, stream)))
 
 
 class PreparedCall:
