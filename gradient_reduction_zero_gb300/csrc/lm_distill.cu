@@ -227,6 +227,9 @@ __global__ void __launch_bounds__(NT, 8 * kRowThreads / NT) k_distill_grad(Disti
         return;
     }
     const Slice sl = row_slice<DT>(row, a.V, rank, n);
+    // the row's first vectors come while the entries do
+    uint4 v[kMapLoads];
+    map_load<DT, NT>(row, sl, sl.lo + threadIdx.x, v);
     // in place, other blocks' slices may be overwritten already
     if (threadIdx.x >= NT - 32) {
         clear_hash(hash);
@@ -240,7 +243,7 @@ __global__ void __launch_bounds__(NT, 8 * kRowThreads / NT) k_distill_grad(Disti
         return;
     }
     const StudentGrad f(a.inv_tau, lse, wt * a.inv_tau);
-    map_row<DT, NT>(row, out, sl, sl.lo + threadIdx.x, f);
+    map_row<DT, NT>(row, out, sl, sl.lo + threadIdx.x, v, f);
     __syncthreads();
     if (threadIdx.x >= NT - 32) write_teacher_part<DT>(a, w, sl, f, out);
 }
@@ -455,7 +458,11 @@ __global__ void __launch_bounds__(NT + 32, kStepBlocks<NT>) k_distill_step(Disti
             copy_commit();
         }
         if (zero) zero_row<DT, NT>(out, a.V, rank, n);
-        else map_row<DT, NT>(row, out, sl, first + have * NT, f);
+        else {
+            uint4 v[kMapLoads];
+            map_load<DT, NT>(row, sl, first + have * NT, v);
+            map_row<DT, NT>(row, out, sl, first + have * NT, v, f);
+        }
         barrier_arrive<NT + 32>();
         row = next;
         sl = ns;
@@ -490,7 +497,10 @@ cudaError_t launch_step(const DistillArgs& a, cudaStream_t s)
 {
     static SmemRaised raised;
     const int64_t bytes = row_bytes(a.V, DT);
-    const unsigned n = row_cluster(a.T, bytes, NT);
+    // two blocks where one cannot stage a row (4,096 rows of 50,257 fp32: 299 us,
+    // 342 with one block that reads half of the row again; 2,048 of 128,256 bf16:
+    // 216 and 238; with four blocks 350, their barriers being more than that)
+    const unsigned n = std::max(row_cluster(a.T, bytes, NT), bytes > kStageMax ? 2u : 1u);
     const int64_t vecs = (bytes / 16 + n - 1) / n + 1;
     const int stage = (int)std::min<int64_t>((vecs + NT - 1) / NT, kStageMax / (NT * 16));
     cudaError_t e =
@@ -498,7 +508,7 @@ cudaError_t launch_step(const DistillArgs& a, cudaStream_t s)
     int blocks = 0;
     if (e == cudaSuccess) e = resident_blocks<DT, NT>(stage, &blocks);
     if (e != cudaSuccess) return e;
-    const unsigned grid = n > 1 ? (unsigned)a.T * n : (unsigned)std::min<int64_t>(a.T, blocks);
+    const unsigned grid = n * (unsigned)std::min<int64_t>(a.T, std::max(1u, blocks / n));
     return launch_kernel(k_distill_step<DT, NT>, dim3(grid), dim3(NT + 32), (size_t)stage * NT * 16, s,
                          true, n > 1 ? n : 0u, a, stage);
 }
@@ -530,7 +540,10 @@ cudaError_t launch_distill(const DistillArgs& a, cudaStream_t s)
         return launch_kernel(fn, dim3((unsigned)a.T * n), dim3(nt), 0, s, true, n > 1 ? n : 0u, a);
     }
     set_last_kernel_name("lm_distill_grad");
-    const unsigned n = row_cluster(a.T, bytes, nt);
+    // two independent blocks per row share the last wave better than one (1,000
+    // rows of 32,000 fp32: 45.5 us, 50 with one, 53 with four, each of which loads
+    // the entries again)
+    const unsigned n = std::max(row_cluster(a.T, bytes, nt), small ? 1u : 2u);
     auto fn = small ? (b ? k_distill_grad<DPZ_BF16, kShortThreads> : k_distill_grad<DPZ_F32, kShortThreads>)
                     : (b ? k_distill_grad<DPZ_BF16, kRowThreads> : k_distill_grad<DPZ_F32, kRowThreads>);
     return launch_kernel(fn, dim3((unsigned)a.T, n), dim3(nt), 0, s, true, 0u, a);

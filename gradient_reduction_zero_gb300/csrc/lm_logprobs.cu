@@ -35,6 +35,15 @@ __device__ __forceinline__ uint64_t warp_max64(uint64_t k)
     return k;
 }
 
+// How many of n keys are above this one.
+__device__ __forceinline__ int keys_above(const uint64_t* keys, int n, uint64_t key)
+{
+    int above = 0;
+#pragma unroll 8
+    for (int q = 0; q < n; ++q) above += keys[q] > key;
+    return above;
+}
+
 // Where a thread's largest elements are: the order of its largest one (0
 // without elements), the first of the `count` vectors that were loaded with
 // it, and the order of the largest element elsewhere.
@@ -45,15 +54,23 @@ struct ThreadTop {
 
 constexpr int kTopCap = 512;                        // candidates a block can hold
 
-template <int NT>
+// Vectors that a thread loads at once, and keeps of its largest element's
+// batch.  Two of fp32 take half the shared memory of four: 1,021 rows of 50,304
+// with 20 alternatives 39 us with 2 and 47 with 4; bf16, 4,096 rows of 50,257
+// with 8, 88 us with 2 and 82 with 4.
+template <int DT>
+constexpr int kTopLoads = DT == DPZ_F32 ? 2 : 4;
+
+template <int NT, int LOADS>
 struct TopShared {
-    uint4 kept[kRowLoads * NT];                     // each thread's vectors with its largest element
+    uint4 kept[LOADS * NT];                            // each thread's vectors with its largest element
     uint64_t cand[kTopCap];
     uint64_t merged[kMaxCluster * DPZ_LM_MAX_TOP];  // a cluster's first block: every block's best
     uint64_t best[NT / 32];
-    uint32_t group[32];
+    uint32_t lane_max[NT / 32][32];                 // each thread's largest
+    int2 flag[NT];                                  // threads that reach the threshold
     uint32_t threshold;
-    int n;
+    int n, flags;
 };
 
 // The statistics of this thread's elements of a slice, and where the largest are.
@@ -63,88 +80,85 @@ __device__ __forceinline__ Stat thread_stat(const char* row, const Slice& s, con
 {
     const int t = threadIdx.x;
     ThreadStat<DT, NT, ENT, TOP> ts;
-    thread_rows<DT, NT>(ts, row, s, s.lo + t, k, kept);
+    constexpr int kLoads = TOP ? kTopLoads<DT> : 4;
+    thread_rows<DT, NT, kLoads>(ts, row, s, s.lo + t, k, kept);
     const Stat st = thread_rest<DT>(ts.get(), row, s, k);
     if (TOP) {
         const bool single = t < s.head || t < s.tail;
         top->max = single || s.lo + t < s.hi ? value_order(st.m) : 0u;
         top->second = single ? top->max : value_order(ts.second);
         top->best = ts.best;
-        // full batches of kRowLoads, then one of two, then a single one
+        // the batches of thread_rows
         const int mine = s.hi - s.lo - t, at = (ts.best - s.lo - t) / NT;
         const int n = (mine + NT - 1) / NT - at;
-        top->count = n >= kRowLoads ? kRowLoads : n >= 2 ? 2 : 1;
+        top->count = n >= kLoads ? kLoads : n >= 2 ? 2 : 1;
     }
     return st;
 }
 
-// Calls f(x, j) for each element x of index j that thread `t` of the block
-// has.  part, parts: only every parts-th of its vectors, from part (and the
-// single elements with part 0), for threads that share the work of one.
+// Calls f(x, j) for each element x of index j that this thread has.
 template <int DT, int NT, class F>
-__device__ __forceinline__ void for_elements(const char* row, const Slice& s, int t, int part,
-                                             int parts, F&& f)
+__device__ __forceinline__ void for_elements(const char* row, const Slice& s, F&& f)
 {
     constexpr int kB = El<DT>::kBytes, kV = El<DT>::kVec;
     const char* body = row + s.vec0 * kB;
-    for (int64_t i = s.lo + t + (int64_t)part * NT; i < s.hi; i += (int64_t)parts * NT) {
+    const int t = threadIdx.x;
+    for (int i = s.lo + t; i < s.hi; i += NT) {
         float x[kV];
-        El<DT>::unpack(ld16(body + i * 16), x);
+        El<DT>::unpack(ld16(body + (int64_t)i * 16), x);
 #pragma unroll
-        for (int j = 0; j < kV; ++j) f(x[j], s.vec0 + (int)i * kV + j);
+        for (int j = 0; j < kV; ++j) f(x[j], s.vec0 + i * kV + j);
     }
-    if (part != 0) return;
     if (t < s.head) f(El<DT>::load(row + t * kB), t);
     if (t < s.tail) f(El<DT>::load(row + (int64_t)(s.tail0 + t) * kB), s.tail0 + t);
 }
 
-// Before the block's first barrier: the maxima of 32 groups of threads.
-template <int NT>
-__device__ __forceinline__ void top_groups(uint32_t max_, TopShared<NT>& sh)
-{
-    constexpr int kGroup = NT / 32;
-    uint32_t g = max_;
-#pragma unroll
-    for (int o = 1; o < kGroup; o <<= 1) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
-    if (threadIdx.x % kGroup == 0) sh.group[threadIdx.x / kGroup] = g;
-}
-
-// By one warp: the K-th largest of the groups' maxima (K <= 32).
-template <int NT>
-__device__ __forceinline__ void top_threshold(int K, TopShared<NT>& sh)
+// By one warp: the K-th largest of 64 groups' maxima (K <= 32).  A group is the
+// threads of one lane in the even or the odd warps.  Elements that lie side by
+// side (a vocabulary's frequent tokens come first) are in different lanes, so
+// large ones do not crowd in few groups.
+template <int NT, int LOADS>
+__device__ __forceinline__ void top_threshold(int K, TopShared<NT, LOADS>& sh)
 {
     const int lane = threadIdx.x & 31;
-    const uint32_t v = sh.group[lane];
-    int above = 0;
+    uint32_t a = 0, b = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const uint32_t w = __shfl_sync(0xffffffffu, v, i);
-        above += w > v || (w == v && i < lane);
+    for (int w = 0; w < NT / 32; w += 2) {
+        a = max(a, sh.lane_max[w][lane]);
+        b = max(b, sh.lane_max[w + 1][lane]);
     }
-    if (above == K - 1) sh.threshold = v;
-    if (lane == 0) sh.n = 0;
+    int above_a = 0, above_b = 0;
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i) {
+        const uint32_t x = __shfl_sync(0xffffffffu, a, i), y = __shfl_sync(0xffffffffu, b, i);
+        above_a += (x > a || (x == a && i < lane)) + (y > a);
+        above_b += (x >= b) + (y > b || (y == b && i < lane));
+    }
+    if (above_a == K - 1) sh.threshold = a;
+    if (above_b == K - 1) sh.threshold = b;
+    if (lane == 0) sh.n = sh.flags = 0;
 }
 
 // Calls emit(k, key) once for each of the slice's K largest keys (of all, if
 // it has fewer elements), k being its rank, from any thread of the block.
 //
-// The K-th largest of 32 groups' maxima is a threshold that at least K
+// The K-th largest of 64 groups' maxima is a threshold that at least K
 // elements reach, and few more do: a random row of any length has
-// 32 (H(32) - H(32 - K)) of them, 9 for K = 8, 31 for K = 20 and 130 for
-// K = 32 (H: harmonic numbers).  Only threads whose own maximum reaches it
-// look at their elements again, a warp's lanes sharing the work for each: at
-// the kept vectors if nothing else of theirs reaches it, else at all.  The
-// candidates are ranked against each other.  If more than kTopCap elements
+// 64 (H(64) - H(64 - K)) of them, 9 for K = 8, 24 for K = 20 and 44 for
+// K = 32 (H: harmonic numbers).  Only the elements of threads whose own maximum
+// reaches it are looked at again, the warps taking turns with the threads: the
+// kept vectors if nothing else of the thread's reaches it, else all of them.
+// The candidates are ranked against each other.  If more than kTopCap elements
 // reach it (rows of few distinct values), K rounds of a block-wide maximum
 // are run instead.  If only masked elements are left below the threshold
 // (fewer than K groups have any other), the unmasked ones are candidates and
 // the masked ones of lowest index, which are ties, fill up.
 template <int DT, int NT, class F>
 __device__ __forceinline__ void block_top(const char* row, const Slice& s, const ThreadTop& own,
-                                          int K, TopShared<NT>& sh, F&& emit)
+                                          int K, TopShared<NT, kTopLoads<DT>>& sh, F&& emit)
 {
     constexpr int kB = El<DT>::kBytes, kV = El<DT>::kVec;
-    static_assert(kRowLoads * kV <= 32, "one lane per kept element");
+    static_assert(kTopLoads<DT> * kV <= 32, "one lane per kept element");
     static_assert(2 * DPZ_LM_MAX_TOP <= NT, "one thread per element that fills up");
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const uint32_t th = max(sh.threshold, 1u);
@@ -157,23 +171,37 @@ __device__ __forceinline__ void block_top(const char* row, const Slice& s, const
             if (at < kTopCap) sh.cand[at] = rank_key(o, j);
         }
     };
-    unsigned m = __ballot_sync(0xffffffffu, own.max >= least && own.second < least);
-    while (m != 0) {
-        const int src = __ffs(m) - 1, l = lane / kV, j = lane % kV;
-        m &= m - 1;
-        const int best = __shfl_sync(0xffffffffu, own.best, src);
-        const int count = __shfl_sync(0xffffffffu, own.count, src);
-        if (l < count) {
-            const uint4* v = &sh.kept[l * NT + (wid << 5) + src];
-            offer(El<DT>::load(reinterpret_cast<const char*>(v) + j * kB),
-                  s.vec0 + (best + l * NT) * kV + j);
-        }
+    const bool flagged = own.max >= least;
+    const unsigned m = __ballot_sync(0xffffffffu, flagged);
+    if (m != 0) {
+        int at = 0;
+        if (lane == 0) at = atomicAdd(&sh.flags, __popc(m));
+        at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1u));
+        if (flagged) sh.flag[at] = make_int2(own.second >= least ? -1 : own.best, threadIdx.x << 3 | own.count);
     }
-    m = __ballot_sync(0xffffffffu, own.max >= least && own.second >= least);
-    while (m != 0) {
-        const int owner = (wid << 5) + __ffs(m) - 1;
-        m &= m - 1;
-        for_elements<DT, NT>(row, s, owner, lane, 32, offer);
+    __syncthreads();
+    for (int q = wid; q < sh.flags; q += NT / 32) {
+        const int2 e = sh.flag[q];
+        const int t = e.y >> 3, count = e.y & 7;
+        if (e.x >= 0) {
+            const int l = lane / kV, j = lane % kV;
+            if (l < count)
+                offer(El<DT>::load(reinterpret_cast<const char*>(&sh.kept[l * NT + t]) + j * kB),
+                      s.vec0 + (e.x + l * NT) * kV + j);
+            continue;
+        }
+        for (int i = s.lo + t + lane * NT; i < s.hi; i += 32 * NT) {
+            const uint4 v[1] = {ld16(row + s.vec0 * kB + (int64_t)i * 16)};
+            if (value_order(El<DT>::vec_max(v)) < least) continue;
+            float x[kV];
+            El<DT>::unpack(v[0], x);
+#pragma unroll
+            for (int j = 0; j < kV; ++j) offer(x[j], s.vec0 + i * kV + j);
+        }
+        if (lane == 0) {
+            if (t < s.head) offer(El<DT>::load(row + t * kB), t);
+            if (t < s.tail) offer(El<DT>::load(row + (int64_t)(s.tail0 + t) * kB), s.tail0 + t);
+        }
     }
     __syncthreads();
     int n = sh.n;
@@ -190,8 +218,7 @@ __device__ __forceinline__ void block_top(const char* row, const Slice& s, const
     if (n <= kTopCap) {
         for (int i = threadIdx.x; i < n; i += NT) {
             const uint64_t key = sh.cand[i];
-            int above = 0;
-            for (int q = 0; q < n; ++q) above += sh.cand[q] > key;
+            const int above = keys_above(sh.cand, n, key);
             if (above < K) emit(above, key);
         }
         return;
@@ -203,7 +230,7 @@ __device__ __forceinline__ void block_top(const char* row, const Slice& s, const
     for (int k = 0; k < K; ++k) {
         if (stale) {
             best = 0;
-            for_elements<DT, NT>(row, s, threadIdx.x, 0, 1, [&](float x, int j) {
+            for_elements<DT, NT>(row, s, [&](float x, int j) {
                 const uint64_t key = rank_key(value_order(x), j);
                 if (key < prev && key > best) best = key;
             });
@@ -226,7 +253,7 @@ __global__ void __launch_bounds__(NT, (DT == DPZ_F32 ? 7 : 6) * kRowThreads / NT
     k_logprobs(LogprobArgs a)
 {
     __shared__ StatShared<NT> ssh;
-    __shared__ TopShared<TOP ? NT : 32> tsh;
+    __shared__ TopShared<TOP ? NT : 64, kTopLoads<DT>> tsh;
     __shared__ RowResult s_result;
     const unsigned rank = cluster_rank(), n = cluster_size();
     if (n > 1) cluster_arrive_relaxed();
@@ -244,7 +271,7 @@ __global__ void __launch_bounds__(NT, (DT == DPZ_F32 ? 7 : 6) * kRowThreads / NT
     ThreadTop own;
     const Stat mine = thread_stat<DT, NT, ENT, TOP>(row, sl, k, &own, tsh.kept);
     if constexpr (TOP) {
-        top_groups(own.max, tsh);
+        tsh.lane_max[threadIdx.x >> 5][threadIdx.x & 31] = own.max;
         if (n > 1 && rank == 0)
             for (unsigned i = threadIdx.x; i < n * a.K; i += NT) tsh.merged[i] = 0;
     }
@@ -283,8 +310,7 @@ __global__ void __launch_bounds__(NT, (DT == DPZ_F32 ? 7 : 6) * kRowThreads / NT
         if (rank != 0) return;
         for (unsigned i = threadIdx.x; i < n * a.K; i += NT) {
             const uint64_t key = tsh.merged[i];
-            int above = 0;
-            for (unsigned q = 0; q < n * a.K; ++q) above += tsh.merged[q] > key;
+            const int above = keys_above(tsh.merged, n * a.K, key);
             if (key != 0 && above < a.K) write(above, key);
         }
     }
@@ -326,8 +352,10 @@ __global__ void __launch_bounds__(NT) k_logprobs_grad(LogprobGradArgs a)
     const bool mine = g != 0.0f && y >= s.first && y < s.last;
     if (mine && threadIdx.x == 0)
         at_y = lo2(d(pack2(El<DT>::load_now(row + (int64_t)y * El<DT>::kBytes), 0.0f)));
+    uint4 w[kMapLoads];
+    map_load<DT, NT>(row, s, s.lo + threadIdx.x, w);
     if (mine) __syncthreads();     // in place, before it is overwritten
-    map_row<DT, NT>(row, out, s, s.lo + threadIdx.x, d);
+    map_row<DT, NT>(row, out, s, s.lo + threadIdx.x, w, d);
     if (!mine) return;
     __syncthreads();
     if (threadIdx.x == 0)

@@ -20,7 +20,6 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kRowLoads = 4;         // vectors a thread loads at once (then 2, then 1)
 
 __device__ __forceinline__ int load_token(const Ids& ids, int64_t i, int64_t V)
 {
@@ -100,7 +99,7 @@ __device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fc00000)
 // 16-byte vectors, and a tail.
 
 template <int DT>
-struct El;
+struct El;   // kVec: elements of a 16-byte vector
 
 template <>
 struct El<DPZ_F32> {
@@ -469,19 +468,20 @@ struct RefStat {
     __device__ __forceinline__ Stat get() const { return {ref, lo2(S) + hi2(S), 0.0f}; }
 };
 
-// Adds this thread's vectors of a slice from number i on.
-template <int DT, int NT, class TS>
+// Adds this thread's vectors of a slice from number i on: full batches of
+// kLoads, then one of two, then a single one.
+template <int DT, int NT, int kLoads = 4, class TS>
 __device__ __forceinline__ void thread_rows(TS& ts, const char* row, const Slice& s, int i,
                                             const StatScale& k, uint4* kept = nullptr)
 {
     const char* body = row + s.vec0 * El<DT>::kBytes;
-    for (; i < s.hi - (kRowLoads - 1) * NT; i += kRowLoads * NT) {
-        uint4 w[kRowLoads];
+    for (; i < s.hi - (kLoads - 1) * NT; i += kLoads * NT) {
+        uint4 w[kLoads];
 #pragma unroll
-        for (int l = 0; l < kRowLoads; ++l) w[l] = ld16(body + (int64_t)(i + l * NT) * 16);
+        for (int l = 0; l < kLoads; ++l) w[l] = ld16(body + (int64_t)(i + l * NT) * 16);
         ts.add(w, i, k, kept);
     }
-    if (i < s.hi - NT) {
+    if (kLoads > 2 && i < s.hi - NT) {
         const uint4 w[2] = {ld16(body + (int64_t)i * 16), ld16(body + (int64_t)(i + NT) * 16)};
         ts.add(w, i, k, kept);
         i += 2 * NT;
@@ -623,24 +623,37 @@ __device__ __forceinline__ bool same_alignment(const char* row, const char* out)
     return ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
 }
 
-// The vectors from number i on, then the slice's single elements.
+// A thread's next vectors, loaded ahead of their use.
+constexpr int kMapLoads = 4;
+
+template <int DT, int NT>
+__device__ __forceinline__ void map_load(const char* row, const Slice& s, int i,
+                                         uint4 (&w)[kMapLoads])
+{
+    const char* body = row + s.vec0 * El<DT>::kBytes;
+#pragma unroll
+    for (int l = 0; l < kMapLoads; ++l)
+        if (i + l * NT < s.hi) w[l] = ld16(body + (int64_t)(i + l * NT) * 16);
+}
+
+// The vectors from number i on, of which w are the first, then the slice's
+// single elements.
 template <int DT, int NT, class F>
-__device__ __forceinline__ void map_row(const char* row, char* out, const Slice& s, int i, F&& f)
+__device__ __forceinline__ void map_row(const char* row, char* out, const Slice& s, int i,
+                                        uint4 (&w)[kMapLoads], F&& f)
 {
     constexpr int kB = El<DT>::kBytes;
     const int t = threadIdx.x;
     const bool same = same_alignment(row, out);
     const int body = s.vec0 * kB;
-    for (; i < s.hi - (kRowLoads - 1) * NT; i += kRowLoads * NT) {
-        uint4 w[kRowLoads];
+    while (i < s.hi) {
 #pragma unroll
-        for (int l = 0; l < kRowLoads; ++l) w[l] = ld16(row + body + (int64_t)(i + l * NT) * 16);
-#pragma unroll
-        for (int l = 0; l < kRowLoads; ++l)
-            map_vector<DT, NT>(w[l], out + body + (int64_t)(i + l * NT) * 16, same, f);
+        for (int l = 0; l < kMapLoads; ++l)
+            if (i + l * NT < s.hi)
+                map_vector<DT, NT>(w[l], out + body + (int64_t)(i + l * NT) * 16, same, f);
+        i += kMapLoads * NT;
+        map_load<DT, NT>(row, s, i, w);
     }
-    for (; i < s.hi; i += NT)
-        map_vector<DT, NT>(ld16(row + body + (int64_t)i * 16), out + body + (int64_t)i * 16, same, f);
     if (t < s.head) El<DT>::store(out + t * kB, lo2(f(pack2(El<DT>::load(row + t * kB), 0.0f))));
     if (t < s.tail) {
         const int64_t at = (int64_t)(s.tail0 + t) * kB;
@@ -675,12 +688,17 @@ constexpr int kStepBlocks = NT == kStepThreads ? 2 : 8;   // on an SM, at least
 
 inline int64_t row_bytes(int V, int dt) { return (int64_t)V * (dt == DPZ_F32 ? 4 : 2); }
 
-// Blocks per row: as many as keep one wave of blocks on the GPU when there are
-// few rows, at most 8, each with at least one vector per thread.
+// Blocks per row, a power of two up to 8.  With few rows, as many as keep one
+// wave of blocks on the GPU, each with at least one vector per thread; rows of
+// half a megabyte and more are split for up to two waves, which hides a
+// cluster's barriers (256 rows of 256,000 fp32: 76 us with one block, 55 with
+// 2, 61 with 4; 300 rows of 50,257 bf16: 16.5 us with one, 20 with 2).
 inline unsigned row_cluster(int64_t T, int64_t bytes, int threads)
 {
     unsigned n = 1;
-    while (n < kMaxCluster && T * n * 2 <= 304 && bytes >= (int64_t)2 * n * threads * 16) n *= 2;
+    while (n < kMaxCluster && bytes >= (int64_t)2 * n * threads * 16 &&
+           (T * n * 2 <= 304 || (T * n * 2 <= 608 && bytes >= (int64_t)2 * n * (256 << 10))))
+        n *= 2;
     return n;
 }
 
