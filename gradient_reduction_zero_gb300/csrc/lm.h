@@ -39,11 +39,13 @@ constexpr int kEmbMaxPiece = 64;
 constexpr int kEmbLogBins = 10;   // a sorting block owns at most 2^10 ids
 
 struct EmbWs {
-    int2* owner;      // [owners] pieces and long runs of each owner
+    int4* owner;      // [owners] pieces, long runs and short runs of each owner
     int2* run;        // [V] first sorted position of token v, how often it occurs
     int* order;       // [T] token positions by (owner, id, position)
     int4* longs;      // [owners][2^kEmbLogBins] token, first position, length,
                       // pieces of the owner's long runs before it
+    int4* shorts;     // [owners][2^kEmbLogBins] token, first position, length of the
+                      // others, if the call adds in place
     float* partial;   // [pieces][Dpad] sums of pieces, by owner and run
     int64_t Dpad;     // row stride of partial
     int64_t pieces;   // most pieces there can be
@@ -84,13 +86,15 @@ inline size_t emb_ws_layout(void* p, int64_t T, int64_t V, int64_t D, EmbWs* w)
     };
     const size_t owners = size_t(1) << emb_log_owners(V);
     const int64_t Dpad = (D + 7) / 8 * 8, pieces = emb_pieces(T);
-    const size_t o_owner = take(8 * owners), o_run = take(8 * size_t(V)), o_order = take(4 * size_t(T)),
+    const size_t o_owner = take(16 * owners), o_run = take(8 * size_t(V)), o_order = take(4 * size_t(T)),
                  o_longs = take(16 * (owners << kEmbLogBins)),
+                 o_shorts = take(16 * (owners << kEmbLogBins)),
                  o_partial = take(4 * size_t(Dpad) * size_t(pieces));
     if (w && b)
-        *w = EmbWs{reinterpret_cast<int2*>(b + o_owner), reinterpret_cast<int2*>(b + o_run),
+        *w = EmbWs{reinterpret_cast<int4*>(b + o_owner), reinterpret_cast<int2*>(b + o_run),
                    reinterpret_cast<int*>(b + o_order),  reinterpret_cast<int4*>(b + o_longs),
-                   reinterpret_cast<float*>(b + o_partial), Dpad, pieces, emb_piece(T)};
+                   reinterpret_cast<int4*>(b + o_shorts), reinterpret_cast<float*>(b + o_partial),
+                   Dpad, pieces, emb_piece(T)};
     return at;
 }
 

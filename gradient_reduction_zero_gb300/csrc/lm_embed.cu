@@ -1,4 +1,6 @@
 // Embedding lookup with scaling, and its gradient by sorted tokens.
+#include <algorithm>
+
 #include "bulk.cuh"
 #include "device.cuh"
 #include "internal.h"
@@ -297,15 +299,19 @@ __global__ void __launch_bounds__(kSortThreads)
     const int pieces = total > ws.piece ? (total + ws.piece - 1) / ws.piece : 0;
     const int incl = block_scan(total, warp_tot);
     const int incl_pieces = block_scan(pieces, warp_tot);
-    const int incl_long = block_scan(pieces > 0, warp_tot);
+    // two counts of at most 1,024 in one sum
+    const int is_long = pieces > 0, is_short = total > 0 && !is_long;
+    const int incl_runs = block_scan(is_long << 16 | is_short, warp_tot);
     if (threadIdx.x < bins) {
         int at = s_base + incl - total;
         const int v = (int)(threadIdx.x << log_owners) + me;
         if (v < V) ws.run[v] = make_int2(at, total);
-        if (pieces > 0)
-            ws.longs[((int64_t)me << kSortLogBins) + incl_long - 1] =
-                make_int4(v, at, total, incl_pieces - pieces);
-        if (threadIdx.x == bins - 1) ws.owner[me] = make_int2(incl_pieces, incl_long);
+        const int64_t list = (int64_t)me << kSortLogBins;
+        if (is_long)
+            ws.longs[list + (incl_runs >> 16) - 1] = make_int4(v, at, total, incl_pieces - pieces);
+        if (is_short) ws.shorts[list + (incl_runs & 0xffff) - 1] = make_int4(v, at, total, 0);
+        if (threadIdx.x == bins - 1)
+            ws.owner[me] = make_int4(incl_pieces, incl_runs >> 16, incl_runs & 0xffff, 0);
         for (int w = 0; w < kSortWarps; ++w) {
             const int n = hist[w * bins + threadIdx.x];
             hist[w * bins + threadIdx.x] = at;
@@ -344,7 +350,7 @@ __device__ __forceinline__ OwnerOf find_owner(const EmbWs& ws, int owners, int j
         int n[4], sum = 0;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            n[u] = ws.owner[o0 + lane * 4 + u].x;
+            n[u] = ws.owner[o0 + lane * 4 + u].x;   // pieces
             sum += n[u];
         }
         int incl = sum;
@@ -413,8 +419,9 @@ __device__ __forceinline__ int pieces_before(const EmbWs& ws, int owner)
 
 // Sums of rows.  A block has one thread per unit of columns and a list of
 // segments, each a stretch of the sorted order with one destination: the rows
-// of a group of consecutive ids of one owner (whose tokens stand together), or
-// one piece of a long run, whose sum goes to a partial row.  The base's rows are copied to
+// of a group of consecutive ids of one owner (whose tokens stand together; in
+// place, of consecutive ids that have tokens), or one piece of a long run,
+// whose sum goes to a partial row.  The base's rows are copied to
 // shared memory asynchronously, before anything is known about the tokens
 // (in place: for the rows with tokens only); each thread uses what it copied
 // itself.  Rows without a token are then written as they are.  The others'
@@ -429,50 +436,39 @@ constexpr int kSegments = 8;
 constexpr int kRowsBlocks = 5;   // of kBlock threads on an SM, at least
 
 struct Segments {
-    int empty_bin[kSegments];  // table rows without a token, by their place in the group
-    int bin[kSegments];        // with tokens: the same, or -1 for a piece
+    int empty[kSegments];      // rows without a token, by their place in the group
+    int slot[kSegments];       // with tokens: the same
+    int row[kSegments];        // by place in the group: the table row, -1 for a piece
     int start[kSegments];      // in the sorted order
     int first[kSegments];      // its first item
-    int empty, full, items;    // how many of each
+    int empties, full, items;  // how many of each
     int item[kSegments * kEmbMaxPiece];   // token positions
 };
 
-// By one warp: this lane's segment of the block's (count < 0: none).
-__device__ __forceinline__ void find_segment(const EmbGrad& g, int64_t block, int64_t row0,
-                                             int log_owners, int group, int& bin, int& start, int& count)
+// By one warp: this lane's segment of a piece (lane 0) or a group of rows
+// (count < 0: none).
+__device__ __forceinline__ void find_piece(const EmbGrad& g, int piece, int log_owners, int& start,
+                                           int& count)
 {
     const int lane = threadIdx.x & 31;
-    bin = start = 0;
-    count = -1;
-    if (block < g.ws.pieces) {
-        const OwnerOf o = find_owner(g.ws, 1 << log_owners, (int)block);
-        if (o.owner < 0) return;
-        // the owner's long run that the piece is of: the last to begin at or before it
-        const int j = (int)block - o.before, runs = g.ws.owner[o.owner].y;
-        const int4* list = g.ws.longs + ((int64_t)o.owner << kSortLogBins);
-        int4 run = make_int4(0, 0, 0, 0);
-        for (int i0 = 0; i0 < runs; i0 += 32) {
-            const int4 r = i0 + lane < runs ? list[i0 + lane] : make_int4(0, 0, 0, 0x7fffffff);
-            const unsigned m = __ballot_sync(0xffffffffu, r.w <= j);
-            if (m == 0) break;
-            const int src = 31 - __clz(m);
-            run.y = __shfl_sync(0xffffffffu, r.y, src);
-            run.z = __shfl_sync(0xffffffffu, r.z, src);
-            run.w = __shfl_sync(0xffffffffu, r.w, src);
-        }
-        if (lane > 0) return;
-        bin = -1;
-        start = run.y + (j - run.w) * g.ws.piece;
-        count = min(g.ws.piece, run.y + run.z - start);
-    } else {
-        const int64_t v = row0 + ((int64_t)lane << log_owners);
-        if (lane >= group || v >= g.V) return;
-        const int2 run = g.ws.run[v];
-        if (run.y > g.ws.piece || (run.y == 0 && g.base.p == g.dtable.p)) return;
-        bin = lane;
-        start = run.x;
-        count = run.y;
+    const OwnerOf o = find_owner(g.ws, 1 << log_owners, piece);
+    if (o.owner < 0) return;
+    // the owner's long run that the piece is of: the last to begin at or before it
+    const int j = piece - o.before, runs = g.ws.owner[o.owner].y;
+    const int4* list = g.ws.longs + ((int64_t)o.owner << kSortLogBins);
+    int4 run = make_int4(0, 0, 0, 0);
+    for (int i0 = 0; i0 < runs; i0 += 32) {
+        const int4 r = i0 + lane < runs ? list[i0 + lane] : make_int4(0, 0, 0, 0x7fffffff);
+        const unsigned m = __ballot_sync(0xffffffffu, r.w <= j);
+        if (m == 0) break;
+        const int src = 31 - __clz(m);
+        run.y = __shfl_sync(0xffffffffu, r.y, src);
+        run.z = __shfl_sync(0xffffffffu, r.z, src);
+        run.w = __shfl_sync(0xffffffffu, r.w, src);
     }
+    if (lane > 0) return;
+    start = run.y + (j - run.w) * g.ws.piece;
+    count = min(g.ws.piece, run.y + run.z - start);
 }
 
 // Copies one unit to shared memory, asynchronously where the size allows it.
@@ -487,9 +483,9 @@ __device__ __forceinline__ void stage_unit(Raw* dst, const char* src)
         *dst = *reinterpret_cast<const Raw*>(src);
 }
 
-template <int DDT, int GDT, int W>
+template <int DDT, int GDT, int W, bool IN_PLACE>
 __global__ void __launch_bounds__(kBlock, kRowsBlocks)
-    k_emb_rows(EmbGrad g, int tile_units, int log_owners, int group)
+    k_emb_rows(EmbGrad g, int tile_units, int log_owners, int group, int per_owner)
 {
     constexpr int kAhead = 4;
     constexpr int kGB = bytes_of(GDT), kDB = bytes_of(DDT);
@@ -502,98 +498,125 @@ __global__ void __launch_bounds__(kBlock, kRowsBlocks)
     const bool on = (int)threadIdx.x < tile_units && (int64_t)unit * W < g.D;
     const char* bcol = g.base.p + (int64_t)unit * W * kGB;
     char* gcol = g.dtable.p + (int64_t)unit * W * kGB;
-    const int64_t bld = g.base.ld * kGB, gld = g.dtable.ld * kGB;
-    const bool has_base = g.base.p != nullptr, in_place = g.base.p == g.dtable.p;
-    // the group's rows: row0, row0 + owners, ...; owners vary fastest, so that the
+    const char* dcol = g.dout.p + (int64_t)unit * W * kDB;
+    const int64_t bld = g.base.ld * kGB, gld = g.dtable.ld * kGB, dld = g.dout.ld * kDB;
+    const bool has_base = g.base.p != nullptr;
+    // pieces first, then the owners' groups; owners vary fastest, so that the
     // blocks under way together write neighbouring rows
     const int64_t b = (int64_t)blockIdx.x - g.ws.pieces;
-    const int64_t row0 = b < 0 ? 0 : ((b >> log_owners) * group << log_owners) +
-                                         (b & ((1 << log_owners) - 1));
-    const auto row_of = [&](int bin) { return row0 + ((int64_t)bin << log_owners); };
-    if (b >= 0 && has_base && !in_place && on)
-        for (int i = 0; i < group && row_of(i) < g.V; ++i)
-            stage_unit(own + i * blockDim.x, bcol + row_of(i) * bld);
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
-        int bin, start, count;
-        find_segment(g, blockIdx.x, row0, log_owners, group, bin, start, count);
-        const unsigned below = (1u << lane) - 1u;
-        const unsigned empty = __ballot_sync(0xffffffffu, count == 0);
-        const unsigned full = __ballot_sync(0xffffffffu, count > 0);
-        int end = max(count, 0);
-#pragma unroll
-        for (int o = 1; o < kSegments; o <<= 1) {
-            const int up = __shfl_up_sync(0xffffffffu, end, o);
-            if (lane >= o) end += up;
-        }
-        if (count == 0) sg.empty_bin[__popc(empty & below)] = bin;
-        if (count > 0) {
-            const int k = __popc(full & below);
-            sg.bin[k] = bin;
-            sg.start[k] = start;
-            sg.first[k] = end - count;
-        }
-        if (lane == kSegments - 1) {
-            sg.empty = __popc(empty);
-            sg.full = __popc(full);
-            sg.items = end;
-        }
-    }
-    __syncthreads();
-    const int n = sg.items, full = sg.full, empty = sg.empty;
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        int k = 0;
-        for (int q = 1; q < full; ++q) k = sg.first[q] <= i ? q : k;
-        sg.item[i] = g.ws.order[sg.start[k] + i - sg.first[k]];
-    }
-    if (in_place && b >= 0 && on)
-        for (int k = 0; k < full; ++k)
-            stage_unit(own + sg.bin[k] * blockDim.x, bcol + row_of(sg.bin[k]) * bld);
-    __syncthreads();
-    if (!on) return;
-    const char* dcol = g.dout.p + (int64_t)unit * W * kDB;
-    const int64_t dld = g.dout.ld * kDB;
-    typename Unit<DDT, W>::Raw raw[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-        if (u < n) raw[u] = Unit<DDT, W>::load(dcol + sg.item[u] * dld);
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    for (int i = 0; i < empty; ++i) {
-        const int bin = sg.empty_bin[i];
-        float x[W] = {};
-        if (has_base) Unit<GDT, W>::unpack(own[bin * blockDim.x], x);
-        Unit<GDT, W>::store(gcol + row_of(bin) * gld, x);
-    }
-    if (n == 0) return;
-    int k = 0, end = full > 1 ? sg.first[1] : n;    // the segment at hand
-    float acc[W] = {};
-    for (int i0 = 0; i0 < n; i0 += kAhead) {
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int i = i0 + u;
-            if (i >= n) break;
-            float x[W];
-            Unit<DDT, W>::unpack(raw[u], x);
-#pragma unroll
-            for (int j = 0; j < W; ++j) acc[j] = __fadd_rn(acc[j], x[j]);
-            if (i + kAhead < n) raw[u] = Unit<DDT, W>::load(dcol + sg.item[i + kAhead] * dld);
-            if (i + 1 == end) {
-                const int bin = sg.bin[k];
-                if (bin >= 0) {
-                    float y[W] = {};
-                    if (has_base) Unit<GDT, W>::unpack(own[bin * blockDim.x], y);
-#pragma unroll
-                    for (int j = 0; j < W; ++j) y[j] = __fmaf_rn(g.scale, acc[j], y[j]);
-                    Unit<GDT, W>::store(gcol + row_of(bin) * gld, y);
-                } else {
-                    store_partial<W>(g.ws.partial + blockIdx.x * g.ws.Dpad + (int64_t)unit * W, acc);
+    const int owner = (int)(b & ((1 << log_owners) - 1));
+    const int4* shorts = g.ws.shorts + ((int64_t)owner << kSortLogBins);
+    const int present = IN_PLACE && b >= 0 ? g.ws.owner[owner].z : 0;
+    for (int64_t j = b >> log_owners;; j += per_owner) {      // the owner's j-th group
+        if (IN_PLACE && b >= 0 && j * group >= present) return;
+        const int64_t row0 = owner + (j * group << log_owners);
+        if (b >= 0 && has_base && !IN_PLACE && on)
+            for (int i = 0; i < group; ++i) {
+                const int64_t row = row0 + ((int64_t)i << log_owners);
+                if (row < g.V) stage_unit(own + i * blockDim.x, bcol + row * bld);
+            }
+        if (threadIdx.x < 32) {
+            const int lane = threadIdx.x;
+            int row = -1, start = 0, count = -1;
+            if (b < 0) {
+                find_piece(g, blockIdx.x, log_owners, start, count);
+            } else if (IN_PLACE) {
+                if (lane < group && j * group + lane < present) {
+                    const int4 r = shorts[j * group + lane];
+                    row = r.x;
+                    start = r.y;
+                    count = r.z;
                 }
-                ++k;
-                end = k + 1 < full ? sg.first[k + 1] : n;
+            } else {
+                const int64_t v = row0 + ((int64_t)lane << log_owners);
+                if (lane < group && v < g.V) {
+                    const int2 run = g.ws.run[v];
+                    row = (int)v;
+                    start = run.x;
+                    if (run.y <= g.ws.piece) count = run.y;
+                }
+            }
+            const unsigned below = (1u << lane) - 1u;
+            const unsigned empty = __ballot_sync(0xffffffffu, count == 0);
+            const unsigned full = __ballot_sync(0xffffffffu, count > 0);
+            int end = max(count, 0);
 #pragma unroll
-                for (int j = 0; j < W; ++j) acc[j] = 0.0f;
+            for (int o = 1; o < kSegments; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, end, o);
+                if (lane >= o) end += up;
+            }
+            if (lane < kSegments) sg.row[lane] = row;
+            if (count == 0) sg.empty[__popc(empty & below)] = lane;
+            if (count > 0) {
+                const int k = __popc(full & below);
+                sg.slot[k] = lane;
+                sg.start[k] = start;
+                sg.first[k] = end - count;
+            }
+            if (lane == kSegments - 1) {
+                sg.empties = __popc(empty);
+                sg.full = __popc(full);
+                sg.items = end;
             }
         }
+        __syncthreads();
+        const int n = sg.items, full = sg.full;
+        for (int i = threadIdx.x; i < n; i += blockDim.x) {
+            int k = 0;
+            for (int q = 1; q < full; ++q) k = sg.first[q] <= i ? q : k;
+            sg.item[i] = g.ws.order[sg.start[k] + i - sg.first[k]];
+        }
+        if (IN_PLACE && b >= 0 && on)
+            for (int k = 0; k < full; ++k)
+                stage_unit(own + sg.slot[k] * blockDim.x, bcol + sg.row[sg.slot[k]] * bld);
+        __syncthreads();
+        if (on) {
+            typename Unit<DDT, W>::Raw raw[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (u < n) raw[u] = Unit<DDT, W>::load(dcol + sg.item[u] * dld);
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            if (!IN_PLACE)
+                for (int i = 0; i < sg.empties; ++i) {
+                    const int slot = sg.empty[i];
+                    float x[W] = {};
+                    if (has_base) Unit<GDT, W>::unpack(own[slot * blockDim.x], x);
+                    Unit<GDT, W>::store(gcol + sg.row[slot] * gld, x);
+                }
+            int k = 0, end = full > 1 ? sg.first[1] : n;    // the segment at hand
+            float acc[W] = {};
+            for (int i0 = 0; i0 < n; i0 += kAhead) {
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int i = i0 + u;
+                    if (i >= n) break;
+                    float x[W];
+                    Unit<DDT, W>::unpack(raw[u], x);
+#pragma unroll
+                    for (int q = 0; q < W; ++q) acc[q] = __fadd_rn(acc[q], x[q]);
+                    if (i + kAhead < n) raw[u] = Unit<DDT, W>::load(dcol + sg.item[i + kAhead] * dld);
+                    if (i + 1 == end) {
+                        const int slot = sg.slot[k], row = sg.row[slot];
+                        if (row >= 0) {
+                            float y[W] = {};
+                            if (has_base) Unit<GDT, W>::unpack(own[slot * blockDim.x], y);
+#pragma unroll
+                            for (int q = 0; q < W; ++q) y[q] = __fmaf_rn(g.scale, acc[q], y[q]);
+                            Unit<GDT, W>::store(gcol + row * gld, y);
+                        } else {
+                            store_partial<W>(
+                                g.ws.partial + blockIdx.x * g.ws.Dpad + (int64_t)unit * W, acc);
+                        }
+                        ++k;
+                        end = k + 1 < full ? sg.first[k + 1] : n;
+#pragma unroll
+                        for (int q = 0; q < W; ++q) acc[q] = 0.0f;
+                    }
+                }
+            }
+        }
+        if (!IN_PLACE || b < 0) return;
+        __syncthreads();
     }
 }
 
@@ -688,14 +711,19 @@ cudaError_t rows_typed(const EmbGrad& g, cudaStream_t s)
     const int64_t units = (g.D + W - 1) / W, tiles = (units + kBlock - 1) / kBlock;
     const int tile_units = (int)((units + tiles - 1) / tiles);
     const int log_owners = emb_log_owners(g.V);
-    const int threads = (tile_units + 31) / 32 * 32, group = threads <= 128 ? 4 : kSegments;
+    const bool in_place = g.base.p == g.dtable.p;
+    const int threads = (tile_units + 31) / 32 * 32, group = threads <= 128 && !in_place ? 4 : kSegments;
     const int64_t groups = (emb_bins(g.V, log_owners) + group - 1) / group;
-    const int64_t blocks = g.ws.pieces + (groups << log_owners);
+    // in place: blocks for the ids that an owner can expect to have tokens
+    const int64_t expect = ((g.T >> log_owners) + group) / group;
+    const int64_t per_owner = in_place ? std::min(groups, expect) : groups;
+    const int64_t blocks = g.ws.pieces + (per_owner << log_owners);
     if (blocks > kMaxGrid || tiles > 65535) return cudaErrorInvalidConfiguration;
     const size_t smem =
         g.base.p != nullptr ? size_t(group) * threads * sizeof(typename Unit<GDT, W>::Raw) : 0;
-    return launch_kernel(k_emb_rows<DDT, GDT, W>, dim3((unsigned)blocks, (unsigned)tiles),
-                         dim3(threads), smem, s, true, 0u, g, tile_units, log_owners, group);
+    return launch_kernel(in_place ? k_emb_rows<DDT, GDT, W, true> : k_emb_rows<DDT, GDT, W, false>,
+                         dim3((unsigned)blocks, (unsigned)tiles), dim3(threads), smem, s, true, 0u, g,
+                         tile_units, log_owners, group, (int)per_owner);
 }
 
 template <int GDT, int W>
@@ -735,23 +763,20 @@ cudaError_t launch_embedding(const Mat& table, const Ids& ids, int64_t T, int64_
 
 cudaError_t launch_emb_sort(const EmbGrad& g, cudaStream_t s)
 {
-    static SmemRaised raised32, raised64;
     set_last_kernel_name("lm_emb_sort");
     const int log_owners = emb_log_owners(g.V), bins = (int)emb_bins(g.V, log_owners);
     const auto bytes = [](int b) { return size_t(kSortWarps) * (kSortHits * sizeof(int2) + b * sizeof(int)); };
     const size_t most = bytes(kSortMaxBins), smem = bytes(bins);
     const dim3 grid(1u << log_owners), block(kSortThreads);
-    if (g.ids.it == DPZ_I64) {
-        const cudaError_t e =
-            allow_smem(raised64, reinterpret_cast<const void*>(k_emb_sort<int64_t>), most);
+    const auto launch_typed = [&](auto fn, SmemRaised& raised, const auto* ids) {
+        const cudaError_t e = allow_smem(raised, reinterpret_cast<const void*>(fn), most);
         if (e != cudaSuccess) return e;
-        return launch_kernel(k_emb_sort<int64_t>, grid, block, smem, s, true, 0u,
-                             static_cast<const int64_t*>(g.ids.p), g.T, g.V, log_owners, bins, g.ws);
-    }
-    const cudaError_t e = allow_smem(raised32, reinterpret_cast<const void*>(k_emb_sort<int>), most);
-    if (e != cudaSuccess) return e;
-    return launch_kernel(k_emb_sort<int>, grid, block, smem, s, true, 0u,
-                         static_cast<const int*>(g.ids.p), g.T, g.V, log_owners, bins, g.ws);
+        return launch_kernel(fn, grid, block, smem, s, true, 0u, ids, g.T, g.V, log_owners, bins, g.ws);
+    };
+    static SmemRaised raised32, raised64;
+    return g.ids.it == DPZ_I64
+               ? launch_typed(k_emb_sort<int64_t>, raised64, static_cast<const int64_t*>(g.ids.p))
+               : launch_typed(k_emb_sort<int>, raised32, static_cast<const int*>(g.ids.p));
 }
 
 cudaError_t launch_emb_rows(const EmbGrad& g, cudaStream_t s)
