@@ -446,13 +446,13 @@ __global__ void __launch_bounds__(NT + 32, kStepBlocks<NT>) k_distill_step(Disti
             const int end = min(i + per, max(have, will));
 #pragma unroll 4
             for (; i < min(end, both); ++i) {
-                map_vector<DT, NT>(own[i * NT], q + i * (NT * 16), true, fe);
+                map_vector<DT, false>(own[i * NT], q + i * (NT * 16), true, fe);
                 copy_async16(own + i * NT, np + i * (NT * 16));
             }
 #pragma unroll 1
             for (; i < end; ++i) {
                 if (i < have && !zero)
-                    map_vector<DT, NT>(own[i * NT], q + i * (NT * 16), same, f);
+                    map_vector<DT, false>(own[i * NT], q + i * (NT * 16), same, f);
                 if (i < will) copy_async16(own + i * NT, np + i * (NT * 16));
             }
             copy_commit();
@@ -495,7 +495,7 @@ cudaError_t resident_blocks(int stage, int* blocks)
 template <int DT, int NT>
 cudaError_t launch_step(const DistillArgs& a, cudaStream_t s)
 {
-    static SmemRaised raised;
+    static SmemRaisedOn raised;
     const int64_t bytes = row_bytes(a.V, DT);
     // two blocks where one cannot stage a row (4,096 rows of 50,257 fp32: 299 us,
     // 342 with one block that reads half of the row again; 2,048 of 128,256 bf16:
@@ -504,7 +504,7 @@ cudaError_t launch_step(const DistillArgs& a, cudaStream_t s)
     const int64_t vecs = (bytes / 16 + n - 1) / n + 1;
     const int stage = (int)std::min<int64_t>((vecs + NT - 1) / NT, kStageMax / (NT * 16));
     cudaError_t e =
-        allow_smem(raised, reinterpret_cast<const void*>(k_distill_step<DT, NT>), kStageMax);
+        raise_smem(raised, reinterpret_cast<const void*>(k_distill_step<DT, NT>), kStageMax);
     int blocks = 0;
     if (e == cudaSuccess) e = resident_blocks<DT, NT>(stage, &blocks);
     if (e != cudaSuccess) return e;

@@ -768,12 +768,12 @@ cudaError_t launch_emb_sort(const EmbGrad& g, cudaStream_t s)
     const auto bytes = [](int b) { return size_t(kSortWarps) * (kSortHits * sizeof(int2) + b * sizeof(int)); };
     const size_t most = bytes(kSortMaxBins), smem = bytes(bins);
     const dim3 grid(1u << log_owners), block(kSortThreads);
-    const auto launch_typed = [&](auto fn, SmemRaised& raised, const auto* ids) {
-        const cudaError_t e = allow_smem(raised, reinterpret_cast<const void*>(fn), most);
+    const auto launch_typed = [&](auto fn, SmemRaisedOn& raised, const auto* ids) {
+        const cudaError_t e = raise_smem(raised, reinterpret_cast<const void*>(fn), most);
         if (e != cudaSuccess) return e;
         return launch_kernel(fn, grid, block, smem, s, true, 0u, ids, g.T, g.V, log_owners, bins, g.ws);
     };
-    static SmemRaised raised32, raised64;
+    static SmemRaisedOn raised32, raised64;
     return g.ids.it == DPZ_I64
                ? launch_typed(k_emb_sort<int64_t>, raised64, static_cast<const int64_t*>(g.ids.p))
                : launch_typed(k_emb_sort<int>, raised32, static_cast<const int*>(g.ids.p));

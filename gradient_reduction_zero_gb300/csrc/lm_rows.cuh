@@ -597,8 +597,8 @@ __device__ __forceinline__ float logprob_of(float x, const Stat& s, const RowRes
 //
 // map_row writes f(x) for the elements of a slice, where f takes and gives
 // pairs.  An element is read and written by the same thread, so the output
-// may be the input.
-template <int DT, int NT, class F>
+// may be the input.  STREAM: stores that leave L2 first.
+template <int DT, bool STREAM = true, class F>
 __device__ __forceinline__ void map_vector(const uint4& w, char* q, bool same, F&& f)
 {
     constexpr int kB = El<DT>::kBytes, kV = El<DT>::kVec;
@@ -607,7 +607,8 @@ __device__ __forceinline__ void map_vector(const uint4& w, char* q, bool same, F
 #pragma unroll
     for (int j = 0; j < kV / 2; ++j) x[j] = f(x[j]);
     if (same) {
-        st16(q, El<DT>::pack(x));
+        if (STREAM) st16(q, El<DT>::pack(x));
+        else *reinterpret_cast<uint4*>(q) = El<DT>::pack(x);
     } else {
 #pragma unroll
         for (int j = 0; j < kV / 2; ++j) {
@@ -650,7 +651,7 @@ __device__ __forceinline__ void map_row(const char* row, char* out, const Slice&
 #pragma unroll
         for (int l = 0; l < kMapLoads; ++l)
             if (i + l * NT < s.hi)
-                map_vector<DT, NT>(w[l], out + body + (int64_t)(i + l * NT) * 16, same, f);
+                map_vector<DT>(w[l], out + body + (int64_t)(i + l * NT) * 16, same, f);
         i += kMapLoads * NT;
         map_load<DT, NT>(row, s, i, w);
     }
