@@ -22,8 +22,8 @@ int check_rows(int64_t T, int64_t V)
 
 int check_width(int64_t D)
 {
-    if (D < 1 || D >= (int64_t(1) << 24))
-        return fail(DPZ_ERR_INVALID_ARG, "D = %lld is outside [1, 2^24)", (long long)D);
+    if (D < 1 || D >= (int64_t(1) << 20))
+        return fail(DPZ_ERR_INVALID_ARG, "D = %lld is outside [1, 2^20)", (long long)D);
     return DPZ_OK;
 }
 
@@ -62,10 +62,11 @@ int check_ids(const void* p, int it, int64_t n, const char* what)
     return n > 0 ? check_addr(p, what, it == DPZ_I32 ? 4 : 8) : DPZ_OK;
 }
 
-int check_positive(float x, const char* what)
+// A factor of the logits: beyond 1e30 the difference of two of them overflows.
+int check_factor(float x, const char* what)
 {
-    if (!(x > 0.0f) || !std::isfinite(x))
-        return fail(DPZ_ERR_INVALID_ARG, "%s = %g must be finite and positive", what, x);
+    if (!(x > 0.0f) || x > 1e30f)
+        return fail(DPZ_ERR_INVALID_ARG, "%s = %g is outside (0, 1e30]", what, x);
     return DPZ_OK;
 }
 
@@ -190,7 +191,7 @@ DPZ_API int lm_logprobs(const void* logits, int64_t ld, int64_t T, int64_t V, in
 {
     DPZ_TRY(check_rows(T, V));
     DPZ_TRY(check_mat(logits, ld, T, V, dtype, "logits"));
-    DPZ_TRY(check_positive(scale, "scale"));
+    DPZ_TRY(check_factor(scale, "scale"));
     DPZ_TRY(check_ids(targets, itype, logprob ? T : 0, "targets"));
     if (targets != nullptr && logprob == nullptr && T > 0)
         return fail(DPZ_ERR_INVALID_ARG, "logprob is NULL");
@@ -227,7 +228,7 @@ DPZ_API int lm_logprobs_grad(const void* logits, int64_t ld, int64_t T, int64_t 
     DPZ_TRY(check_rows(T, V));
     DPZ_TRY(check_mat(logits, ld, T, V, dtype, "logits"));
     DPZ_TRY(check_mat(dlogits, ld_dlogits, T, V, dtype, "dlogits"));
-    DPZ_TRY(check_positive(scale, "scale"));
+    DPZ_TRY(check_factor(scale, "scale"));
     DPZ_TRY(check_ids(targets, itype, T, "targets"));
     if (T > 0) {
         DPZ_TRY(check_addr(lse, "lse", 4));
@@ -265,9 +266,9 @@ static int distill_common(const void* logits, int64_t ld, int64_t T, int64_t V, 
     DPZ_TRY(check_mat(logits, ld, T, V, dtype, "logits"));
     if (K < 1 || K > DPZ_LM_MAX_TEACHER)
         return fail(DPZ_ERR_INVALID_ARG, "K = %d is outside 1..%d", K, DPZ_LM_MAX_TEACHER);
-    DPZ_TRY(check_positive(temperature, "temperature"));
+    DPZ_TRY(check_factor(temperature, "temperature"));
     const float inv_tau = 1.0f / temperature;
-    DPZ_TRY(check_positive(inv_tau, "1 / temperature"));
+    DPZ_TRY(check_factor(inv_tau, "1 / temperature"));
     DPZ_TRY(check_ids(teacher_ids, itype, T, "teacher_ids"));
     DPZ_TRY(check_mat(teacher_logits, K, T, K, tdtype, "teacher_logits"));
     if (T > 0) {

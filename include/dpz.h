@@ -330,7 +330,7 @@ DPZ_API int dp_grad_global_norm_static(const void* grads, int64_t P, int N,
  * on the launch or on the order of atomics.
  *
  *   T   tokens (rows), 0 <= T < 2^31;   V  vocabulary, 1 <= V < 2^30
- *   D   width of an embedding row, 1 <= D < 2^24
+ *   D   width of an embedding row, 1 <= D < 2^20
  *   Matrices are row-major with a row stride in elements (ld_*, at least the
  *   row's length), so that a table inside an arena or logits with padded rows
  *   need no copy.  Any stride and any element-aligned address is accepted;
@@ -340,10 +340,12 @@ DPZ_API int dp_grad_global_norm_static(const void* grads, int64_t P, int N,
  *   rounding to the output's type at the end.
  *   A call with T = 0 writes no row (lm_embedding_grad still writes dtable).
  *   Errors are as above: DPZ_ERR_INVALID_ARG for a NULL pointer, a size out
- *   of range, a stride below the row length, an unknown type, a scale or
- *   temperature that is not finite (or not positive where it scales logits)
- *   or buffers that overlap except where a call allows it; DPZ_ERR_ALIGN for
- *   an address that is not a multiple of its element.
+ *   of range, a stride below the row length, an unknown type, a scale that is
+ *   not finite, a factor of the logits (scale, temperature or its inverse)
+ *   outside (0, 1e30], or buffers of which one is written and that overlap,
+ *   except where a call allows it (two matrices of one stride may interleave,
+ *   as column ranges of a larger one do); DPZ_ERR_ALIGN for an address that is
+ *   not a multiple of its element.
  * ------------------------------------------------------------------- */
 
 /* id types */

@@ -121,6 +121,37 @@ def test_lookup_grad_long_runs(dpz, T, D, pattern):
     assert torch.equal(a, b)                             # the same bits again
 
 
+@pytest.mark.parametrize("T,D", [(200, 20), (5000, 12), (60007, 8), (120011, 3)])
+@pytest.mark.parametrize("pattern", ["one", "mixed", "runs65"])
+@pytest.mark.parametrize("base", ["none", "same"])
+def test_lookup_grad_many_tokens(dpz, T, D, pattern, base):
+    """Past the numbers of tokens at which the length of the pieces changes and a
+    warp's list of its own tokens overflows, in place too."""
+    V = 1000
+    t = torch.arange(T, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(T)
+    ids = {"one": torch.full_like(t, 640),
+           "mixed": torch.where(torch.rand(T, generator=g, device="cuda") < 0.5, t % 3,
+                                torch.randint(-1, V + 1, (T,), generator=g, device="cuda")),
+           "runs65": (t // 65) % V}[pattern]
+    _grad_case(dpz, ids.int() if T % 2 else ids, V, D, "f32", "f32", base, seed=T)
+
+
+def test_lookup_grad_stays_in_its_workspace(dpz):
+    """The bytes behind the workspace keep their values, whatever the runs."""
+    for T, V, D in ((1, 1, 1), (33, 40, 24), (4097, 129, 40), (65537, 700, 8)):
+        need = dpz.lib.lm_embedding_workspace_bytes(T, V, D)
+        ws = torch.full((need + 4096,), 0x5a, dtype=torch.uint8, device="cuda")
+        g = torch.Generator(device="cuda").manual_seed(T)
+        ids = torch.where(torch.rand(T, generator=g, device="cuda") < 0.7, 0,
+                          torch.randint(0, V, (T,), generator=g, device="cuda"))
+        dout = torch.ones(T, D, device="cuda")
+        dt = torch.empty(V, D, device="cuda")
+        dpz.lm_embedding_grad(dout, ids, dt, ws[:need])
+        assert bool((ws[need:] == 0x5a).all())
+        assert torch.equal(dt[:, 0].cpu(), torch.bincount(ids.cpu(), minlength=V).float())
+
+
 @pytest.mark.parametrize("V", [127, 128, 129, 131072, 131073, 300001])
 def test_lookup_grad_vocabularies(dpz, V):
     g = torch.Generator(device="cuda").manual_seed(V)
@@ -442,6 +473,43 @@ def test_same_bits_every_run_and_on_a_side_stream(dpz):
     for b in (run(None), run(side)):
         for p, q in zip(a, b):
             assert torch.equal(bits(p), bits(q))
+
+
+def test_calls_in_a_graph(dpz):
+    """Captured once and replayed on new inputs: the bits of direct calls."""
+    T, V, K, D = 150, 3001, 7, 40
+    x, y = _logits(T, V, "bf16", "plain", 1), torch.randint(0, V, (T,), device="cuda")
+    ids, t = _teacher(T, V, K, "f32", 2, False)
+    w, dout = torch.randn(T, device="cuda"), torch.randn(T, D, device="cuda")
+    lp, lse, H, loss = (torch.empty(T, device="cuda") for _ in range(4))
+    ti, tl = torch.empty(T, K, dtype=torch.int64, device="cuda"), torch.empty(T, K, device="cuda")
+    d1, d2, d3 = torch.empty_like(x), torch.empty_like(x), torch.empty(V, D, device="cuda")
+    h = torch.empty(T, D, device="cuda")
+    ws = dpz.lm_embedding_workspace(T, V, D)
+    out = (lp, lse, H, ti, tl, d1, loss, d2, d3, h)
+
+    def calls():
+        dpz.lm_logprobs(x, y, lp, lse=lse, entropy=H, top_ids=ti, top_logprobs=tl)
+        dpz.lm_logprobs_grad(x, y, lse, w, d1, entropy=H, dentropy=w)
+        dpz.lm_distill_step(x, ids, t, w, loss, d2)
+        dpz.lm_embedding_grad(dout, y, d3, ws)
+        dpz.lm_embedding(d3, y, h, scale=2.0)
+
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    x.copy_(_logits(T, V, "bf16", "some", 9))
+    y.copy_(torch.randint(0, V, (T,), device="cuda"))
+    for o in out:
+        o.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [o.clone() for o in out]
+    calls()
+    for a, b in zip(got, out):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
 def test_offsets_beyond_32_bits(dpz):

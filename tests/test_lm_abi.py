@@ -43,7 +43,8 @@ CASES = [
     ("lm_embedding", EMB, EMB_D, [
         (dict(table=None), 1), (dict(ids=None), 1), (dict(out=None), 1), (dict(T=-1), 1),
         (dict(V=0), 1), (dict(D=0), 1), (dict(V=1 << 30), 1), (dict(D=1 << 24), 1),
-        (dict(T=1 << 31), 1), (dict(ld_table=63), 1), (dict(ld_out=63), 1), (dict(wdt=2), 1),
+        (dict(T=1 << 31), 1), (dict(D=1 << 20, ld_table=1 << 20, ld_out=1 << 20), 1),
+        (dict(ld_table=63), 1), (dict(ld_out=63), 1), (dict(wdt=2), 1),
         (dict(odt=5), 1), (dict(it=0), 1), (dict(scale=NAN), 1), (dict(scale=INF), 1),
         (dict(table=A + 1), 2), (dict(ids=A + GB + 4), 2), (dict(out=A + 64), 1),
         (dict(odt=0, out=A + 2 * GB + 2), 2), (dict(ld_table=1 << 39, V=1 << 20), 1)]),
@@ -57,7 +58,7 @@ CASES = [
     ("lm_logprobs", LP, LP_D, [
         (dict(x=None), 1), (dict(y=None), 1), (dict(lp=None), 1), (dict(K=-1), 1), (dict(K=33), 1),
         (dict(V=3, K=4), 1), (dict(ti=None), 1), (dict(tl=None), 1), (dict(scale=0.0), 1),
-        (dict(scale=-1.0), 1), (dict(scale=NAN), 1), (dict(ld=99), 1), (dict(dt=2), 1),
+        (dict(scale=-1.0), 1), (dict(scale=NAN), 1), (dict(scale=2e30), 1), (dict(ld=99), 1), (dict(dt=2), 1),
         (dict(it=1), 1), (dict(lse=A + 2 * GB + 4), 1), (dict(lse=A + 3 * GB + 2), 2),
         (dict(x=A + 1), 2), (dict(H=A + 40), 1), (dict(ti=A + 5 * GB + 4), 2)]),
     ("lm_logprobs_grad", LG, LG_D, [
@@ -68,7 +69,7 @@ CASES = [
         (dict(x=None), 1), (dict(ids=None), 1), (dict(t=None), 1), (dict(w=None), 1),
         (dict(loss=None), 1), (dict(dx=None), 1), (dict(K=0), 1), (dict(K=257), 1),
         (dict(tau=0.0), 1), (dict(tau=-2.0), 1), (dict(tau=INF), 1), (dict(tau=NAN), 1),
-        (dict(tau=1e-42), 1), (dict(tdt=2), 1), (dict(dx=A + 2), 1), (dict(dx=A, ld_dx=101), 1),
+        (dict(tau=1e-42), 1), (dict(tau=1e-31), 1), (dict(tau=1e31), 1), (dict(tdt=2), 1), (dict(dx=A + 2), 1), (dict(dx=A, ld_dx=101), 1),
         (dict(loss=A + 5 * GB), 1), (dict(t=A + 2 * GB + 2), 2), (dict(ld=99), 1)]),
 ]
 
