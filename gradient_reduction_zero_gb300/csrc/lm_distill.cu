@@ -183,9 +183,10 @@ __device__ __forceinline__ void write_teacher_part(const DistillArgs& a, const T
 
 // ------------------------------------------------------------ loss alone
 
+// A row per block (or cluster) of NT threads, and a warp more that loads the
+// entries meanwhile.
 template <int DT, int NT>
-__global__ void __launch_bounds__(NT, (DT == DPZ_F32 ? 7 : 6) * kRowThreads / NT)
-    k_distill(DistillArgs a)
+__global__ void __launch_bounds__(NT + 32, kLossBlocks<DT, NT>) k_distill(DistillArgs a)
 {
     __shared__ Teacher w;
     __shared__ StatShared<NT> ssh;
@@ -194,9 +195,13 @@ __global__ void __launch_bounds__(NT, (DT == DPZ_F32 ? 7 : 6) * kRowThreads / NT
     pdl_enter();
     const int64_t t = blockIdx.x >> (31 - __clz(n));
     const char* row = a.x.p + t * a.x.ld * El<DT>::kBytes;
+    if (threadIdx.x >= NT) {
+        if (rank == 0) load_teacher<DT>(a, t, row, 0, a.V, w);
+        row_stat_beside(n);
+        return;
+    }
     const Slice sl = row_slice<DT>(row, a.V, rank, n);
     const StatScale k(a.inv_tau);
-    if (rank == 0 && threadIdx.x >= NT - 32) load_teacher<DT>(a, t, row, 0, a.V, w);
     RefStat<DT> rs;
     thread_rows<DT, NT>(rs, row, sl, sl.lo + threadIdx.x, k);
     Stat own = rs.get();
@@ -211,8 +216,12 @@ __global__ void __launch_bounds__(NT, (DT == DPZ_F32 ? 7 : 6) * kRowThreads / NT
 
 // ------------------------------------------------------------ gradient alone
 
+// Blocks (row, slice) of NT threads, and a warp more that loads the entries
+// meanwhile.  In place the others wait for it before they write, since it
+// reads logits; otherwise they do not, and a row that turns out to have no
+// entry is written again.
 template <int DT, int NT>
-__global__ void __launch_bounds__(NT, 8 * kRowThreads / NT) k_distill_grad(DistillArgs a)
+__global__ void __launch_bounds__(NT + 32, kGradBlocks<NT>) k_distill_grad(DistillArgs a)
 {
     __shared__ Teacher w;
     __shared__ TokenHash hash;
@@ -221,31 +230,31 @@ __global__ void __launch_bounds__(NT, 8 * kRowThreads / NT) k_distill_grad(Disti
     const int64_t t = blockIdx.x;
     const char* row = a.x.p + t * a.x.ld * El<DT>::kBytes;
     char* out = a.dx.p + t * a.dx.ld * El<DT>::kBytes;
+    const bool in_place = row == out;
     const float wt = a.dloss[t], lse = a.lse_in[t];
     if (wt == 0.0f || lse == -INFINITY) {
-        zero_row<DT, NT>(out, a.V, rank, n);
+        if (threadIdx.x < NT) zero_row<DT, NT>(out, a.V, rank, n);
         return;
     }
     const Slice sl = row_slice<DT>(row, a.V, rank, n);
-    // the row's first vectors come while the entries do
-    uint4 v[kMapLoads];
-    map_load<DT, NT>(row, sl, sl.lo + threadIdx.x, v);
-    // in place, other blocks' slices may be overwritten already
-    if (threadIdx.x >= NT - 32) {
+    const StudentGrad f(a.inv_tau, lse, wt * a.inv_tau);
+    if (threadIdx.x >= NT) {
         clear_hash(hash);
+        // other blocks' slices may be overwritten already
         load_teacher<DT>(a, t, row, sl.first, sl.last, w);
         const bool repeats = find_repeats(w.id, a.K, hash);
-        if (threadIdx.x == NT - 32) w.repeats = repeats;
-    }
-    __syncthreads();
-    if (!w.any) {
-        zero_row<DT, NT>(out, a.V, rank, n);
+        if (threadIdx.x == NT) w.repeats = repeats;
+        if (in_place) __syncthreads();
+        __syncthreads();
+        if (w.any) write_teacher_part<DT>(a, w, sl, f, out);
         return;
     }
-    const StudentGrad f(a.inv_tau, lse, wt * a.inv_tau);
+    uint4 v[kMapLoads];
+    map_load<DT, NT>(row, sl, sl.lo + threadIdx.x, v);
+    if (in_place) __syncthreads();
     map_row<DT, NT>(row, out, sl, sl.lo + threadIdx.x, v, f);
     __syncthreads();
-    if (threadIdx.x >= NT - 32) write_teacher_part<DT>(a, w, sl, f, out);
+    if (!w.any) zero_row<DT, NT>(out, a.V, rank, n);
 }
 
 // ------------------------------------------------------------ both in one pass
@@ -537,7 +546,8 @@ cudaError_t launch_distill(const DistillArgs& a, cudaStream_t s)
         const unsigned n = row_cluster(a.T, bytes, nt);
         auto fn = small ? (b ? k_distill<DPZ_BF16, kShortThreads> : k_distill<DPZ_F32, kShortThreads>)
                         : (b ? k_distill<DPZ_BF16, kRowThreads> : k_distill<DPZ_F32, kRowThreads>);
-        return launch_kernel(fn, dim3((unsigned)a.T * n), dim3(nt), 0, s, true, n > 1 ? n : 0u, a);
+        return launch_kernel(fn, dim3((unsigned)a.T * n), dim3(nt + 32), 0, s, true, n > 1 ? n : 0u,
+                             a);
     }
     set_last_kernel_name("lm_distill_grad");
     // two independent blocks per row share the last wave better than one (1,000
@@ -546,7 +556,7 @@ cudaError_t launch_distill(const DistillArgs& a, cudaStream_t s)
     const unsigned n = std::max(row_cluster(a.T, bytes, nt), small ? 1u : 2u);
     auto fn = small ? (b ? k_distill_grad<DPZ_BF16, kShortThreads> : k_distill_grad<DPZ_F32, kShortThreads>)
                     : (b ? k_distill_grad<DPZ_BF16, kRowThreads> : k_distill_grad<DPZ_F32, kRowThreads>);
-    return launch_kernel(fn, dim3((unsigned)a.T, n), dim3(nt), 0, s, true, 0u, a);
+    return launch_kernel(fn, dim3((unsigned)a.T, n), dim3(nt + 32), 0, s, true, 0u, a);
 }
 
 }  // namespace dpz

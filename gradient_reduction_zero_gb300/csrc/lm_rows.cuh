@@ -564,6 +564,20 @@ __device__ __forceinline__ Stat row_stat(Stat s, const StatScale& k, StatShared<
     return s;
 }
 
+// The barriers of row_stat for a warp beside the NT threads, which works until
+// then and has nothing to add.
+__device__ __forceinline__ void row_stat_beside(unsigned n)
+{
+    __syncthreads();
+    if (n == 1) {
+        __syncthreads();
+        return;
+    }
+    cluster_wait();
+    cluster_arrive_release();
+    cluster_wait();
+}
+
 // lse and entropy of a row's statistics; m NaN or +inf: NaN, m -inf: -inf and 0.
 struct RowResult {
     float lse, log2S, entropy;
@@ -687,6 +701,10 @@ constexpr int64_t kShortRow = 16384;
 // The distillation step's blocks and the most shared memory each stages.
 constexpr int kStepThreads = 256;
 constexpr int kStageMax = 100 * 1024;
+template <int DT, int NT>
+constexpr int kLossBlocks = NT == kRowThreads ? (DT == DPZ_F32 ? 6 : 5) : 20;
+template <int NT>
+constexpr int kGradBlocks = NT == kRowThreads ? 7 : 20;   // on an SM, at least
 template <int NT>
 constexpr int kStepBlocks = NT == kStepThreads ? 2 : 8;   // on an SM, at least
 
