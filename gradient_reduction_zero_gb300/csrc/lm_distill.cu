@@ -551,8 +551,9 @@ cudaError_t launch_distill(const DistillArgs& a, cudaStream_t s)
     }
     set_last_kernel_name("lm_distill_grad");
     // two independent blocks per row share the last wave better than one (1,000
-    // rows of 32,000 fp32: 45.5 us, 50 with one, 53 with four, each of which loads
-    // the entries again)
+    // rows of 32,000 fp32: 41.4 us, 45.7 with one).  Four blocks take 40.8 there,
+    // but each loads the entries again, which shorter rows pay for (a row of 32 KB
+    // has 8 KB a block: 52 to 54 us where two take 33).
     const unsigned n = std::max(row_cluster(a.T, bytes, nt), small ? 1u : 2u);
     auto fn = small ? (b ? k_distill_grad<DPZ_BF16, kShortThreads> : k_distill_grad<DPZ_F32, kShortThreads>)
                     : (b ? k_distill_grad<DPZ_BF16, kRowThreads> : k_distill_grad<DPZ_F32, kRowThreads>);

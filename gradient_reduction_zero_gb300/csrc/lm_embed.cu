@@ -243,8 +243,8 @@ __device__ __forceinline__ int block_scan(int x, int* warp_tot)
 // prefix sums of those counts place each token.  Warps take consecutive
 // ranges of positions, so the order within an id is that of positions.  The
 // long runs (more than ws.piece terms) are listed for the kernels that sum
-// them in pieces.  A warp keeps its hits in shared memory; one with more than kSortHits (a very
-// frequent id) reads its range again.
+// them in pieces.  A warp keeps its hits in shared memory; one with more than
+// kSortHits (a very frequent id) reads its range again.
 template <class ID>
 __global__ void __launch_bounds__(kSortThreads)
     k_emb_sort(const ID* __restrict__ ids, int64_t T, int64_t V, int log_owners, int bins, EmbWs ws)
