@@ -231,12 +231,12 @@ __global__ void __launch_bounds__(NT + 32, kGradBlocks<NT>) k_distill_grad(Disti
     const char* row = a.x.p + t * a.x.ld * El<DT>::kBytes;
     char* out = a.dx.p + t * a.dx.ld * El<DT>::kBytes;
     const bool in_place = row == out;
+    const Slice sl = row_slice<DT>(row, a.V, rank, n);
     const float wt = a.dloss[t], lse = a.lse_in[t];
     if (wt == 0.0f || lse == -INFINITY) {
-        if (threadIdx.x < NT) zero_row<DT, NT>(out, a.V, rank, n);
+        if (threadIdx.x < NT) zero_slice<DT, NT>(out, sl);
         return;
     }
-    const Slice sl = row_slice<DT>(row, a.V, rank, n);
     const StudentGrad f(a.inv_tau, lse, wt * a.inv_tau);
     if (threadIdx.x >= NT) {
         clear_hash(hash);
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(NT + 32, kGradBlocks<NT>) k_distill_grad(Disti
     if (in_place) __syncthreads();
     map_row<DT, NT>(row, out, sl, sl.lo + threadIdx.x, v, f);
     __syncthreads();
-    if (!w.any) zero_row<DT, NT>(out, a.V, rank, n);
+    if (!w.any) zero_slice<DT, NT>(out, sl);
 }
 
 // ------------------------------------------------------------ both in one pass
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(NT + 32, kStepBlocks<NT>) k_distill_step(Disti
             }
             copy_commit();
         }
-        if (zero) zero_row<DT, NT>(out, a.V, rank, n);
+        if (zero) zero_slice<DT, NT>(out, sl);
         else {
             uint4 v[kMapLoads];
             map_load<DT, NT>(row, sl, first + have * NT, v);

@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(NT) k_logprobs_grad(LogprobGradArgs a)
     const float h = a.dentropy != nullptr ? a.dentropy[t] : 0.0f;
     const float lse = a.lse[t];
     if ((g == 0.0f && h == 0.0f) || lse == -INFINITY) {
-        zero_row<DT, NT>(out, a.V, rank, n);
+        zero_slice<DT, NT>(out, row_slice<DT>(row, a.V, rank, n));
         return;
     }
     const float H = h != 0.0f ? a.entropy[t] : 0.0f;

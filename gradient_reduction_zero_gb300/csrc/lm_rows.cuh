@@ -676,17 +676,19 @@ __device__ __forceinline__ void map_row(const char* row, char* out, const Slice&
     }
 }
 
-// Zeros in this block's part of a row.
+// Zeros in the elements of a slice, which is the logits' also where the output
+// is aligned otherwise: a block never writes to another one's elements.
 template <int DT, int NT>
-__device__ __forceinline__ void zero_row(char* out, int V, unsigned rank, unsigned n)
+__device__ __forceinline__ void zero_slice(char* out, const Slice& s)
 {
-    const Slice s = row_slice<DT>(out, V, rank, n);
     constexpr int kB = El<DT>::kBytes;
+    char* p = out + (int64_t)s.first * kB;
+    const RowSpan r = row_span<DT>(p, s.last - s.first);
     const int t = threadIdx.x;
-    for (int i = s.lo + t; i < s.hi; i += NT)
-        st16(out + s.vec0 * kB + (int64_t)i * 16, make_uint4(0, 0, 0, 0));
-    if (t < s.head) El<DT>::store(out + t * kB, 0.0f);
-    if (t < s.tail) El<DT>::store(out + (int64_t)(s.tail0 + t) * kB, 0.0f);
+    for (int i = t; i < r.nvec; i += NT)
+        st16(p + r.head * kB + (int64_t)i * 16, make_uint4(0, 0, 0, 0));
+    if (t < r.head) El<DT>::store(p + t * kB, 0.0f);
+    if (t < r.tail) El<DT>::store(p + (int64_t)(r.head + r.nvec * El<DT>::kVec + t) * kB, 0.0f);
 }
 
 // ------------------------------------------------------------ launch shapes

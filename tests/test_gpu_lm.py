@@ -377,6 +377,28 @@ def test_distill(dpz, T, V, K, extra, offset, dt, tdt, mask):
                             "dlogits of the step")
 
 
+@pytest.mark.parametrize("V", [8193, 12289, 50257])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("step", [False, True])
+def test_distill_without_entries(dpz, V, dt, step):
+    """Rows without a teacher's entry have a gradient of zeros in every element,
+    also where the output's rows are aligned otherwise than the logits'."""
+    T = 400
+    x = Box(T, V, DT[dt], 0, 0, _logits(T, V, dt, "plain", 2))
+    ids = torch.full((T, 3), -1, device="cuda")
+    t, w = torch.zeros(T, 3, device="cuda"), torch.ones(T, device="cuda")
+    lse, loss = torch.logsumexp(x.m.float(), 1), torch.ones(T, device="cuda")
+    for extra, offset in ((0, 0), (1, 1), (2, 5)):
+        out = Box(T, V, DT[dt], extra, offset)
+        if step:
+            dpz.lm_distill_step(x.m, ids, t, w, loss, out.m)
+            assert not bool(loss.any())
+        else:
+            dpz.lm_distill_grad(x.m, ids, t, lse, w, out.m)
+        out.check("dlogits")
+        assert not bool(out.m.any())
+
+
 # ------------------------------------------------------------ differences
 
 def test_gradients_against_differences(dpz):
