@@ -181,6 +181,21 @@ __device__ __forceinline__ void write_teacher_part(const DistillArgs& a, const T
     }
 }
 
+// The statistics of this thread's elements of a slice.
+template <int DT, int NT>
+__device__ __forceinline__ Stat slice_stat(const char* row, const Slice& sl, const StatScale& k)
+{
+    RefStat<DT> rs;
+    thread_rows<DT, NT>(rs, row, sl, sl.lo + threadIdx.x, k);
+    Stat own = rs.get();
+    if (!rs.good(k)) {
+        ThreadStat<DT, NT, false, false> ts;
+        thread_rows<DT, NT>(ts, row, sl, sl.lo + threadIdx.x, k);
+        own = ts.get();
+    }
+    return thread_rest<DT>(own, row, sl, k);
+}
+
 // ------------------------------------------------------------ loss alone
 
 // A row per block (or cluster) of NT threads, and a warp more that loads the
@@ -195,22 +210,14 @@ __global__ void __launch_bounds__(NT + 32, kLossBlocks<DT, NT>) k_distill(Distil
     pdl_enter();
     const int64_t t = blockIdx.x >> (31 - __clz(n));
     const char* row = a.x.p + t * a.x.ld * El<DT>::kBytes;
+    const StatScale k(a.inv_tau);
     if (threadIdx.x >= NT) {
         if (rank == 0) load_teacher<DT>(a, t, row, 0, a.V, w);
-        row_stat_beside(n);
+        row_stat_beside(k, ssh, n);
         return;
     }
     const Slice sl = row_slice<DT>(row, a.V, rank, n);
-    const StatScale k(a.inv_tau);
-    RefStat<DT> rs;
-    thread_rows<DT, NT>(rs, row, sl, sl.lo + threadIdx.x, k);
-    Stat own = rs.get();
-    if (!rs.good(k)) {
-        ThreadStat<DT, NT, false, false> ts;
-        thread_rows<DT, NT>(ts, row, sl, sl.lo + threadIdx.x, k);
-        own = ts.get();
-    }
-    const Stat s = row_stat<NT>(thread_rest<DT>(own, row, sl, k), k, ssh, rank, n, [] {});
+    const Stat s = row_stat<NT>(slice_stat<DT, NT>(row, sl, k), k, ssh, rank, n, [] {});
     if (rank == 0 && threadIdx.x < 32) write_loss(a, t, w, s, row_result(s, a.inv_tau, k), k);
 }
 
@@ -329,7 +336,7 @@ __device__ __forceinline__ Stat step_stat(const StatScale& k, StatShared<NT>& sh
 }
 
 template <int DT, int NT>
-__global__ void __launch_bounds__(NT + 32, kStepBlocks<NT>) k_distill_step(DistillArgs a, int stage)
+__global__ void __launch_bounds__(NT + 32, kStepBlocks) k_distill_step(DistillArgs a, int stage)
 {
     extern __shared__ uint4 staged[];           // [stage][NT]
     __shared__ Teacher w[2];                    // this row's and the next one's
@@ -478,6 +485,52 @@ __global__ void __launch_bounds__(NT + 32, kStepBlocks<NT>) k_distill_step(Disti
     }
 }
 
+// The same for short rows: a block (or cluster) per row, which reads it twice,
+// the second time from L1 or L2.  Enough blocks are resident to load while
+// others compute, without a row ahead.
+template <int DT, int NT>
+__global__ void __launch_bounds__(NT + 32, kRereadBlocks<NT>) k_distill_step_reread(DistillArgs a)
+{
+    __shared__ Teacher w;
+    __shared__ StatShared<NT> ssh;
+    __shared__ TokenHash hash;
+    const unsigned rank = cluster_rank(), n = cluster_size();
+    if (n > 1) cluster_arrive_relaxed();
+    pdl_enter();
+    const int64_t t = blockIdx.x >> (31 - __clz(n));
+    const char* row = a.x.p + t * a.x.ld * El<DT>::kBytes;
+    char* out = a.dx.p + t * a.dx.ld * El<DT>::kBytes;
+    const float wt = a.dloss[t];
+    const StatScale k(a.inv_tau);
+    const Slice sl = row_slice<DT>(row, a.V, rank, n);
+    if (threadIdx.x >= NT) {
+        clear_hash(hash);
+        load_teacher<DT>(a, t, row, 0, a.V, w);
+        const bool repeats = find_repeats(w.id, a.K, hash);
+        if (threadIdx.x == NT) w.repeats = repeats;
+        const Stat s = row_stat_beside(k, ssh, n);
+        const RowResult r = row_result(s, a.inv_tau, k);
+        if (rank == 0) write_loss(a, t, w, s, r, k);
+        barrier_wait<NT + 32>();
+        if (wt == 0.0f || !w.any || r.lse == -INFINITY) return;
+        write_teacher_part<DT>(a, w, sl, StudentGrad(a.inv_tau, r.lse, wt * a.inv_tau), out);
+        return;
+    }
+    const Stat s = row_stat<NT>(slice_stat<DT, NT>(row, sl, k), k, ssh, rank, n, [] {});
+    const float lse = row_result(s, a.inv_tau, k).lse;
+    if (wt == 0.0f || !w.any || lse == -INFINITY) zero_slice<DT, NT>(out, sl);
+    else {
+        const int first = sl.lo + threadIdx.x;
+        uint4 v[kMapLoads];
+        map_load<DT, NT>(row, sl, first, v);
+        if (StudentGradExp::holds(DT, lse, wt * a.inv_tau))
+            map_row<DT, NT>(row, out, sl, first, v, StudentGradExp(a.inv_tau, lse, wt * a.inv_tau));
+        else
+            map_row<DT, NT>(row, out, sl, first, v, StudentGrad(a.inv_tau, lse, wt * a.inv_tau));
+    }
+    barrier_arrive<NT + 32>();
+}
+
 // Blocks of a persistent kernel that fit on the GPU together, by the vectors
 // each thread stages; asked for once.
 template <int DT, int NT>
@@ -525,8 +578,14 @@ cudaError_t launch_step(const DistillArgs& a, cudaStream_t s)
 template <int DT>
 cudaError_t step_typed(const DistillArgs& a, cudaStream_t s)
 {
-    return row_bytes(a.V, DT) <= kShortRow ? launch_step<DT, kShortThreads>(a, s)
-                                           : launch_step<DT, kStepThreads>(a, s);
+    const int64_t bytes = row_bytes(a.V, DT);
+    if (bytes > kRereadRow) return launch_step<DT, kStepThreads>(a, s);
+    const bool small = bytes <= kShortRow;
+    const int nt = small ? kShortThreads : kRereadThreads;
+    const unsigned n = row_cluster(a.T, bytes, nt);
+    return launch_kernel(small ? k_distill_step_reread<DT, kShortThreads>
+                               : k_distill_step_reread<DT, kRereadThreads>,
+                         dim3((unsigned)a.T * n), dim3(nt + 32), 0, s, true, n > 1 ? n : 0u, a);
 }
 
 }  // namespace

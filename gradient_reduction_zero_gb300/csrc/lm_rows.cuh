@@ -526,6 +526,15 @@ struct StatShared {
     Stat block[kMaxCluster];   // by cluster rank
 };
 
+// What the blocks of a row's cluster have found, joined.
+template <int NT>
+__device__ __forceinline__ Stat blocks_stat(const StatScale& k, const StatShared<NT>& sh, unsigned n)
+{
+    Stat s = sh.block[0];
+    for (unsigned r = 1; r < n; ++r) s = stat_join(s, sh.block[r], k);
+    return s;
+}
+
 // The statistics of the whole row, in every thread, from each thread's own.
 // In a cluster every block must have announced itself with
 // cluster_arrive_relaxed before.  The block's barriers are two __syncthreads,
@@ -553,29 +562,27 @@ __device__ __forceinline__ Stat row_stat(Stat s, const StatScale& k, StatShared<
         }
     }
     if (wid == kWarps - 1) other();
-    if (n == 1) {
-        __syncthreads();
-        return sh.block[0];
+    if (n == 1) __syncthreads();
+    else {
+        cluster_arrive_release();
+        cluster_wait();
     }
-    cluster_arrive_release();
-    cluster_wait();
-    s = sh.block[0];
-    for (unsigned r = 1; r < n; ++r) s = stat_join(s, sh.block[r], k);
-    return s;
+    return blocks_stat(k, sh, n);
 }
 
-// The barriers of row_stat for a warp beside the NT threads, which works until
-// then and has nothing to add.
-__device__ __forceinline__ void row_stat_beside(unsigned n)
+// row_stat for a warp beside the NT threads, which works until then and has
+// nothing to add.
+template <int NT>
+__device__ __forceinline__ Stat row_stat_beside(const StatScale& k, StatShared<NT>& sh, unsigned n)
 {
     __syncthreads();
-    if (n == 1) {
-        __syncthreads();
-        return;
+    if (n == 1) __syncthreads();
+    else {
+        cluster_wait();
+        cluster_arrive_release();
+        cluster_wait();
     }
-    cluster_wait();
-    cluster_arrive_release();
-    cluster_wait();
+    return blocks_stat(k, sh, n);
 }
 
 // lse and entropy of a row's statistics; m NaN or +inf: NaN, m -inf: -inf and 0.
@@ -694,8 +701,8 @@ __device__ __forceinline__ void zero_slice(char* out, const Slice& s)
 // ------------------------------------------------------------ launch shapes
 
 // Threads per block for rows up to kShortRow bytes, and for longer ones.  At
-// 8,000 bf16 (16 KB) the distillation step takes 27 us with 64 threads and 45
-// with 256 (6,250 rows), eight alternatives 36 and 47 (12,500 rows); at 16,000,
+// 8,000 bf16 (16 KB) eight alternatives take 36 us with 64 threads and 47 with
+// 256 (12,500 rows), the distillation step 54 and 64 (8,192 rows); at 16,000,
 // eight alternatives 33 and 32.
 constexpr int kRowThreads = 256, kShortThreads = 64;
 constexpr int64_t kShortRow = 16384;
@@ -704,17 +711,29 @@ constexpr int64_t kShortRow = 16384;
 constexpr int kStepThreads = 256;
 constexpr int kStageMax = 100 * 1024;
 
+// Rows up to kRereadRow bytes are read twice by the step, in blocks of
+// kRereadThreads above kShortRow, instead of being staged: 8,192 rows of 16,000
+// bf16 take 92 us (staged 128; with blocks of 256 threads 99), of 24,000 149 and
+// 151, of 32,000 224 and 176.  All resident blocks' rows have to stay in L2
+// until they are read again: with 12 blocks on an SM instead of 9, 16,000 take
+// 106 us.
+constexpr int kRereadThreads = 128;
+constexpr int64_t kRereadRow = 49152;
+
 // Blocks on an SM that the compiler leaves registers for, the teacher's warp
 // counted in.  The loss of 8,192 x 50,257 bf16 takes 137.6 us with 4, 129.6 with
 // 5 and 133.6 with 6; fp32 rows need fewer registers.  The gradient with 5 takes
 // 125 us at 4,096 x 50,257 bf16 against 127.6 with 7, but 37 to 38 at rows of 16
-// to 32 KB against 33.  The step's two blocks are what shared memory holds.
+// to 32 KB against 33.  The step's two blocks are what shared memory holds; in
+// blocks of 64 threads that read the row twice, 14, 16 and 20 take 23.4, 22.1 and
+// 22.6 us at 8,192 x 2,000 bf16, 54.6, 54.1 and 58.9 at 8,192 x 8,000.
 template <int DT, int NT>
 constexpr int kLossBlocks = NT == kRowThreads ? (DT == DPZ_F32 ? 6 : 5) : 20;
 template <int NT>
 constexpr int kGradBlocks = NT == kRowThreads ? 7 : 20;   // on an SM, at least
 template <int NT>
-constexpr int kStepBlocks = NT == kStepThreads ? 2 : 8;   // on an SM, at least
+constexpr int kRereadBlocks = NT == kRereadThreads ? 9 : 16;
+constexpr int kStepBlocks = 2;
 
 inline int64_t row_bytes(int V, int dt) { return (int64_t)V * (dt == DPZ_F32 ? 4 : 2); }
 

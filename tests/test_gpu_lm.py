@@ -377,6 +377,19 @@ def test_distill(dpz, T, V, K, extra, offset, dt, tdt, mask):
                             "dlogits of the step")
 
 
+# T, V, K, extra, offset: both sides of the row lengths in bytes at which the
+# step changes its form (16 and 48 KB), more rows than resident blocks
+LENGTHS = [(330, 4096, 5, 0, 0), (170, 4097, 40, 1, 0), (170, 8192, 70, 0, 0), (330, 8193, 9, 0, 3),
+           (170, 12288, 33, 0, 0), (620, 12289, 3, 0, 0), (40, 24576, 256, 0, 0), (620, 24577, 8, 3, 1)]
+
+
+@pytest.mark.parametrize("T,V,K,extra,offset", LENGTHS)
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("mask", ["plain", "hard"])
+def test_distill_at_row_lengths(dpz, T, V, K, extra, offset, dt, mask):
+    test_distill(dpz, T, V, K, extra, offset, dt, "f32", mask)
+
+
 @pytest.mark.parametrize("V", [8193, 12289, 50257])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("step", [False, True])
