@@ -579,13 +579,13 @@ template <int DT>
 cudaError_t step_typed(const DistillArgs& a, cudaStream_t s)
 {
     const int64_t bytes = row_bytes(a.V, DT);
-    if (bytes > kRereadRow) return launch_step<DT, kStepThreads>(a, s);
-    const bool small = bytes <= kShortRow;
-    const int nt = small ? kShortThreads : kRereadThreads;
-    const unsigned n = row_cluster(a.T, bytes, nt);
-    return launch_kernel(small ? k_distill_step_reread<DT, kShortThreads>
-                               : k_distill_step_reread<DT, kRereadThreads>,
-                         dim3((unsigned)a.T * n), dim3(nt + 32), 0, s, true, n > 1 ? n : 0u, a);
+    if (bytes > kMidRow) return launch_step<DT, kStepThreads>(a, s);
+    return by_row_threads(a.T, bytes, [&](auto threads) {
+        constexpr int NT = threads;
+        const unsigned n = row_cluster(a.T, bytes, NT);
+        return launch_kernel(k_distill_step_reread<DT, NT>, dim3((unsigned)a.T * n), dim3(NT + 32), 0,
+                             s, true, n > 1 ? n : 0u, a);
+    });
 }
 
 }  // namespace
@@ -598,25 +598,23 @@ cudaError_t launch_distill(const DistillArgs& a, cudaStream_t s)
         return b ? step_typed<DPZ_BF16>(a, s) : step_typed<DPZ_F32>(a, s);
     }
     const int64_t bytes = row_bytes(a.V, a.x.dt);
-    const bool small = bytes <= kShortRow;
-    const int nt = small ? kShortThreads : kRowThreads;
-    if (a.loss != nullptr) {
-        set_last_kernel_name("lm_distill");
-        const unsigned n = row_cluster(a.T, bytes, nt);
-        auto fn = small ? (b ? k_distill<DPZ_BF16, kShortThreads> : k_distill<DPZ_F32, kShortThreads>)
-                        : (b ? k_distill<DPZ_BF16, kRowThreads> : k_distill<DPZ_F32, kRowThreads>);
-        return launch_kernel(fn, dim3((unsigned)a.T * n), dim3(nt + 32), 0, s, true, n > 1 ? n : 0u,
-                             a);
-    }
-    set_last_kernel_name("lm_distill_grad");
-    // two independent blocks per row share the last wave better than one (1,000
-    // rows of 32,000 fp32: 41.4 us, 45.7 with one).  Four blocks take 40.8 there,
-    // but each loads the entries again, which shorter rows pay for (a row of 32 KB
-    // has 8 KB a block: 52 to 54 us where two take 33).
-    const unsigned n = std::max(row_cluster(a.T, bytes, nt), small ? 1u : 2u);
-    auto fn = small ? (b ? k_distill_grad<DPZ_BF16, kShortThreads> : k_distill_grad<DPZ_F32, kShortThreads>)
-                    : (b ? k_distill_grad<DPZ_BF16, kRowThreads> : k_distill_grad<DPZ_F32, kRowThreads>);
-    return launch_kernel(fn, dim3((unsigned)a.T, n), dim3(nt + 32), 0, s, true, 0u, a);
+    set_last_kernel_name(a.loss != nullptr ? "lm_distill" : "lm_distill_grad");
+    return by_row_threads(a.T, bytes, [&](auto threads) {
+        constexpr int NT = threads;
+        unsigned n = row_cluster(a.T, bytes, NT);
+        if (a.loss != nullptr)
+            return launch_kernel(b ? k_distill<DPZ_BF16, NT> : k_distill<DPZ_F32, NT>,
+                                 dim3((unsigned)a.T * n), dim3(NT + 32), 0, s, true, n > 1 ? n : 0u,
+                                 a);
+        // two independent blocks per row share the last wave better than one
+        // (1,000 rows of 32,000 fp32: 41.4 us, 45.7 with one).  Four blocks take
+        // 40.8 there, but each loads the entries again, which shorter rows pay
+        // for: 8,192 rows of 16,000 bf16 take 82 us with two blocks of 256
+        // threads and 80 with one of 128.
+        if (bytes > kMidRow) n = std::max(n, 2u);
+        return launch_kernel(b ? k_distill_grad<DPZ_BF16, NT> : k_distill_grad<DPZ_F32, NT>,
+                             dim3((unsigned)a.T, n), dim3(NT + 32), 0, s, true, 0u, a);
+    });
 }
 
 }  // namespace dpz

@@ -374,31 +374,26 @@ void (*logprobs_kernel(bool ent, bool top))(LogprobArgs)
 cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t s)
 {
     set_last_kernel_name("lm_logprobs");
-    const int64_t bytes = row_bytes(a.V, a.x.dt);
-    const int nt = bytes <= kShortRow ? kShortThreads : kRowThreads;
-    const unsigned n = row_cluster(a.T, bytes, nt);
     const bool ent = a.entropy != nullptr, top = a.K > 0, b = a.x.dt == DPZ_BF16;
-    void (*fn)(LogprobArgs) =
-        nt == kShortThreads ? (b ? logprobs_kernel<DPZ_BF16, kShortThreads>(ent, top)
-                                 : logprobs_kernel<DPZ_F32, kShortThreads>(ent, top))
-                            : (b ? logprobs_kernel<DPZ_BF16, kRowThreads>(ent, top)
-                                 : logprobs_kernel<DPZ_F32, kRowThreads>(ent, top));
-    return launch_kernel(fn, dim3((unsigned)a.T * n), dim3(nt), 0, s, true, n > 1 ? n : 0u, a);
+    return by_row_threads(a.T, row_bytes(a.V, a.x.dt), [&](auto threads) {
+        constexpr int NT = threads;
+        const unsigned n = row_cluster(a.T, row_bytes(a.V, a.x.dt), NT);
+        void (*fn)(LogprobArgs) = b ? logprobs_kernel<DPZ_BF16, NT>(ent, top)
+                                    : logprobs_kernel<DPZ_F32, NT>(ent, top);
+        return launch_kernel(fn, dim3((unsigned)a.T * n), dim3(NT), 0, s, true, n > 1 ? n : 0u, a);
+    });
 }
 
 cudaError_t launch_logprobs_grad(const LogprobGradArgs& a, cudaStream_t s)
 {
     set_last_kernel_name("lm_logprobs_grad");
-    const bool b = a.x.dt == DPZ_BF16;
-    const int64_t bytes = row_bytes(a.V, a.x.dt);
-    const int nt = bytes <= kShortRow ? kShortThreads : kRowThreads;
-    const unsigned n = row_cluster(a.T, bytes, nt);
-    void (*fn)(LogprobGradArgs) =
-        nt == kShortThreads ? (b ? k_logprobs_grad<DPZ_BF16, kShortThreads>
-                                 : k_logprobs_grad<DPZ_F32, kShortThreads>)
-                            : (b ? k_logprobs_grad<DPZ_BF16, kRowThreads>
-                                 : k_logprobs_grad<DPZ_F32, kRowThreads>);
-    return launch_kernel(fn, dim3((unsigned)a.T, n), dim3(nt), 0, s, true, 0u, a);
+    return by_row_threads(a.T, row_bytes(a.V, a.x.dt), [&](auto threads) {
+        constexpr int NT = threads;
+        const unsigned n = row_cluster(a.T, row_bytes(a.V, a.x.dt), NT);
+        return launch_kernel(a.x.dt == DPZ_BF16 ? k_logprobs_grad<DPZ_BF16, NT>
+                                                : k_logprobs_grad<DPZ_F32, NT>,
+                             dim3((unsigned)a.T, n), dim3(NT), 0, s, true, 0u, a);
+    });
 }
 
 }  // namespace dpz

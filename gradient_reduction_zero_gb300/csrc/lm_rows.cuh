@@ -8,6 +8,7 @@
 #include <atomic>
 #include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include "bulk.cuh"
 #include "device.cuh"
@@ -700,25 +701,41 @@ __device__ __forceinline__ void zero_slice(char* out, const Slice& s)
 
 // ------------------------------------------------------------ launch shapes
 
-// Threads per block for rows up to kShortRow bytes, and for longer ones.  At
-// 8,000 bf16 (16 KB) eight alternatives take 36 us with 64 threads and 47 with
-// 256 (12,500 rows), the distillation step 54 and 64 (8,192 rows); at 16,000,
-// eight alternatives 33 and 32.
-constexpr int kRowThreads = 256, kShortThreads = 64;
-constexpr int64_t kShortRow = 16384;
+// Threads per block for rows up to kShortRow bytes, up to kMidRow, and for
+// longer ones or up to kFewRows rows.  8,192 rows of bf16, in us:
+//
+//   logits                8,000 (16 KB)   16,000     24,000 (48 KB)
+//   threads               64  128  256   128  256     128  256
+//   log probabilities     27   30   40    47   55      66   70
+//   eight alternatives    44   49   61    68   77      88   91
+//   their gradient        39   37   42    71   71     107  104
+//   distillation loss     28   30   43    48   57      66   72
+//   its gradient          44   44   59    80   82     120  120
+//
+// Rows that all fit on the GPU at once want many threads each: 300 rows of 8,000
+// with eight alternatives take 7.4 us with 64 threads and 5.1 with 256, their
+// gradient 4.2 and 2.5; at 450 rows of 2,000, 5.5 and 4.6, but 2.4 and 2.9.
+constexpr int kRowThreads = 256, kMidThreads = 128, kShortThreads = 64;
+constexpr int64_t kShortRow = 16384, kMidRow = 49152, kFewRows = 304;
 
-// The distillation step's blocks and the most shared memory each stages.
-constexpr int kStepThreads = 256;
+// Calls f with the threads for T rows of this length, as a constant.
+template <class F>
+cudaError_t by_row_threads(int64_t T, int64_t bytes, F&& f)
+{
+    if (T <= kFewRows) return f(std::integral_constant<int, kRowThreads>{});
+    if (bytes <= kShortRow) return f(std::integral_constant<int, kShortThreads>{});
+    if (bytes <= kMidRow) return f(std::integral_constant<int, kMidThreads>{});
+    return f(std::integral_constant<int, kRowThreads>{});
+}
+
+// The distillation step's blocks for rows longer than kMidRow, and the most
+// shared memory each stages.  Shorter ones are read twice instead: 8,192 rows
+// of 16,000 bf16 take 92 us (staged 128; with blocks of 256 threads 99), of
+// 24,000 149 and 151, of 32,000 224 and 176.  All resident blocks' rows have to
+// stay in L2 until they are read again: with 12 blocks on an SM instead of 9,
+// 16,000 take 106 us.
+constexpr int kStepThreads = kRowThreads;
 constexpr int kStageMax = 100 * 1024;
-
-// Rows up to kRereadRow bytes are read twice by the step, in blocks of
-// kRereadThreads above kShortRow, instead of being staged: 8,192 rows of 16,000
-// bf16 take 92 us (staged 128; with blocks of 256 threads 99), of 24,000 149 and
-// 151, of 32,000 224 and 176.  All resident blocks' rows have to stay in L2
-// until they are read again: with 12 blocks on an SM instead of 9, 16,000 take
-// 106 us.
-constexpr int kRereadThreads = 128;
-constexpr int64_t kRereadRow = 49152;
 
 // Blocks on an SM that the compiler leaves registers for, the teacher's warp
 // counted in.  The loss of 8,192 x 50,257 bf16 takes 137.6 us with 4, 129.6 with
@@ -728,11 +745,11 @@ constexpr int64_t kRereadRow = 49152;
 // blocks of 64 threads that read the row twice, 14, 16 and 20 take 23.4, 22.1 and
 // 22.6 us at 8,192 x 2,000 bf16, 54.6, 54.1 and 58.9 at 8,192 x 8,000.
 template <int DT, int NT>
-constexpr int kLossBlocks = NT == kRowThreads ? (DT == DPZ_F32 ? 6 : 5) : 20;
+constexpr int kLossBlocks = NT == kRowThreads ? (DT == DPZ_F32 ? 6 : 5) : NT == kMidThreads ? 10 : 20;
 template <int NT>
-constexpr int kGradBlocks = NT == kRowThreads ? 7 : 20;   // on an SM, at least
+constexpr int kGradBlocks = NT == kRowThreads ? 7 : NT == kMidThreads ? 8 : 20;
 template <int NT>
-constexpr int kRereadBlocks = NT == kRereadThreads ? 9 : 16;
+constexpr int kRereadBlocks = NT == kRowThreads ? 4 : NT == kMidThreads ? 9 : 16;
 constexpr int kStepBlocks = 2;
 
 inline int64_t row_bytes(int V, int dt) { return (int64_t)V * (dt == DPZ_F32 ? 4 : 2); }

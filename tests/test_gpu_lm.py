@@ -377,6 +377,23 @@ def test_distill(dpz, T, V, K, extra, offset, dt, tdt, mask):
                             "dlogits of the step")
 
 
+@pytest.mark.parametrize("V", [2000, 8001, 16001])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_top_of_ties_in_many_rows(dpz, V, dt):
+    """Rows of few distinct values, which the threshold does not thin out."""
+    T, K = 350, 20
+    g = torch.Generator(device="cuda").manual_seed(V)
+    few = torch.randint(0, 4, (T, V), generator=g, device="cuda").float()
+    few[::3] = torch.where(few[::3] == 3.0, -float("inf"), 0.0)
+    few[1::7, 5:] = -float("inf")
+    x = few.to(DT[dt])
+    y = torch.zeros(T, dtype=torch.int64, device="cuda")
+    lp, tl = torch.empty(T, device="cuda"), torch.empty(T, K, device="cuda")
+    ti = torch.empty(T, K, dtype=torch.int64, device="cuda")
+    dpz.lm_logprobs(x, y, lp, top_ids=ti, top_logprobs=tl)
+    assert np.array_equal(ti.cpu().numpy(), R.top(few.cpu().numpy(), K))
+
+
 # T, V, K, extra, offset: both sides of the row lengths in bytes at which the
 # step changes its form (16 and 48 KB), more rows than resident blocks
 LENGTHS = [(330, 4096, 5, 0, 0), (170, 4097, 40, 1, 0), (170, 8192, 70, 0, 0), (330, 8193, 9, 0, 3),
@@ -388,6 +405,21 @@ LENGTHS = [(330, 4096, 5, 0, 0), (170, 4097, 40, 1, 0), (170, 8192, 70, 0, 0), (
 @pytest.mark.parametrize("mask", ["plain", "hard"])
 def test_distill_at_row_lengths(dpz, T, V, K, extra, offset, dt, mask):
     test_distill(dpz, T, V, K, extra, offset, dt, "f32", mask)
+
+
+# more rows than are given the most threads each (304), on both sides of the
+# lengths in bytes at which the threads change
+MANY = [(310, 1, 0, 0), (310, 9, 7, 5), (310, 1000, 0, 3), (310, 4097, 0, 0), (310, 8192, 0, 0),
+        (310, 8193, 1, 0), (310, 12289, 0, 0), (310, 24577, 0, 0)]
+
+
+@pytest.mark.parametrize("T,V,extra,offset", MANY)
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_many_rows(dpz, T, V, extra, offset, dt):
+    test_logprobs(dpz, T, V, extra, offset, dt, "hard")
+    for place in ("same", "shifted"):
+        test_logprobs_grad(dpz, T, V, extra, offset, dt, "hard", place)
+    test_distill(dpz, T, V, min(V, 40), extra, offset, dt, "f32", "hard")
 
 
 @pytest.mark.parametrize("V", [8193, 12289, 50257])
