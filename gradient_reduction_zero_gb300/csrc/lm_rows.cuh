@@ -6,7 +6,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <cfloat>
 #include <cmath>
 #include <type_traits>
 
@@ -435,9 +434,13 @@ struct ThreadStat {
 // A thread's S alone (U is left out), against the largest element of its first
 // vectors instead of the running maximum: the reference cancels in the result,
 // and nothing has to be compared or rescaled, a third fewer instructions.
-// Elements so far above the reference that S overflows, NaN, +inf and a
-// reference too low for the fused exponent show in good(); the thread's
-// vectors then go through ThreadStat.
+// Elements so far above the reference that S passes kRefSumMax, NaN, +inf and
+// a reference too low for the fused exponent show in good(); the thread's
+// vectors then go through ThreadStat.  With S below 2^60 no join of up to 2^11
+// threads' sums overflows, and a sum that a join's factor 2^d flushes to zero
+// (d < -126) was at most 2^-66 of the others.
+constexpr float kRefSumMax = 0x1p60f;
+
 template <int DT>
 struct RefStat {
     float ref = -INFINITY;
@@ -463,7 +466,7 @@ struct RefStat {
 
     __device__ __forceinline__ bool good(const StatScale& k) const
     {
-        return ref == -INFINITY || (ref >= k.low_max && lo2(S) + hi2(S) < FLT_MAX);
+        return ref == -INFINITY || (ref >= k.low_max && lo2(S) + hi2(S) < kRefSumMax);
     }
 
     __device__ __forceinline__ Stat get() const { return {ref, lo2(S) + hi2(S), 0.0f}; }
