@@ -171,7 +171,7 @@ __device__ __forceinline__ void load_teacher(const DistillArgs& a, int64_t t, co
 
 // By one warp: sum_k q_k (log q_k - log p_k), in a fixed order; lane 0 writes.
 __device__ __forceinline__ void write_loss(const DistillArgs& a, int64_t t, const Teacher& w,
-                                           const Stat& s, const RowResult& r, const StatScale& k)
+                                           const Stat& s, const RowResult& r)
 {
     const int lane = threadIdx.x & 31;
     float sum = 0.0f;
@@ -181,7 +181,7 @@ __device__ __forceinline__ void write_loss(const DistillArgs& a, int64_t t, cons
         for (int l = 0; l < kEntries; ++l) {
             const int i = min(i0 + 32 * l, a.K - 1);
             q[l] = i0 + 32 * l < a.K ? w.q[i] : 0.0f;
-            d[l] = w.logq[i] - logprob_of(w.x[i], s, r, a.inv_tau, k);
+            d[l] = w.logq[i] - logprob_of(w.x[i], s, r, a.inv_tau);
         }
 #pragma unroll
         for (int l = 0; l < kEntries; ++l)
@@ -269,11 +269,11 @@ __device__ __forceinline__ Stat slice_stat(const char* row, const Slice& sl, con
 {
     RefStat<DT> rs;
     thread_rows<DT, NT>(rs, row, sl, sl.lo + threadIdx.x, k);
-    Stat own = rs.get();
+    Stat own = rs.get(k);
     if (!rs.good(k)) {
         ThreadStat<DT, NT, false, false> ts;
         thread_rows<DT, NT>(ts, row, sl, sl.lo + threadIdx.x, k);
-        own = ts.get();
+        own = ts.get(k);
     }
     return thread_rest<DT>(own, row, sl, k);
 }
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(NT + 32, kLossBlocks<DT, NT>) k_distill(Distil
     }
     const Slice sl = row_slice<DT>(row, a.V, rank, n);
     const Stat s = row_stat<NT>(slice_stat<DT, NT>(row, sl, k), k, ssh, rank, n, [] {});
-    if (rank == 0 && threadIdx.x < 32) write_loss(a, t, w, s, row_result(s, a.inv_tau, k), k);
+    if (rank == 0 && threadIdx.x < 32) write_loss(a, t, w, s, row_result(s, a.inv_tau));
 }
 
 // ------------------------------------------------------------ gradient alone
@@ -449,8 +449,8 @@ __global__ void __launch_bounds__(NT + 32, kStepBlocks) k_distill_step(DistillAr
             const float wt = a.dloss[t];
             __syncthreads();
             const Stat s = step_stat<NT>(k, ssh[b], rank, n);
-            const RowResult r = row_result(s, a.inv_tau, k);
-            if (rank == 0) write_loss(a, t, w[b], s, r, k);
+            const RowResult r = row_result(s, a.inv_tau);
+            if (rank == 0) write_loss(a, t, w[b], s, r);
             if (t + step < a.T) load(t + step, w[b ^ 1]);
             barrier_wait<NT + 32>();
             if (wt == 0.0f || !w[b].any || r.lse == -INFINITY) continue;
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(NT + 32, kStepBlocks) k_distill_step(DistillAr
             add_group(g);
         }
         thread_rows<DT, NT>(rs, row, sl, first + have * NT, k);
-        Stat mine = rs.get();
+        Stat mine = rs.get(k);
         if (!rs.good(k)) {
             ThreadStat<DT, NT, false, false> ts;
 #pragma unroll 1
@@ -517,13 +517,13 @@ __global__ void __launch_bounds__(NT + 32, kStepBlocks) k_distill_step(DistillAr
                 ts.add(v, 0, k, nullptr);
             }
             thread_rows<DT, NT>(ts, row, sl, first + have * NT, k);
-            mine = ts.get();
+            mine = ts.get(k);
         }
         mine = warp_stat(thread_rest<DT>(mine, row, sl, k), k);
         if (lane == 0) ssh[b].warp[wid] = mine;
         __syncthreads();
         const Stat s = step_stat<NT>(k, ssh[b], rank, n);
-        const float lse = row_result(s, a.inv_tau, k).lse;
+        const float lse = row_result(s, a.inv_tau).lse;
         char* out = a.dx.p + t * a.dx.ld * kB;
         const bool same = same_alignment(row, out);
         const bool zero = wt == 0.0f || !w[b].any || lse == -INFINITY;
@@ -591,15 +591,15 @@ __global__ void __launch_bounds__(NT + 32, kRereadBlocks<NT>) k_distill_step_rer
         const bool repeats = find_repeats(w.id, a.K, hash);
         if (threadIdx.x == NT) w.repeats = repeats;
         const Stat s = row_stat_beside(k, ssh, n);
-        const RowResult r = row_result(s, a.inv_tau, k);
-        if (rank == 0) write_loss(a, t, w, s, r, k);
+        const RowResult r = row_result(s, a.inv_tau);
+        if (rank == 0) write_loss(a, t, w, s, r);
         barrier_wait<NT + 32>();
         if (wt == 0.0f || !w.any || r.lse == -INFINITY) return;
         write_teacher_part<DT>(a, w, sl, StudentGrad(a.inv_tau, r.lse, wt * a.inv_tau), out);
         return;
     }
     const Stat s = row_stat<NT>(slice_stat<DT, NT>(row, sl, k), k, ssh, rank, n, [] {});
-    const float lse = row_result(s, a.inv_tau, k).lse;
+    const float lse = row_result(s, a.inv_tau).lse;
     if (wt == 0.0f || !w.any || lse == -INFINITY) zero_slice<DT, NT>(out, sl);
     else {
         const int first = sl.lo + threadIdx.x;

@@ -82,7 +82,7 @@ __device__ __forceinline__ Stat thread_stat(const char* row, const Slice& s, con
     ThreadStat<DT, NT, ENT, TOP> ts;
     constexpr int kLoads = TOP ? kTopLoads<DT> : 4;
     thread_rows<DT, NT, kLoads>(ts, row, s, s.lo + t, k, kept);
-    const Stat st = thread_rest<DT>(ts.get(), row, s, k);
+    const Stat st = thread_rest<DT>(ts.get(k), row, s, k);
     if (TOP) {
         const bool single = t < s.head || t < s.tail;
         top->max = single || s.lo + t < s.hi ? value_order(st.m) : 0u;
@@ -279,11 +279,11 @@ __global__ void __launch_bounds__(NT, (DT == DPZ_F32 ? 7 : 6) * kRowThreads / NT
         if constexpr (TOP) top_threshold(a.K, tsh);
     });
     if (rank == 0 && threadIdx.x < 32) {
-        const RowResult r = row_result(s, a.scale, k);
+        const RowResult r = row_result(s, a.scale);
         if (threadIdx.x == 0) {
             if (TOP) s_result = r;          // read after block_top's barrier
             if (a.logprob != nullptr)
-                a.logprob[t] = y < 0 ? 0.0f : logprob_of(target, s, r, a.scale, k);
+                a.logprob[t] = y < 0 ? 0.0f : logprob_of(target, s, r, a.scale);
             if (a.lse != nullptr) a.lse[t] = r.lse;
             if (ENT) a.entropy[t] = r.entropy;
         }
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(NT, (DT == DPZ_F32 ? 7 : 6) * kRowThreads / NT
             const int64_t o = t * a.K + at;
             if (a.targets.it == DPZ_I64) static_cast<int64_t*>(a.top_ids)[o] = j;
             else static_cast<int*>(a.top_ids)[o] = j;
-            a.top_logprobs[o] = logprob_of(x, s, s_result, a.scale, k);
+            a.top_logprobs[o] = logprob_of(x, s, s_result, a.scale);
         };
         if (n == 1) {
             block_top<DT, NT>(row, sl, own, a.K, tsh, write);

@@ -307,40 +307,56 @@ __device__ __forceinline__ Slice row_slice(const char* p, int V, unsigned rank, 
 //
 // Running maximum m, S = sum 2^u and U = sum u 2^u (where ENT) over a part of
 // a row, with u = (x - m) c and c = scale * log2(e): one pass over the logits,
-// whatever came before a larger maximum being rescaled.  u is computed as
-// x c - (m c) in one fused operation; m c is rounded once and the same value
-// is used wherever m is, so its rounding cancels.  Elements below kLowest
-// count as kLowest there, whose 2^u is 0, so that a masked element (-inf) gives
-// 0 * u = 0 to U.  That needs a maximum well above kLowest and an ordinary
-// scale; otherwise (a row of the type's lowest value, or nothing but -inf so
-// far) u is (x - m) c and -inf is left out.
+// whatever came before a larger maximum being rescaled.
 struct Stat {
     float m, S, U;
 };
 
-constexpr float kMinExp = -16384.0f;
+constexpr float kMinExp = -16384.0f;   // 2^u is 0 there, and u 2^u too
 constexpr float kLowest = -1e20f;
 
-// c, and the smallest maximum for which the fused form holds.
+// Within a thread u is x c - (m c) in one fused operation where it may be:
+// m c is rounded once and the same value is used wherever m is, so that its
+// rounding shifts every u of the thread alike, by at most half a unit in the
+// last place of m c, and unshifted() takes the shift out at the end.  That
+// holds for |m c| up to kFusedMost, where the shift is 2^-10; at a row of -1e10
+// it would be 512, beyond the range of 2^u.  Elements below kLowest count as
+// kLowest, whose 2^u is 0, so that a masked element (-inf) gives 0 * u = 0 to
+// U.  Larger maxima (a row wholly masked by a finite value) and extreme scales
+// take the product of the difference, which has one operation more.
+constexpr float kFusedMost = 0x1p15f;
+
 struct StatScale {
-    float c, low_max;
+    float c, most;   // most: the largest |m c| for the fused form; -1: none
     __device__ __forceinline__ explicit StatScale(float scale)
-        : c(scale * kLog2e), low_max(c > 1e-15f && c < 1e17f ? -1e19f : INFINITY)
+        : c(scale * kLog2e), most(c > 1e-12f && c < 1e17f ? kFusedMost : -1.0f)
     {
     }
+    __device__ __forceinline__ bool fused(float mc) const { return fabsf(mc) <= most; }
 };
 
-// (a - m) c for the maxima a <= m of two parts.
-__device__ __forceinline__ float max_step(float a, float m, const StatScale& k)
+// (x - m) c, at least kMinExp; of halves, since the difference of two of the
+// type's values may overflow.
+__device__ __forceinline__ float exponent(float x, float m, float c)
 {
-    const float d = m < k.low_max ? (a - m) * k.c : a * k.c - m * k.c;
-    return fmaxf(d, kMinExp);
+    return fmaxf((0.5f * x - 0.5f * m) * (2.0f * c), kMinExp);
+}
+
+// A thread's S and U against rnd(m c), if that is the fused form's, against m c.
+__device__ __forceinline__ Stat unshifted(Stat s, const StatScale& k)
+{
+    const float mc = s.m * k.c;
+    if (!k.fused(mc)) return s;
+    const float d = __fmaf_rn(s.m, k.c, -mc);            // exact; u is too large by d
+    const float g = -d * kLn2, f = __fmaf_rn(0.5f * g, g, g);   // 2^-d - 1, d^3 left out
+    const float U = __fmaf_rn(-d, s.S, s.U);
+    return {s.m, __fmaf_rn(s.S, f, s.S), __fmaf_rn(U, f, U)};
 }
 
 __device__ __forceinline__ void stat_rebase(Stat& s, float m, const StatScale& k)
 {
     // u against the new maximum is u + d, so 2^u gets the factor 2^d
-    const float d = max_step(s.m, m, k);
+    const float d = exponent(s.m, m, k.c);
     const float f = ex2(d);
     s.U = f * __fmaf_rn(d, s.S, s.U);
     s.S *= f;
@@ -361,7 +377,7 @@ __device__ __forceinline__ void stat_add(Stat& s, float x, const StatScale& k)
 {
     if (!(x <= s.m)) stat_rebase(s, max_nan(s.m, x), k);
     if (x == -INFINITY) return;
-    const float u = fmaxf(s.m < k.low_max ? (x - s.m) * k.c : __fmaf_rn(x, k.c, -(s.m * k.c)), kMinExp);
+    const float u = exponent(x, s.m, k.c);
     const float e = ex2(u);
     s.S += e;
     s.U = __fmaf_rn(e, u, s.U);
@@ -376,6 +392,15 @@ struct ThreadStat {
     F2 S = 0, U = 0;
     int best = 0;
     float second = -INFINITY;
+
+    // The exponent of what is summed so far against a new maximum mm.
+    __device__ __forceinline__ float step(float mm, const StatScale& k) const
+    {
+        const float a = m * k.c, b = mm * k.c;
+        if (a >= -k.most && b <= k.most) return fmaxf(a - b, kMinExp);   // a <= b: both fused
+        if (k.fused(b)) return fmaxf(__fmaf_rn(m, k.c, -b), kMinExp);
+        return k.fused(a) ? fmaxf(-__fmaf_rn(mm, k.c, -a), kMinExp) : exponent(m, mm, k.c);
+    }
 
     // N vectors at once, the first of them number i.
     template <int N>
@@ -392,42 +417,46 @@ struct ThreadStat {
                 for (int l = 0; l < N; ++l) kept[l * NT + threadIdx.x] = w[l];
             }
             const float mm = max_nan(m, vm);
-            const float d = max_step(m, mm, k);
+            const float d = step(mm, k);
             const F2 f = pack2(ex2(d), ex2(d));
             if (ENT) U = fma2(f, fma2(pack2(d, d), S, U), 0);
             S = fma2(f, S, 0);
             m = mm;
         }
-        if (m < k.low_max) {
+        const float mc = m * k.c;
+        const auto term = [&](F2 u) {
+            const F2 e = ex2x2(u);
+            S = add2(S, e);
+            if (ENT) U = fma2(e, u, U);
+        };
+        if (k.fused(mc)) {
+            const F2 c2 = pack2(k.c, k.c), b2 = pack2(-mc, -mc);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                float x[kV];
-                El<DT>::unpack(w[i], x);
-                Stat s{m, 0.0f, 0.0f};
-                for (int j = 0; j < kV; ++j) stat_add(s, x[j], k);
-                S = add2(S, pack2(s.S, 0.0f));
-                U = add2(U, pack2(s.U, 0.0f));
+                F2 x[kV / 2];
+                El<DT>::pairs_above(w[i], kLowest, x);
+#pragma unroll
+                for (int j = 0; j < kV / 2; ++j) term(fma2(x[j], c2, b2));
             }
-            return;
-        }
-        const F2 c2 = pack2(k.c, k.c), b2 = pack2(-(m * k.c), -(m * k.c));
+        } else if (m != -INFINITY) {          // else nothing but masked elements so far
+            const F2 h2 = pack2(0.5f, 0.5f), b2 = pack2(-0.5f * m, -0.5f * m);
+            const F2 c2 = pack2(2.0f * k.c, 2.0f * k.c);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            F2 x[kV / 2];
-            El<DT>::pairs_above(w[i], kLowest, x);
+            for (int i = 0; i < N; ++i) {
+                F2 x[kV / 2];
+                El<DT>::pairs(w[i], x);
 #pragma unroll
-            for (int j = 0; j < kV / 2; ++j) {
-                const F2 u = fma2(x[j], c2, b2);
-                const F2 e = pack2(ex2(lo2(u)), ex2(hi2(u)));
-                S = add2(S, e);
-                if (ENT) U = fma2(e, u, U);
+                for (int j = 0; j < kV / 2; ++j) {
+                    const F2 u = mul2(fma2(x[j], h2, b2), c2);
+                    term(pack2(fmaxf(lo2(u), kMinExp), fmaxf(hi2(u), kMinExp)));
+                }
             }
         }
     }
 
-    __device__ __forceinline__ Stat get() const
+    __device__ __forceinline__ Stat get(const StatScale& k) const
     {
-        return {m, lo2(S) + hi2(S), ENT ? lo2(U) + hi2(U) : 0.0f};
+        return unshifted({m, lo2(S) + hi2(S), ENT ? lo2(U) + hi2(U) : 0.0f}, k);
     }
 };
 
@@ -435,7 +464,7 @@ struct ThreadStat {
 // vectors instead of the running maximum: the reference cancels in the result,
 // and nothing has to be compared or rescaled, a third fewer instructions.
 // Elements so far above the reference that S passes kRefSumMax, NaN, +inf and
-// a reference too low for the fused exponent show in good(); the thread's
+// a reference too large for the fused form show in good(); the thread's
 // vectors then go through ThreadStat.  With S below 2^60 no join of up to 2^11
 // threads' sums overflows, and a sum that a join's factor 2^d flushes to zero
 // (d < -126) was at most 2^-66 of the others.
@@ -466,10 +495,13 @@ struct RefStat {
 
     __device__ __forceinline__ bool good(const StatScale& k) const
     {
-        return ref == -INFINITY || (ref >= k.low_max && lo2(S) + hi2(S) < kRefSumMax);
+        return ref == -INFINITY || (k.fused(ref * k.c) && lo2(S) + hi2(S) < kRefSumMax);
     }
 
-    __device__ __forceinline__ Stat get() const { return {ref, lo2(S) + hi2(S), 0.0f}; }
+    __device__ __forceinline__ Stat get(const StatScale& k) const
+    {
+        return unshifted({ref, lo2(S) + hi2(S), 0.0f}, k);
+    }
 };
 
 // Adds this thread's vectors of a slice from number i on: full batches of
@@ -595,27 +627,23 @@ struct RowResult {
     bool empty, bad;
 };
 
-__device__ __forceinline__ RowResult row_result(const Stat& s, float scale, const StatScale& k)
+__device__ __forceinline__ RowResult row_result(const Stat& s, float scale)
 {
     RowResult r;
     r.empty = s.m == -INFINITY;
     r.bad = !(s.m < INFINITY);
     r.log2S = log2f(s.S);
-    r.lse = r.bad ? quiet_nan()
-            : r.empty ? -INFINITY
-            : s.m < k.low_max ? __fmaf_rn(s.m, scale, r.log2S * kLn2)
-                              : (s.m * k.c + r.log2S) * kLn2;
+    r.lse = r.bad ? quiet_nan() : r.empty ? -INFINITY : __fmaf_rn(s.m, scale, r.log2S * kLn2);
     r.entropy = r.bad ? quiet_nan() : r.empty ? 0.0f : (r.log2S - s.U / s.S) * kLn2;
     return r;
 }
 
-__device__ __forceinline__ float logprob_of(float x, const Stat& s, const RowResult& r, float scale,
-                                            const StatScale& k)
+__device__ __forceinline__ float logprob_of(float x, const Stat& s, const RowResult& r, float scale)
 {
     if (r.bad) return quiet_nan();
     if (r.empty) return -INFINITY;
-    if (s.m < k.low_max || x < kLowest) return __fmaf_rn(x - s.m, scale, -r.log2S * kLn2);
-    return (__fmaf_rn(x, k.c, -(s.m * k.c)) - r.log2S) * kLn2;
+    // of halves, as in exponent()
+    return __fmaf_rn(0.5f * x - 0.5f * s.m, 2.0f * scale, -r.log2S * kLn2);
 }
 
 // ------------------------------------------------------------ gradients

@@ -36,7 +36,9 @@ def soft64(z):
 
 
 def within(got, want, tol, what):
+    """Values beyond fp32's largest are infinite there."""
     got, want = got.double(), want.double()
+    want = torch.where(want.abs() > torch.finfo(torch.float32).max, want * float("inf"), want)
     bad = ~(((got - want).abs() <= tol) | (got == want))
     if bool(bad.any()):
         i = tuple(bad.nonzero()[0].tolist())
@@ -52,8 +54,9 @@ def teacher(T, V, K, seed):
     return ids, torch.randn(T, K, generator=g, device="cuda") * 2
 
 
-def check_distill(dpz, x, tau, K, seed, weight=None):
-    """lm_distill and lm_distill_step on x against the definition in 64 bits."""
+def check_distill(dpz, x, tau, K, seed, weight=None, grad=True):
+    """lm_distill and lm_distill_step (grad: its gradient too) on x against the
+    definition in 64 bits."""
     T, V = x.shape
     bf16 = x.dtype == torch.bfloat16
     ids, t = teacher(T, V, K, seed)
@@ -77,6 +80,8 @@ def check_distill(dpz, x, tau, K, seed, weight=None):
     dpz.lm_distill_step(x, ids, t, w, got_loss, dx, lse=got_lse, temperature=tau)
     within(got_lse, lse, tol_lse, "lse of the step")
     within(got_loss, loss, tol_loss, "loss of the step")
+    if not grad:
+        return
     p = logp.exp()
     # of p: its exponent's roundings and log2(S)'s error; of q: the teacher's softmax
     tol = p * U * (base + 8 * (logp.clamp(min=-200).abs() + 1))
@@ -114,3 +119,67 @@ def filled_rows(T, V, dt, tau, seed):
 @pytest.mark.parametrize("tau", [1.0, 0.5])
 def test_first_elements_far_below_the_row(dpz, T, V, dt, tau):
     check_distill(dpz, filled_rows(T, V, dt, tau, V + T), tau, 24, T)
+
+
+def large_rows(V, dt, seed):
+    """Rows of one value and rows around one, of all magnitudes; one large element
+    among ordinary ones; ordinary elements among masked ones, and masked ones alone."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rand = lambda: torch.randn(V, generator=g, device="cuda").double() * 4  # noqa: E731
+    rows = []
+    for a in (1e4, 3e5, 7.25e5, 7.2682e5, 7.27e5, 9.08e5, 1e6, 1e7, 1e9, 5e9, 1e10, 1e11, 1e12,
+              1e15, 1e18, 2e19, 1e25, 1e30):
+        for v in (a, -a):
+            rows += [torch.full((V,), v, device="cuda", dtype=torch.float64), v + rand()]
+        rows.append(rand())
+        rows[-1][V // 3] = a
+        rows.append(torch.where(torch.arange(V, device="cuda") % 5 < 4, -a, rand()))
+        rows.append(torch.where(torch.arange(V, device="cuda") % 5 < 4, -float("inf"), -a))
+    return torch.stack(rows).to(DT[dt])
+
+
+def largest_rows(V, dt):
+    """Rows of the type's largest and lowest values."""
+    hi, lo = torch.finfo(DT[dt]).max, torch.finfo(DT[dt]).min
+    j = torch.arange(V, device="cuda")
+    zero = torch.zeros(V, device="cuda")
+    rows = [zero + hi, zero + lo, torch.where(j == V // 2, hi, zero), torch.where(j < V // 2, lo, zero),
+            torch.where(j % 3 == 0, hi, lo), torch.where(j == V - 1, -float("inf"), zero + hi)]
+    return torch.stack(rows).to(DT[dt])
+
+
+@pytest.mark.parametrize("V", [9, 700, 8200, 50257])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [1.0, 1.25, 2.0, 1e-3, 1e-30])
+def test_logprobs_of_large_logits(dpz, V, dt, scale):
+    """Log probabilities and entropy do not depend on a row's common value."""
+    x = torch.cat([large_rows(V, dt, V), largest_rows(V, dt)])
+    T, K = x.shape[0], min(V, 8)
+    z = x.double() * float(np.float32(scale))
+    lse, H, logp = soft64(z)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    y = torch.randint(0, V, (T,), generator=g, device="cuda")
+    top = torch.sort(x.double(), dim=1, descending=True, stable=True).indices[:, :K]
+    base = R.chain(V) + 256
+    tol_p = U * (base + 8 * logp.abs())
+    for k in (0, K):
+        lp, ls, h = (torch.empty(T, device="cuda") for _ in range(3))
+        ti, tl = torch.empty(T, K, dtype=torch.int64, device="cuda"), torch.empty(T, K, device="cuda")
+        dpz.lm_logprobs(x, y, lp, lse=ls, entropy=h, top_ids=ti if k else None,
+                        top_logprobs=tl if k else None, scale=scale)
+        within(ls, lse, U * (base + 8 * lse.abs()), "lse")
+        within(lp, logp.gather(1, y[:, None])[:, 0], tol_p.gather(1, y[:, None])[:, 0], "logprob")
+        within(h, H, U * (R.chain(V) * (4 + 2 * np.log(V + 1.0)) + 256), "entropy")
+        dpz.lm_logprobs(x, y, lp, lse=ls, scale=scale)
+        within(ls, lse, U * (base + 8 * lse.abs()), "lse without entropy")
+    assert torch.equal(ti, top)
+    within(tl, logp.gather(1, top), tol_p.gather(1, top), "top log probabilities")
+
+
+@pytest.mark.parametrize("V", [40, 2000, 24577, 50257])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("tau", [1.0, 2.0])
+@pytest.mark.parametrize("copies", [1, 3])        # 126 and 378 rows: clusters, a block a row
+def test_distillation_loss_of_large_logits(dpz, V, dt, tau, copies):
+    x = large_rows(V, dt, V + 1).repeat(copies, 1)
+    check_distill(dpz, x, tau, 24, 7, grad=False)
