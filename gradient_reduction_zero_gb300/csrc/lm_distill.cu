@@ -194,7 +194,7 @@ __device__ __forceinline__ void write_loss(const DistillArgs& a, int64_t t, cons
     }
 }
 
-// The gradient without the teacher's part: (w / tau) p, in pairs.
+// The gradient without the teacher's part: (w / tau) p, in pairs.  From lse:
 struct StudentGrad {
     F2 it, l, e, ws;
     __device__ __forceinline__ StudentGrad(float inv_tau, float lse, float weight)
@@ -206,29 +206,46 @@ struct StudentGrad {
     __device__ __forceinline__ F2 operator()(F2 x) const { return mul2(ws, p(x)); }
 };
 
-// The same for a bf16 result with w > 0 and an ordinary lse, with everything in
-// one exponent: 2^(x log2(e) / tau + log2(w / tau) - lse log2(e)).  The
-// constant's rounding, 2^-24 of a few tens, is far below the result's.
-struct StudentGradExp {
-    F2 c, b;
-    __device__ __forceinline__ StudentGradExp(float inv_tau, float lse, float weight)
+// From the row's statistics, p = 2^((x - m) c - log2 S): lse, which holds a
+// large m's sum only to 2^-24 of it, is not passed through.
+struct StepGrad {
+    F2 m, c, l, ws;
+    __device__ __forceinline__ StepGrad(const StatScale& k, const Stat& s, const RowResult& r,
+                                        float weight)
+        : m(pack2(-s.m, -s.m)), c(pack2(k.c, k.c)), l(pack2(-r.log2S, -r.log2S)),
+          ws(pack2(weight, weight))
     {
-        const float cc = inv_tau * kLog2e, bb = __fmaf_rn(-lse, kLog2e, log2f(weight));
-        c = pack2(cc, cc);
+    }
+    __device__ __forceinline__ F2 p(F2 x) const { return ex2x2(fma2(add2(x, m), c, l)); }
+    __device__ __forceinline__ F2 operator()(F2 x) const { return mul2(ws, p(x)); }
+};
+
+// The same for a bf16 result with w > 0 and |m c| up to 2^10, with everything
+// in one exponent: 2^(x c + log2(w / tau) - log2 S - m c).  The roundings of m c
+// and of the constant, below 2^11, are at most 2^-13 together, a fiftieth of
+// the result's own half unit (2^-9 to 2^-8).
+struct StepGradExp {
+    F2 c, b;
+    __device__ __forceinline__ StepGradExp(const StatScale& k, const Stat& s, const RowResult& r,
+                                           float weight)
+    {
+        const float bb = (log2f(weight) - r.log2S) - s.m * k.c;
+        c = pack2(k.c, k.c);
         b = pack2(bb, bb);
     }
-    static __device__ __forceinline__ bool holds(int DT, float lse, float weight)
+    static __device__ __forceinline__ bool holds(int DT, const StatScale& k, const Stat& s,
+                                                 float weight)
     {
-        return DT == DPZ_BF16 && weight > 0.0f && fabsf(lse) < 1e6f;
+        return DT == DPZ_BF16 && weight > 0.0f && fabsf(s.m * k.c) <= 1024.0f;
     }
     __device__ __forceinline__ F2 operator()(F2 x) const { return ex2x2(fma2(x, c, b)); }
 };
 
 // The elements of the teacher's tokens in a slice again, now with their q, by
 // one warp.  An entry that repeats an earlier one's token leaves it to that one.
-template <int DT>
+template <int DT, class F>
 __device__ __forceinline__ void write_teacher_part(const DistillArgs& a, const Teacher& w,
-                                                   const Slice& s, const StudentGrad& f, char* out)
+                                                   const Slice& s, const F& f, char* out)
 {
     const int lane = threadIdx.x & 31;
     const auto value = [&](float x, float q) { return lo2(f.ws) * (lo2(f.p(pack2(x, 0.0f))) - q); };
@@ -455,7 +472,7 @@ __global__ void __launch_bounds__(NT + 32, kStepBlocks) k_distill_step(DistillAr
             barrier_wait<NT + 32>();
             if (wt == 0.0f || !w[b].any || r.lse == -INFINITY) continue;
             write_teacher_part<DT>(a, w[b], row_slice<DT>(row_of(t), a.V, rank, n),
-                                   StudentGrad(a.inv_tau, r.lse, wt * a.inv_tau),
+                                   StepGrad(k, s, r, wt * a.inv_tau),
                                    a.dx.p + t * a.dx.ld * kB);
         }
         return;
@@ -523,11 +540,11 @@ __global__ void __launch_bounds__(NT + 32, kStepBlocks) k_distill_step(DistillAr
         if (lane == 0) ssh[b].warp[wid] = mine;
         __syncthreads();
         const Stat s = step_stat<NT>(k, ssh[b], rank, n);
-        const float lse = row_result(s, a.inv_tau).lse;
+        const RowResult r = row_result(s, a.inv_tau);
         char* out = a.dx.p + t * a.dx.ld * kB;
         const bool same = same_alignment(row, out);
-        const bool zero = wt == 0.0f || !w[b].any || lse == -INFINITY;
-        const StudentGrad f(a.inv_tau, lse, wt * a.inv_tau);
+        const bool zero = wt == 0.0f || !w[b].any || r.lse == -INFINITY;
+        const StepGrad f(k, s, r, wt * a.inv_tau);
         char* q = out + sl.vec0 * kB + (int64_t)first * 16;
         // the next row's copies take the places as they become free
         const bool more = t + step < a.T;
@@ -535,9 +552,9 @@ __global__ void __launch_bounds__(NT + 32, kStepBlocks) k_distill_step(DistillAr
         const Slice ns = row_slice<DT>(next, a.V, rank, n);
         const int will = more ? staged_of(ns) : 0;
         const char* np = next + ns.vec0 * kB + (int64_t)first_of(ns) * 16;
-        const int both = same && !zero && StudentGradExp::holds(DT, lse, wt * a.inv_tau)
+        const int both = same && !zero && StepGradExp::holds(DT, k, s, wt * a.inv_tau)
                              ? min(have, will) : 0;
-        const StudentGradExp fe(a.inv_tau, lse, wt * a.inv_tau);
+        const StepGradExp fe(k, s, r, wt * a.inv_tau);
 #pragma unroll 1
         for (int g = 0; g < kStageGroups; ++g) {
             int i = g * per;
@@ -595,20 +612,20 @@ __global__ void __launch_bounds__(NT + 32, kRereadBlocks<NT>) k_distill_step_rer
         if (rank == 0) write_loss(a, t, w, s, r);
         barrier_wait<NT + 32>();
         if (wt == 0.0f || !w.any || r.lse == -INFINITY) return;
-        write_teacher_part<DT>(a, w, sl, StudentGrad(a.inv_tau, r.lse, wt * a.inv_tau), out);
+        write_teacher_part<DT>(a, w, sl, StepGrad(k, s, r, wt * a.inv_tau), out);
         return;
     }
     const Stat s = row_stat<NT>(slice_stat<DT, NT>(row, sl, k), k, ssh, rank, n, [] {});
-    const float lse = row_result(s, a.inv_tau).lse;
-    if (wt == 0.0f || !w.any || lse == -INFINITY) zero_slice<DT, NT>(out, sl);
+    const RowResult r = row_result(s, a.inv_tau);
+    if (wt == 0.0f || !w.any || r.lse == -INFINITY) zero_slice<DT, NT>(out, sl);
     else {
         const int first = sl.lo + threadIdx.x;
         uint4 v[kMapLoads];
         map_load<DT, NT>(row, sl, first, v);
-        if (StudentGradExp::holds(DT, lse, wt * a.inv_tau))
-            map_row<DT, NT>(row, out, sl, first, v, StudentGradExp(a.inv_tau, lse, wt * a.inv_tau));
+        if (StepGradExp::holds(DT, k, s, wt * a.inv_tau))
+            map_row<DT, NT>(row, out, sl, first, v, StepGradExp(k, s, r, wt * a.inv_tau));
         else
-            map_row<DT, NT>(row, out, sl, first, v, StudentGrad(a.inv_tau, lse, wt * a.inv_tau));
+            map_row<DT, NT>(row, out, sl, first, v, StepGrad(k, s, r, wt * a.inv_tau));
     }
     barrier_arrive<NT + 32>();
 }

@@ -621,7 +621,8 @@ __device__ __forceinline__ Stat row_stat_beside(const StatScale& k, StatShared<N
     return blocks_stat(k, sh, n);
 }
 
-// lse and entropy of a row's statistics; m NaN or +inf: NaN, m -inf: -inf and 0.
+// log2 of S, lse and entropy of a row's statistics; m NaN or +inf: NaN, m -inf:
+// lse -inf and entropy 0.
 struct RowResult {
     float lse, log2S, entropy;
     bool empty, bad;
@@ -632,7 +633,7 @@ __device__ __forceinline__ RowResult row_result(const Stat& s, float scale)
     RowResult r;
     r.empty = s.m == -INFINITY;
     r.bad = !(s.m < INFINITY);
-    r.log2S = log2f(s.S);
+    r.log2S = r.bad ? quiet_nan() : log2f(s.S);
     r.lse = r.bad ? quiet_nan() : r.empty ? -INFINITY : __fmaf_rn(s.m, scale, r.log2S * kLn2);
     r.entropy = r.bad ? quiet_nan() : r.empty ? 0.0f : (r.log2S - s.U / s.S) * kLn2;
     return r;

@@ -406,7 +406,11 @@ DPZ_API int lm_logprobs(const void* logits, int64_t ld, int64_t T, int64_t V, in
  * dentropy may be NULL (zero; entropy is then not read).  Where the id names
  * no token, dlogprob counts as 0.  A row whose two gradients are 0, or whose
  * lse is -inf, is zeros (its logits are not read).  dlogits [T][V] (dtype)
- * may be logits itself (same address and stride). */
+ * may be logits itself (same address and stride).
+ * p_j = exp(z_j - lse[t]) with lse as given, in fp32: lse's own rounding is an
+ * error of p of up to 2^-24 |lse|, relative, and an lse beyond 1e6 no longer
+ * holds log V.  A row wholly masked by a large finite value instead of -inf
+ * wants weights of 0. */
 DPZ_API int lm_logprobs_grad(const void* logits, int64_t ld, int64_t T, int64_t V, int dtype,
                              float scale, const void* targets, int itype, const float* lse,
                              const float* entropy, const float* dlogprob, const float* dentropy,
@@ -429,7 +433,8 @@ DPZ_API int lm_distill(const void* logits, int64_t ld, int64_t T, int64_t V, int
 /* Gradient of sum_t dloss[t] * loss[t] with respect to the logits, from lse:
  *     dlogits[t, j] = R(dloss[t] / tau * (p_j - sum over k with id j of q_k))
  * Rows with dloss 0, without entries or with lse -inf are zeros.  dlogits
- * [T][V] (dtype) may be logits itself (same address and stride). */
+ * [T][V] (dtype) may be logits itself (same address and stride).  p_j comes
+ * from lse as lm_logprobs_grad's does, with the same error. */
 DPZ_API int lm_distill_grad(const void* logits, int64_t ld, int64_t T, int64_t V, int dtype,
                             const void* teacher_ids, int itype, const void* teacher_logits,
                             int tdtype, int K, float temperature, const float* lse,
@@ -438,7 +443,8 @@ DPZ_API int lm_distill_grad(const void* logits, int64_t ld, int64_t T, int64_t V
 /* lm_distill and lm_distill_grad in one pass, for a training step that knows
  * its rows' weights dloss beforehand (1 / tokens, or 0 for padding): the
  * logits are read from memory once.  Here a row with dloss 0 still gets its
- * loss and lse. */
+ * loss and lse, and p_j does not pass through lse's rounding: a value common
+ * to a row's logits does not change its gradient. */
 DPZ_API int lm_distill_step(const void* logits, int64_t ld, int64_t T, int64_t V, int dtype,
                             const void* teacher_ids, int itype, const void* teacher_logits,
                             int tdtype, int K, float temperature, const float* dloss, float* loss,

@@ -183,3 +183,27 @@ def test_logprobs_of_large_logits(dpz, V, dt, scale):
 def test_distillation_loss_of_large_logits(dpz, V, dt, tau, copies):
     x = large_rows(V, dt, V + 1).repeat(copies, 1)
     check_distill(dpz, x, tau, 24, 7, grad=False)
+
+
+def shifted_rows(V, dt, seed):
+    """N(0, 4) on top of a value common to the row, some of it masked."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    shifts = (0.0, 50.0, -300.0, 700.0, 2e3, -1e4, 1.5e4, 3e4, -1e5, 5e5)
+    z = torch.randn(len(shifts), V, generator=g, device="cuda") * 4
+    z = z + torch.tensor(shifts, device="cuda")[:, None]
+    z[:, V // 3::7] = -float("inf")
+    return z.to(DT[dt])
+
+
+@pytest.mark.parametrize("V", [40, 2000, 12289, 24577, 50257])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("tau", [1.0, 2.0])
+@pytest.mark.parametrize("copies", [1, 3])
+def test_step_gradient_does_not_depend_on_the_rows_level(dpz, V, dt, tau, copies):
+    """p of the step against a softmax in 64 bits, not against the returned lse;
+    rows of one value are uniform whatever the value."""
+    low = torch.full((1, V), torch.finfo(DT[dt]).min, device="cuda").to(DT[dt])
+    x = torch.cat([large_rows(V, dt, V + 2), shifted_rows(V, dt, V), low]).repeat(copies, 1)
+    T = x.shape[0]
+    for sign in (1.0, -1.0):
+        check_distill(dpz, x, tau, 24, 8, weight=sign * torch.linspace(0.5, 2.0, T, device="cuda"))
