@@ -544,7 +544,6 @@ __global__ void __launch_bounds__(NT + 32, kStepBlocks) k_distill_step(DistillAr
         char* out = a.dx.p + t * a.dx.ld * kB;
         const bool same = same_alignment(row, out);
         const bool zero = wt == 0.0f || !w[b].any || r.lse == -INFINITY;
-        const StepGrad f(k, s, r, wt * a.inv_tau);
         char* q = out + sl.vec0 * kB + (int64_t)first * 16;
         // the next row's copies take the places as they become free
         const bool more = t + step < a.T;
@@ -552,9 +551,12 @@ __global__ void __launch_bounds__(NT + 32, kStepBlocks) k_distill_step(DistillAr
         const Slice ns = row_slice<DT>(next, a.V, rank, n);
         const int will = more ? staged_of(ns) : 0;
         const char* np = next + ns.vec0 * kB + (int64_t)first_of(ns) * 16;
-        const int both = same && !zero && StepGradExp::holds(DT, k, s, wt * a.inv_tau)
-                             ? min(have, will) : 0;
+        // all of a row's elements in one form, whichever rows are beside it
+        const StepGrad f(k, s, r, wt * a.inv_tau);
         const StepGradExp fe(k, s, r, wt * a.inv_tau);
+        const bool exp = StepGradExp::holds(DT, k, s, wt * a.inv_tau);
+        const auto form = [&](F2 x) { return exp ? fe(x) : f(x); };
+        const int both = same && !zero && exp ? min(have, will) : 0;
 #pragma unroll 1
         for (int g = 0; g < kStageGroups; ++g) {
             int i = g * per;
@@ -567,7 +569,7 @@ __global__ void __launch_bounds__(NT + 32, kStepBlocks) k_distill_step(DistillAr
 #pragma unroll 1
             for (; i < end; ++i) {
                 if (i < have && !zero)
-                    map_vector<DT, false>(own[i * NT], q + i * (NT * 16), same, f);
+                    map_vector<DT, false>(own[i * NT], q + i * (NT * 16), same, form);
                 if (i < will) copy_async16(own + i * NT, np + i * (NT * 16));
             }
             copy_commit();
@@ -576,7 +578,7 @@ __global__ void __launch_bounds__(NT + 32, kStepBlocks) k_distill_step(DistillAr
         else {
             uint4 v[kMapLoads];
             map_load<DT, NT>(row, sl, first + have * NT, v);
-            map_row<DT, NT>(row, out, sl, first + have * NT, v, f);
+            map_row<DT, NT>(row, out, sl, first + have * NT, v, form);
         }
         barrier_arrive<NT + 32>();
         row = next;

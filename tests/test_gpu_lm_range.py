@@ -207,3 +207,25 @@ def test_step_gradient_does_not_depend_on_the_rows_level(dpz, V, dt, tau, copies
     T = x.shape[0]
     for sign in (1.0, -1.0):
         check_distill(dpz, x, tau, 24, 8, weight=sign * torch.linspace(0.5, 2.0, T, device="cuda"))
+
+
+@pytest.mark.parametrize("V", [2000, 12296, 24584, 50264, 60000])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_equal_rows_give_equal_bits(dpz, V, dt):
+    """A row's results depend on its values and alignment, not on its place in the
+    batch, the rows beside it or the alignment of the output."""
+    T, K = 650, 24
+    g = torch.Generator(device="cuda").manual_seed(V)
+    x = (torch.randn(1, V, generator=g, device="cuda") * 3).to(DT[dt]).repeat(T, 1)
+    ids, t = teacher(1, V, K, V)
+    ids, t = ids.repeat(T, 1), t.repeat(T, 1)
+    w = torch.full((T,), 1.0 / T, device="cuda")
+    first = None
+    for extra in (0, 8, 1):
+        out = torch.zeros(T, V + extra, dtype=DT[dt], device="cuda")[:, :V]
+        loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+        dpz.lm_distill_step(x, ids, t, w, loss, out, lse=lse)
+        for got in (loss, lse):
+            assert bool((got == got[0]).all())
+        first = out[0].clone() if first is None else first
+        assert torch.equal(out, first.expand(T, V))
