@@ -280,88 +280,118 @@ def dp_zero2_update(shards, master, m, v, weights, N: int, cfg: AdamWCfg, ws=Non
 # ------------------------------------------------------------ vocabulary-sized ends
 #
 # Shapes, strides, types and devices are checked here (the C call sees
-# addresses only); sizes, alignment and overlaps by the library.  The checks
-# ask a tensor for few things, because on a small call they are most of it.
+# addresses only, and launches on the current device); sizes, alignment and
+# overlaps by the library.  The checks ask a tensor for few things, because on
+# a small call they are most of it.
 
 _ID_CODES: dict = {}
+_float32 = None
 
 
 def _dtypes() -> dict:
     """Element and id type codes by torch dtype."""
+    global _float32
     if not _ID_CODES:
         torch = _torch()
         _ID_CODES.update({torch.int32: I32, torch.int64: I64})
         _CODES.update({torch.bfloat16: BF16, torch.float32: F32})
+        _float32 = torch.float32
     return _CODES
 
 
-def _current_stream(t, stream) -> int:
-    """The handle of `stream`, or of the current stream of t's device."""
-    if stream is not None:
-        return stream.cuda_stream
-    return _torch()._C._cuda_getCurrentRawStream(t.get_device())
+# The first call of each puts torch's own function in its place.
+
+def _current_device() -> int:
+    global _current_device
+    _current_device = _torch()._C._cuda_getDevice
+    return _current_device()
 
 
-def _bad_mat(t, what, rows, cols):
+def _raw_stream(dev: int) -> int:
+    """The handle of the GPU's current stream."""
+    global _raw_stream
+    _raw_stream = _torch()._C._cuda_getCurrentRawStream
+    return _raw_stream(dev)
+
+
+def _bad_device(t, what: str) -> None:
+    d = t.get_device()
+    raise ValueError(f"{what} must be a CUDA tensor, not on {t.device}" if d < 0 else
+                     f"{what} is on cuda:{d}, which is not the current device")
+
+
+def _current_stream(dev: int, stream) -> int:
+    """The handle of `stream`, or of the current stream of the GPU."""
+    if stream is None:
+        return _raw_stream(dev)
+    if getattr(stream, "device_index", dev) != dev:
+        raise ValueError(f"stream is of cuda:{stream.device_index}, the tensors are on cuda:{dev}")
+    return stream.cuda_stream
+
+
+def _bad_mat(t, what, dev, rows, cols):
     if t.dtype not in _dtypes():
         raise TypeError(f"{what}: unsupported dtype {t.dtype}")
     want = f" [{rows}, {cols}]" if rows >= 0 and cols >= 0 else ""
-    raise ValueError(f"{what} must be a CUDA matrix{want} of unit column stride, not "
+    raise ValueError(f"{what} must be a matrix{want} of unit column stride on cuda:{dev}, not "
                      f"{list(t.shape)} with strides {list(t.stride())} on {t.device}")
 
 
-def _mat(t, what: str, rows: int = -1, cols: int = -1) -> tuple:
+def _mat(t, what: str, dev: int, rows: int = -1, cols: int = -1) -> tuple:
     """(address, row stride, dtype code, rows, columns) of a 2-D matrix of unit
-    column stride on a GPU."""
+    column stride on GPU `dev`."""
     shape, strides = t.shape, t.stride()
     code = _dtypes().get(t.dtype)
-    if code is None or len(shape) != 2 or t.get_device() < 0:
-        _bad_mat(t, what, rows, cols)
+    if code is None or len(shape) != 2 or t.get_device() != dev:
+        _bad_mat(t, what, dev, rows, cols)
     r, c = shape
     ld, step = strides
     if (rows >= 0 and (r != rows or c != cols)) or (step != 1 and c > 1):
-        _bad_mat(t, what, rows, cols)
+        _bad_mat(t, what, dev, rows, cols)
     if r < 2 and ld < c:
         ld = c
     return t.data_ptr(), ld, code, r, c
 
 
-def _dense(t, what: str, n: int, k: int = 0, dtype=None):
-    """The address of a dense GPU tensor [n] ([n, k] with k) of fp32 (or dtype);
-    None for None."""
+def _dense(t, what: str, dev: int, n: int, k: int = 0, dtype=None):
+    """The address of a dense tensor [n] ([n, k] with k) of fp32 (or dtype) on
+    GPU `dev`; None for None."""
     if t is None:
         return None
     shape = t.shape
-    want = dtype or _torch().float32
+    want = dtype or _float32
     if t.dtype != want:
         raise TypeError(f"{what} must be {want}, not {t.dtype}")
     ok = len(shape) == 1 and shape[0] == n if not k else \
         len(shape) == 2 and shape[0] == n and shape[1] == k
-    if not ok or not t.is_contiguous() or t.get_device() < 0:
-        raise ValueError(f"{what} must be a dense CUDA tensor of shape "
-                         f"{[n, k] if k else [n]}, not {list(shape)}")
+    if not ok or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{what} must be a dense tensor of shape {[n, k] if k else [n]} on "
+                         f"cuda:{dev}, not {list(shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _tokens(t, what: str, n: int, k: int = 0) -> tuple:
+def _tokens(t, what: str, dev: int, n: int, k: int = 0) -> tuple:
     """(address, id type code) of token ids [n] or [n, k]."""
     _dtypes()
     code = _ID_CODES.get(t.dtype)
     if code is None:
         raise TypeError(f"{what} must be int32 or int64, not {t.dtype}")
-    return _dense(t, what, n, k, t.dtype), code
+    return _dense(t, what, dev, n, k, t.dtype), code
 
 
 def lm_embedding(table, ids, out, scale: float = 1.0, stream=None) -> None:
     """out[t] = scale * table[ids[t]] (a row of zeros where ids[t] is outside
     the table).  table [V, D] and out [T, D], bf16 or fp32 with any row
     stride; ids [T], int32 or int64."""
-    pt, ldt, tc, V, D = _mat(table, "table")
+    dev = table.get_device()
+    if dev != _current_device():     # the other tensors are compared with it
+        _bad_device(table, "table")
+    pt, ldt, tc, V, D = _mat(table, "table", dev)
     T = ids.numel()
-    po, ldo, oc, _, _ = _mat(out, "out", T, D)
-    p, it = _tokens(ids, "ids", T)
+    po, ldo, oc, _, _ = _mat(out, "out", dev, T, D)
+    p, it = _tokens(ids, "ids", dev, T)
     _check(_C.lm_embedding(pt, ldt, V, D, tc, p, it, T, scale, po, ldo, oc,
-                           _current_stream(out, stream)))
+                           _current_stream(dev, stream)))
 
 
 def lm_embedding_workspace(T: int, V: int, D: int, device=None):
@@ -377,20 +407,23 @@ def lm_embedding_grad(dout, ids, dtable, ws, base=None, scale: float = 1.0, stre
     base None: zeros; base may be dtable itself (rows of absent tokens are
     then left as they are).  dout [T, D], dtable and base [V, D]; ws:
     lm_embedding_workspace(T, V, D) or larger."""
-    pg, ldg, gc, V, D = _mat(dtable, "dtable")
+    dev = dtable.get_device()
+    if dev != _current_device():     # the other tensors are compared with it
+        _bad_device(dtable, "dtable")
+    pg, ldg, gc, V, D = _mat(dtable, "dtable", dev)
     T = ids.numel()
-    pd, ldd, dc, _, _ = _mat(dout, "dout", T, D)
-    p, it = _tokens(ids, "ids", T)
+    pd, ldd, dc, _, _ = _mat(dout, "dout", dev, T, D)
+    p, it = _tokens(ids, "ids", dev, T)
     pb, ldb = None, 0
     if base is not None:
-        pb, ldb, bc, _, _ = _mat(base, "base", V, D)
+        pb, ldb, bc, _, _ = _mat(base, "base", dev, V, D)
         if bc != gc:
             raise TypeError("base and dtable must have one dtype")
     need = lib.lm_embedding_workspace_bytes(T, V, D)
-    if ws.get_device() < 0 or not ws.is_contiguous() or ws.nbytes < need:
-        raise ValueError(f"ws must be a dense CUDA tensor of at least {need} bytes")
+    if ws.get_device() != dev or not ws.is_contiguous() or ws.nbytes < need:
+        raise ValueError(f"ws must be a dense tensor of at least {need} bytes on cuda:{dev}")
     _check(_C.lm_embedding_grad(pd, ldd, dc, p, it, T, scale, pb, ldb, pg, ldg, gc, V, D,
-                                ws.data_ptr(), _current_stream(dtable, stream)))
+                                ws.data_ptr(), _current_stream(dev, stream)))
 
 
 def lm_logprobs(logits, targets, logprob, lse=None, entropy=None, top_ids=None,
@@ -399,20 +432,23 @@ def lm_logprobs(logits, targets, logprob, lse=None, entropy=None, top_ids=None,
     logprob [T]; lse [T], entropy [T], and the K largest logits' ids (of
     targets' dtype) and log probabilities, top_ids and top_logprobs [T, K],
     where given.  logits [T, V], bf16 or fp32 with any row stride."""
-    px, ld, xc, T, V = _mat(logits, "logits")
-    p, it = _tokens(targets, "targets", T)
+    dev = logits.get_device()
+    if dev != _current_device():     # the other tensors are compared with it
+        _bad_device(logits, "logits")
+    px, ld, xc, T, V = _mat(logits, "logits", dev)
+    p, it = _tokens(targets, "targets", dev, T)
     K, pt, pl = 0, None, None
     if top_ids is not None:
         if top_ids.dim() != 2 or top_logprobs is None:
             raise ValueError("top_ids must be [T, K] and come with top_logprobs")
         K = top_ids.shape[1]
-        pt = _dense(top_ids, "top_ids", T, K, targets.dtype)
-        pl = _dense(top_logprobs, "top_logprobs", T, K)
+        pt = _dense(top_ids, "top_ids", dev, T, K, targets.dtype)
+        pl = _dense(top_logprobs, "top_logprobs", dev, T, K)
     elif top_logprobs is not None:
         raise ValueError("top_logprobs comes with top_ids")
-    _check(_C.lm_logprobs(px, ld, T, V, xc, scale, p, it, _dense(logprob, "logprob", T),
-                          _dense(lse, "lse", T), _dense(entropy, "entropy", T), K, pt, pl,
-                          _current_stream(logits, stream)))
+    _check(_C.lm_logprobs(px, ld, T, V, xc, scale, p, it, _dense(logprob, "logprob", dev, T),
+                          _dense(lse, "lse", dev, T), _dense(entropy, "entropy", dev, T), K, pt, pl,
+                          _current_stream(dev, stream)))
 
 
 def lm_logprobs_grad(logits, targets, lse, dlogprob, dlogits, entropy=None, dentropy=None,
@@ -420,31 +456,39 @@ def lm_logprobs_grad(logits, targets, lse, dlogprob, dlogits, entropy=None, dent
     """The gradient of lm_logprobs' logprob (weighted by dlogprob [T]) and
     entropy (by dentropy [T], with the entropy it gave) with respect to the
     logits, into dlogits, which may be logits itself."""
-    px, ld, xc, T, V = _mat(logits, "logits")
-    pd, ldd, dc, _, _ = _mat(dlogits, "dlogits", T, V)
+    dev = logits.get_device()
+    if dev != _current_device():     # the other tensors are compared with it
+        _bad_device(logits, "logits")
+    px, ld, xc, T, V = _mat(logits, "logits", dev)
+    pd, ldd, dc, _, _ = _mat(dlogits, "dlogits", dev, T, V)
     if dc != xc:
         raise TypeError("logits and dlogits must have one dtype")
-    p, it = _tokens(targets, "targets", T)
-    _check(_C.lm_logprobs_grad(px, ld, T, V, xc, scale, p, it, _dense(lse, "lse", T),
-                               _dense(entropy, "entropy", T), _dense(dlogprob, "dlogprob", T),
-                               _dense(dentropy, "dentropy", T), pd, ldd,
-                               _current_stream(logits, stream)))
+    p, it = _tokens(targets, "targets", dev, T)
+    _check(_C.lm_logprobs_grad(px, ld, T, V, xc, scale, p, it, _dense(lse, "lse", dev, T),
+                               _dense(entropy, "entropy", dev, T),
+                               _dense(dlogprob, "dlogprob", dev, T),
+                               _dense(dentropy, "dentropy", dev, T), pd, ldd,
+                               _current_stream(dev, stream)))
 
 
 def _distill_args(logits, teacher_ids, teacher_logits, temperature) -> tuple:
-    px, ld, xc, T, V = _mat(logits, "logits")
+    """The GPU and the arguments that the three calls have in common."""
+    dev = logits.get_device()
+    if dev != _current_device():     # the other tensors are compared with it
+        _bad_device(logits, "logits")
+    px, ld, xc, T, V = _mat(logits, "logits", dev)
     if teacher_ids.dim() != 2:
         raise ValueError(f"teacher_ids must be [T, K], not {list(teacher_ids.shape)}")
     K = teacher_ids.shape[1]
     if K == 0:
         raise ValueError("teacher_ids must have at least one column")
-    p, it = _tokens(teacher_ids, "teacher_ids", T, K)
+    p, it = _tokens(teacher_ids, "teacher_ids", dev, T, K)
     tc = _dtypes().get(teacher_logits.dtype)
     if tc is None:
         raise TypeError(f"teacher_logits: unsupported dtype {teacher_logits.dtype}")
-    return (px, ld, T, V, xc, p, it,
-            _dense(teacher_logits, "teacher_logits", T, K, teacher_logits.dtype), tc, K,
-            temperature)
+    return dev, (px, ld, T, V, xc, p, it,
+                 _dense(teacher_logits, "teacher_logits", dev, T, K, teacher_logits.dtype), tc,
+                 K, temperature)
 
 
 def lm_distill(logits, teacher_ids, teacher_logits, loss, lse=None, temperature: float = 1.0,
@@ -453,36 +497,37 @@ def lm_distill(logits, teacher_ids, teacher_logits, loss, lse=None, temperature:
     [T, K] (int32 or int64) and teacher_logits [T, K] (bf16 or fp32), softmax
     over the K entries at the given temperature, against softmax(logits /
     temperature) over the whole vocabulary.  loss and lse: [T]."""
-    args = _distill_args(logits, teacher_ids, teacher_logits, temperature)
+    dev, args = _distill_args(logits, teacher_ids, teacher_logits, temperature)
     T = args[2]
-    _check(_C.lm_distill(*args, _dense(loss, "loss", T), _dense(lse, "lse", T),
-                         _current_stream(logits, stream)))
+    _check(_C.lm_distill(*args, _dense(loss, "loss", dev, T), _dense(lse, "lse", dev, T),
+                         _current_stream(dev, stream)))
 
 
 def lm_distill_grad(logits, teacher_ids, teacher_logits, lse, dloss, dlogits,
                     temperature: float = 1.0, stream=None) -> None:
     """The gradient of sum(dloss * loss) of lm_distill with respect to the
     logits, from its lse, into dlogits, which may be logits itself."""
-    args = _distill_args(logits, teacher_ids, teacher_logits, temperature)
+    dev, args = _distill_args(logits, teacher_ids, teacher_logits, temperature)
     T, V = args[2], args[3]
-    pd, ldd, dc, _, _ = _mat(dlogits, "dlogits", T, V)
+    pd, ldd, dc, _, _ = _mat(dlogits, "dlogits", dev, T, V)
     if dc != args[4]:
         raise TypeError("logits and dlogits must have one dtype")
-    _check(_C.lm_distill_grad(*args, _dense(lse, "lse", T), _dense(dloss, "dloss", T), pd, ldd,
-                              _current_stream(logits, stream)))
+    _check(_C.lm_distill_grad(*args, _dense(lse, "lse", dev, T),
+                              _dense(dloss, "dloss", dev, T), pd, ldd,
+                              _current_stream(dev, stream)))
 
 
 def lm_distill_step(logits, teacher_ids, teacher_logits, dloss, loss, dlogits, lse=None,
                     temperature: float = 1.0, stream=None) -> None:
     """lm_distill and lm_distill_grad in one pass over the logits, for weights
     dloss [T] known beforehand; dlogits may be logits itself."""
-    args = _distill_args(logits, teacher_ids, teacher_logits, temperature)
+    dev, args = _distill_args(logits, teacher_ids, teacher_logits, temperature)
     T, V = args[2], args[3]
-    pd, ldd, dc, _, _ = _mat(dlogits, "dlogits", T, V)
+    pd, ldd, dc, _, _ = _mat(dlogits, "dlogits", dev, T, V)
     if dc != args[4]:
         raise TypeError("logits and dlogits must have one dtype")
-    _check(_C.lm_distill_step(*args, _dense(dloss, "dloss", T), _dense(loss, "loss", T),
-                              _dense(lse, "lse", T), pd, ldd, _current_stream(logits, stream)))
+    _check(_C.lm_distill_step(*args, _dense(dloss, "dloss", dev, T), _dense(loss, "loss", dev, T),
+                              _dense(lse, "lse", dev, T), pd, ldd, _current_stream(dev, stream)))
 
 
 class PreparedCall:

@@ -338,6 +338,7 @@ DPZ_API int dp_grad_global_norm_static(const void* grads, int64_t P, int N,
  *   Ids are DPZ_I32 or DPZ_I64; an id outside [0, V) names no token.
  *   Element types are DPZ_F32 or DPZ_BF16; arithmetic is fp32, with one
  *   rounding to the output's type at the end.
+ *   Kernels run on the current device, where all of a call's buffers must be.
  *   A call with T = 0 writes no row (lm_embedding_grad still writes dtable).
  *   Errors are as above: DPZ_ERR_INVALID_ARG for a NULL pointer, a size out
  *   of range, a stride below the row length, an unknown type, a scale that is
