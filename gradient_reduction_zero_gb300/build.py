@@ -22,8 +22,8 @@ LIB = os.path.join(PKG, "libdpz.so")
 
 SOURCES = ["api.cpp", "reduce.cu", "adamw.cu", "staged.cu", "norm_static.cu", "lm_api.cpp",
            "lm_embed.cu", "lm_logprobs.cu", "lm_distill.cu"]
-HEADERS = [os.path.join(CSRC, h) for h in ("internal.h", "api_util.h", "lm.h", "lm_rows.cuh",
-                                          "device.cuh", "bulk.cuh")] + \
+HEADERS = [os.path.join(CSRC, h) for h in ("internal.h", "api_util.h", "lm.h", "lm_shape.h",
+                                          "lm_rows.cuh", "device.cuh", "bulk.cuh")] + \
     [os.path.join(INCLUDE, "dpz.h")]
 
 NVCC_FLAGS = [

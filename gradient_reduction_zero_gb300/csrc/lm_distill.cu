@@ -632,44 +632,36 @@ __global__ void __launch_bounds__(NT + 32, kRereadBlocks<NT>) k_distill_step_rer
     barrier_arrive<NT + 32>();
 }
 
-// Blocks of a persistent kernel that fit on the GPU together, by the vectors
-// each thread stages; asked for once.
+// Blocks of a persistent kernel that fit on the current device together, by the
+// vectors each thread stages; asked for once.
 template <int DT, int NT>
-cudaError_t resident_blocks(int stage, int* blocks)
+cudaError_t resident_blocks(int stage, int sms, int* blocks)
 {
-    constexpr int kMost = kStageMax / (NT * 16);
-    static std::atomic<int> known[kMost + 1];
-    int got = known[stage].load(std::memory_order_relaxed);
-    if (got == 0) {
-        int dev = 0, sms = 0, per_sm = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e == cudaSuccess)
-            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_distill_step<DT, NT>, NT + 32,
-                                                              (size_t)stage * NT * 16);
-        if (e != cudaSuccess) return e;
-        got = std::max(1, sms * per_sm);
-        known[stage].store(got, std::memory_order_relaxed);
-    }
-    *blocks = got;
-    return cudaSuccess;
+    static PerDevice<kStageMax / (NT * 16) + 1> known;
+    return known.get(stage, blocks, [&](int, int* n) {
+        int per_sm = 0;
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+            &per_sm, k_distill_step<DT, NT>, NT + 32, (size_t)stage * NT * 16);
+        *n = std::max(1, sms * per_sm);
+        return e;
+    });
 }
 
 template <int DT, int NT>
-cudaError_t launch_step(const DistillArgs& a, cudaStream_t s)
+cudaError_t launch_step(const DistillArgs& a, int sms, cudaStream_t s)
 {
     static SmemRaisedOn raised;
     const int64_t bytes = row_bytes(a.V, DT);
     // two blocks where one cannot stage a row (4,096 rows of 50,257 fp32: 299 us,
     // 342 with one block that reads half of the row again; 2,048 of 128,256 bf16:
     // 216 and 238; with four blocks 350, their barriers being more than that)
-    const unsigned n = std::max(row_cluster(a.T, bytes, NT), bytes > kStageMax ? 2u : 1u);
+    const unsigned n = std::max(row_cluster(a.T, bytes, NT, sms), bytes > kStageMax ? 2u : 1u);
     const int64_t vecs = (bytes / 16 + n - 1) / n + 1;
     const int stage = (int)std::min<int64_t>((vecs + NT - 1) / NT, kStageMax / (NT * 16));
     cudaError_t e =
         raise_smem(raised, reinterpret_cast<const void*>(k_distill_step<DT, NT>), kStageMax);
     int blocks = 0;
-    if (e == cudaSuccess) e = resident_blocks<DT, NT>(stage, &blocks);
+    if (e == cudaSuccess) e = resident_blocks<DT, NT>(stage, sms, &blocks);
     if (e != cudaSuccess) return e;
     const unsigned grid = n * (unsigned)std::min<int64_t>(a.T, std::max(1u, blocks / n));
     return launch_kernel(k_distill_step<DT, NT>, dim3(grid), dim3(NT + 32), (size_t)stage * NT * 16, s,
@@ -677,13 +669,13 @@ cudaError_t launch_step(const DistillArgs& a, cudaStream_t s)
 }
 
 template <int DT>
-cudaError_t step_typed(const DistillArgs& a, cudaStream_t s)
+cudaError_t step_typed(const DistillArgs& a, int sms, cudaStream_t s)
 {
     const int64_t bytes = row_bytes(a.V, DT);
-    if (bytes > kMidRow) return launch_step<DT, kStepThreads>(a, s);
-    return by_row_threads(a.T, bytes, [&](auto threads) {
+    if (bytes > kMidRow) return launch_step<DT, kStepThreads>(a, sms, s);
+    return by_row_threads(a.T, bytes, sms, [&](auto threads) {
         constexpr int NT = threads;
-        const unsigned n = row_cluster(a.T, bytes, NT);
+        const unsigned n = row_cluster(a.T, bytes, NT, sms);
         return launch_kernel(k_distill_step_reread<DT, NT>, dim3((unsigned)a.T * n), dim3(NT + 32), 0,
                              s, true, n > 1 ? n : 0u, a);
     });
@@ -694,15 +686,18 @@ cudaError_t step_typed(const DistillArgs& a, cudaStream_t s)
 cudaError_t launch_distill(const DistillArgs& a, cudaStream_t s)
 {
     const bool b = a.x.dt == DPZ_BF16;
+    int sms = 0;
+    const cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
     if (a.loss != nullptr && a.dx.p != nullptr) {
         set_last_kernel_name("lm_distill_step");
-        return b ? step_typed<DPZ_BF16>(a, s) : step_typed<DPZ_F32>(a, s);
+        return b ? step_typed<DPZ_BF16>(a, sms, s) : step_typed<DPZ_F32>(a, sms, s);
     }
     const int64_t bytes = row_bytes(a.V, a.x.dt);
     set_last_kernel_name(a.loss != nullptr ? "lm_distill" : "lm_distill_grad");
-    return by_row_threads(a.T, bytes, [&](auto threads) {
+    return by_row_threads(a.T, bytes, sms, [&](auto threads) {
         constexpr int NT = threads;
-        unsigned n = row_cluster(a.T, bytes, NT);
+        unsigned n = row_cluster(a.T, bytes, NT, sms);
         if (a.loss != nullptr)
             return launch_kernel(b ? k_distill<DPZ_BF16, NT> : k_distill<DPZ_F32, NT>,
                                  dim3((unsigned)a.T * n), dim3(NT + 32), 0, s, true, n > 1 ? n : 0u,

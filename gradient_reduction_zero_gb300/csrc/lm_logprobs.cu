@@ -374,10 +374,13 @@ void (*logprobs_kernel(bool ent, bool top))(LogprobArgs)
 cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t s)
 {
     set_last_kernel_name("lm_logprobs");
+    int sms = 0;
+    const cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
     const bool ent = a.entropy != nullptr, top = a.K > 0, b = a.x.dt == DPZ_BF16;
-    return by_row_threads(a.T, row_bytes(a.V, a.x.dt), [&](auto threads) {
+    return by_row_threads(a.T, row_bytes(a.V, a.x.dt), sms, [&](auto threads) {
         constexpr int NT = threads;
-        const unsigned n = row_cluster(a.T, row_bytes(a.V, a.x.dt), NT);
+        const unsigned n = row_cluster(a.T, row_bytes(a.V, a.x.dt), NT, sms);
         void (*fn)(LogprobArgs) = b ? logprobs_kernel<DPZ_BF16, NT>(ent, top)
                                     : logprobs_kernel<DPZ_F32, NT>(ent, top);
         return launch_kernel(fn, dim3((unsigned)a.T * n), dim3(NT), 0, s, true, n > 1 ? n : 0u, a);
@@ -387,9 +390,12 @@ cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t s)
 cudaError_t launch_logprobs_grad(const LogprobGradArgs& a, cudaStream_t s)
 {
     set_last_kernel_name("lm_logprobs_grad");
-    return by_row_threads(a.T, row_bytes(a.V, a.x.dt), [&](auto threads) {
+    int sms = 0;
+    const cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    return by_row_threads(a.T, row_bytes(a.V, a.x.dt), sms, [&](auto threads) {
         constexpr int NT = threads;
-        const unsigned n = row_cluster(a.T, row_bytes(a.V, a.x.dt), NT);
+        const unsigned n = row_cluster(a.T, row_bytes(a.V, a.x.dt), NT, sms);
         return launch_kernel(a.x.dt == DPZ_BF16 ? k_logprobs_grad<DPZ_BF16, NT>
                                                 : k_logprobs_grad<DPZ_F32, NT>,
                              dim3((unsigned)a.T, n), dim3(NT), 0, s, true, 0u, a);

@@ -5,14 +5,13 @@
 #pragma once
 
 #include <algorithm>
-#include <atomic>
 #include <cmath>
-#include <type_traits>
 
 #include "bulk.cuh"
 #include "device.cuh"
 #include "internal.h"
 #include "lm.h"
+#include "lm_shape.h"
 
 namespace dpz {
 
@@ -277,8 +276,6 @@ __device__ __forceinline__ void store_rank_u64(uint64_t* p, unsigned rank, uint6
 {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr_of_rank(p, rank)), "l"(v) : "memory");
 }
-
-constexpr int kMaxCluster = 8;
 
 struct Slice {
     int head, lo, hi, tail;   // single elements, vectors [lo, hi), single elements
@@ -733,33 +730,6 @@ __device__ __forceinline__ void zero_slice(char* out, const Slice& s)
 
 // ------------------------------------------------------------ launch shapes
 
-// Threads per block for rows up to kShortRow bytes, up to kMidRow, and for
-// longer ones or up to kFewRows rows.  8,192 rows of bf16, in us:
-//
-//   logits                8,000 (16 KB)   16,000     24,000 (48 KB)
-//   threads               64  128  256   128  256     128  256
-//   log probabilities     27   30   40    47   55      66   70
-//   eight alternatives    44   49   61    68   77      88   91
-//   their gradient        39   37   42    71   71     107  104
-//   distillation loss     28   30   43    48   57      66   72
-//   its gradient          44   44   59    80   82     120  120
-//
-// Rows that all fit on the GPU at once want many threads each: 300 rows of 8,000
-// with eight alternatives take 7.4 us with 64 threads and 5.1 with 256, their
-// gradient 4.2 and 2.5; at 450 rows of 2,000, 5.5 and 4.6, but 2.4 and 2.9.
-constexpr int kRowThreads = 256, kMidThreads = 128, kShortThreads = 64;
-constexpr int64_t kShortRow = 16384, kMidRow = 49152, kFewRows = 304;
-
-// Calls f with the threads for T rows of this length, as a constant.
-template <class F>
-cudaError_t by_row_threads(int64_t T, int64_t bytes, F&& f)
-{
-    if (T <= kFewRows) return f(std::integral_constant<int, kRowThreads>{});
-    if (bytes <= kShortRow) return f(std::integral_constant<int, kShortThreads>{});
-    if (bytes <= kMidRow) return f(std::integral_constant<int, kMidThreads>{});
-    return f(std::integral_constant<int, kRowThreads>{});
-}
-
 // The distillation step's blocks for rows longer than kMidRow, and the most
 // shared memory each stages.  Shorter ones are read twice instead: 8,192 rows
 // of 16,000 bf16 take 92 us (staged 128; with blocks of 256 threads 99), of
@@ -783,22 +753,6 @@ constexpr int kGradBlocks = NT == kRowThreads ? 7 : NT == kMidThreads ? 8 : 20;
 template <int NT>
 constexpr int kRereadBlocks = NT == kRowThreads ? 4 : NT == kMidThreads ? 9 : 16;
 constexpr int kStepBlocks = 2;
-
-inline int64_t row_bytes(int V, int dt) { return (int64_t)V * (dt == DPZ_F32 ? 4 : 2); }
-
-// Blocks per row, a power of two up to 8.  With few rows, as many as keep one
-// wave of blocks on the GPU, each with at least one vector per thread; rows of
-// half a megabyte and more are split for up to two waves, which hides a
-// cluster's barriers (256 rows of 256,000 fp32: 76 us with one block, 55 with
-// 2, 61 with 4; 300 rows of 50,257 bf16: 16.5 us with one, 20 with 2).
-inline unsigned row_cluster(int64_t T, int64_t bytes, int threads)
-{
-    unsigned n = 1;
-    while (n < kMaxCluster && bytes >= (int64_t)2 * n * threads * 16 &&
-           (T * n * 2 <= 304 || (T * n * 2 <= 608 && bytes >= (int64_t)2 * n * (256 << 10))))
-        n *= 2;
-    return n;
-}
 
 }  // namespace
 
