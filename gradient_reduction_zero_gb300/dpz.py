@@ -426,24 +426,34 @@ def lm_embedding_grad(dout, ids, dtable, ws, base=None, scale: float = 1.0, stre
                                 ws.data_ptr(), _current_stream(dev, stream)))
 
 
-def lm_logprobs(logits, targets, logprob, lse=None, entropy=None, top_ids=None,
+def lm_logprobs(logits, targets=None, logprob=None, lse=None, entropy=None, top_ids=None,
                 top_logprobs=None, scale: float = 1.0, stream=None) -> None:
     """Log probabilities of `targets` [T] under softmax(scale * logits), into
-    logprob [T]; lse [T], entropy [T], and the K largest logits' ids (of
-    targets' dtype) and log probabilities, top_ids and top_logprobs [T, K],
-    where given.  logits [T, V], bf16 or fp32 with any row stride."""
+    logprob [T] (both or neither); lse [T], entropy [T], and the K largest
+    logits' ids (of targets' dtype, if given) and log probabilities, top_ids and
+    top_logprobs [T, K], where given.  logits [T, V], bf16 or fp32 with any row
+    stride."""
     dev = logits.get_device()
     if dev != _current_device():     # the other tensors are compared with it
         _bad_device(logits, "logits")
     px, ld, xc, T, V = _mat(logits, "logits", dev)
-    p, it = _tokens(targets, "targets", dev, T)
-    K, pt, pl = 0, None, None
+    if (targets is None) != (logprob is None):
+        raise ValueError("targets and logprob come together")
+    K, p, pt, pl, it = 0, None, None, None, I64
+    if targets is not None:
+        p, it = _tokens(targets, "targets", dev, T)
     if top_ids is not None:
         if top_ids.dim() != 2 or top_logprobs is None:
             raise ValueError("top_ids must be [T, K] and come with top_logprobs")
         K = top_ids.shape[1]
-        pt = _dense(top_ids, "top_ids", dev, T, K, targets.dtype)
-        pl = _dense(top_logprobs, "top_logprobs", dev, T, K)
+        if K > 0:
+            pt, kt = _tokens(top_ids, "top_ids", dev, T, K)
+            if targets is not None and kt != it:
+                raise TypeError("targets and top_ids must have one dtype")
+            it = kt
+            pl = _dense(top_logprobs, "top_logprobs", dev, T, K)
+        elif tuple(top_ids.shape) != (T, 0) or tuple(top_logprobs.shape) != (T, 0):
+            raise ValueError(f"top_ids and top_logprobs must be [{T}, K]")
     elif top_logprobs is not None:
         raise ValueError("top_logprobs comes with top_ids")
     _check(_C.lm_logprobs(px, ld, T, V, xc, scale, p, it, _dense(logprob, "logprob", dev, T),

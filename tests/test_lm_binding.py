@@ -103,3 +103,27 @@ def test_another_device_than_the_current_one_is_refused(lib, call):
     getattr(lib, call)(**arguments()[call], stream=Stream(0))
     assert [n for n, _ in lib.calls_made] == [call]
     assert lib.calls_made[0][1][-1] == Stream(0).cuda_stream
+
+
+def test_logprobs_without_targets(lib):
+    x, s = Fake(T, V), Stream(0)
+    lse, H = Fake(T), Fake(T)
+    lib.lm_logprobs(x, lse=lse, entropy=H, stream=s)
+    top, tl = Fake(T, K, dtype=torch.int32), Fake(T, K)
+    lib.lm_logprobs(x, top_ids=top, top_logprobs=tl, stream=s)
+    lib.lm_logprobs(x, ids(T), Fake(T), top_ids=ids(T, 0), top_logprobs=Fake(T, 0), stream=s)
+    a, b, c = (args for _, args in lib.calls_made)
+    # logits, ld, T, V, dtype, scale, targets, itype, logprob, lse, entropy, K, top ids, top log p
+    assert a[6:14] == (None, lib.I64, None, lse.data_ptr(), H.data_ptr(), 0, None, None)
+    assert b[6:14] == (None, lib.I32, None, None, None, K, top.data_ptr(), tl.data_ptr())
+    assert c[11:14] == (0, None, None)
+    for bad in (dict(targets=ids(T)), dict(logprob=Fake(T)), dict(top_ids=top),
+                dict(top_logprobs=tl), dict(top_ids=ids(T + 1, 0), top_logprobs=Fake(T + 1, 0)),
+                dict(top_ids=ids(T, 0), top_logprobs=Fake(T, 1))):
+        with pytest.raises(ValueError):
+            lib.lm_logprobs(x, **bad, stream=s)
+    for bad in (dict(top_ids=Fake(T, K), top_logprobs=tl),
+                dict(targets=ids(T), logprob=Fake(T), top_ids=top, top_logprobs=tl)):
+        with pytest.raises(TypeError):
+            lib.lm_logprobs(x, **bad, stream=s)
+    assert len(lib.calls_made) == 3
