@@ -72,6 +72,13 @@ int check_factor(float x, const char* what)
 
 int id_bytes(int it) { return it == DPZ_I32 ? 4 : 8; }
 
+// Whether two matrices of one size and type are the same elements: a single
+// row's stride says nothing.
+bool same_mat(const void* p, int64_t ldp, const void* q, int64_t ldq, int64_t rows)
+{
+    return p == q && (ldp == ldq || rows < 2);
+}
+
 // The bytes of one buffer of a call: `rows` rows of `width` bytes, `stride`
 // bytes apart.
 struct Block {
@@ -170,7 +177,7 @@ DPZ_API int lm_embedding_grad(const void* dout, int64_t ld_dout, int ddtype, con
     EmbGrad g{mat(dout, ld_dout, ddtype), mat(base, ld_base, gdtype),
               mat(dtable, ld_dtable, gdtype), Ids{ids, itype}, T, V, D, scale, {}};
     const size_t wsb = emb_ws_layout(ws, T, V, D, &g.ws);
-    const bool in_place = base == dtable && ld_base == ld_dtable;
+    const bool in_place = same_mat(base, ld_base, dtable, ld_dtable, V);
     DPZ_TRY(check_blocks({mat_block("dout", dout, ld_dout, T, D, ddtype, false),
                           vec_block("ids", ids, T * id_bytes(itype), false),
                           mat_block("base", in_place ? nullptr : base, ld_base, V, D, gdtype,
@@ -238,7 +245,7 @@ DPZ_API int lm_logprobs_grad(const void* logits, int64_t ld, int64_t T, int64_t 
             DPZ_TRY(check_addr(entropy, "entropy", 4));
         }
     }
-    const bool in_place = logits == dlogits && ld == ld_dlogits;
+    const bool in_place = same_mat(logits, ld, dlogits, ld_dlogits, T);
     DPZ_TRY(check_blocks({mat_block("logits", in_place ? nullptr : logits, ld, T, V, dtype, false),
                           vec_block("targets", targets, T * id_bytes(itype), false),
                           vec_block("lse", lse, T * 4, false),
@@ -278,7 +285,7 @@ static int distill_common(const void* logits, int64_t ld, int64_t T, int64_t V, 
         if (with_grad) DPZ_TRY(check_addr(dloss, "dloss", 4));
     }
     if (with_grad) DPZ_TRY(check_mat(dlogits, ld_dlogits, T, V, dtype, "dlogits"));
-    const bool in_place = with_grad && logits == dlogits && ld == ld_dlogits;
+    const bool in_place = with_grad && same_mat(logits, ld, dlogits, ld_dlogits, T);
     DPZ_TRY(check_blocks(
         {mat_block("logits", in_place ? nullptr : logits, ld, T, V, dtype, false),
          vec_block("teacher_ids", teacher_ids, T * K * id_bytes(itype), false),

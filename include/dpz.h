@@ -334,7 +334,8 @@ DPZ_API int dp_grad_global_norm_static(const void* grads, int64_t P, int N,
  *   Matrices are row-major with a row stride in elements (ld_*, at least the
  *   row's length), so that a table inside an arena or logits with padded rows
  *   need no copy.  Any stride and any element-aligned address is accepted;
- *   the fastest accesses need the alignment each call states.
+ *   the fastest accesses need the alignment each call states.  (A matrix of
+ *   one row is the same matrix whatever its stride.)
  *   Ids are DPZ_I32 or DPZ_I64; an id outside [0, V) names no token.
  *   Element types are DPZ_F32 or DPZ_BF16; arithmetic is fp32, with one
  *   rounding to the output's type at the end.
