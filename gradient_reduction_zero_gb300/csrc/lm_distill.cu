@@ -556,15 +556,15 @@ __global__ void __launch_bounds__(NT + 32, kStepBlocks) k_distill_step(DistillAr
         const StepGradExp fe(k, s, r, wt * a.inv_tau);
         const bool exp = StepGradExp::holds(DT, k, s, wt * a.inv_tau);
         const auto form = [&](F2 x) { return exp ? fe(x) : f(x); };
-        const int both = same && !zero && exp ? min(have, will) : 0;
+        const int fast = same && !zero && exp ? have : 0;   // vectors written without more checks
 #pragma unroll 1
         for (int g = 0; g < kStageGroups; ++g) {
             int i = g * per;
             const int end = min(i + per, max(have, will));
 #pragma unroll 4
-            for (; i < min(end, both); ++i) {
+            for (; i < min(end, fast); ++i) {
                 map_vector<DT, false>(own[i * NT], q + i * (NT * 16), true, fe);
-                copy_async16(own + i * NT, np + i * (NT * 16));
+                if (i < will) copy_async16(own + i * NT, np + i * (NT * 16));
             }
 #pragma unroll 1
             for (; i < end; ++i) {
