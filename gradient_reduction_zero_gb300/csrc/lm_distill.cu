@@ -287,7 +287,7 @@ __device__ __forceinline__ Stat slice_stat(const char* row, const Slice& sl, con
     RefStat<DT> rs;
     thread_rows<DT, NT>(rs, row, sl, sl.lo + threadIdx.x, k);
     Stat own = rs.get(k);
-    if (!rs.good(k)) {
+    if (!rs.good()) {
         ThreadStat<DT, NT, false, false> ts;
         thread_rows<DT, NT>(ts, row, sl, sl.lo + threadIdx.x, k);
         own = ts.get(k);
@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(NT + 32, kStepBlocks) k_distill_step(DistillAr
         }
         thread_rows<DT, NT>(rs, row, sl, first + have * NT, k);
         Stat mine = rs.get(k);
-        if (!rs.good(k)) {
+        if (!rs.good()) {
             ThreadStat<DT, NT, false, false> ts;
 #pragma unroll 1
             for (int i = 0; i < have; ++i) {

@@ -336,7 +336,7 @@ struct StatScale {
 // type's values may overflow.
 __device__ __forceinline__ float exponent(float x, float m, float c)
 {
-    return fmaxf((0.5f * x - 0.5f * m) * (2.0f * c), kMinExp);
+    return fmaxf(__fmaf_rn(0.5f, x, -0.5f * m) * (2.0f * c), kMinExp);
 }
 
 // A thread's S and U against rnd(m c), if that is the fused form's, against m c.
@@ -390,11 +390,12 @@ struct ThreadStat {
     int best = 0;
     float second = -INFINITY;
 
-    // The exponent of what is summed so far against a new maximum mm.
+    // The exponent of what is summed so far against a new maximum mm >= m; an
+    // infinite m c has nothing that counts.
     __device__ __forceinline__ float step(float mm, const StatScale& k) const
     {
         const float a = m * k.c, b = mm * k.c;
-        if (a >= -k.most && b <= k.most) return fmaxf(a - b, kMinExp);   // a <= b: both fused
+        if (b <= k.most && (a >= -k.most || a == -INFINITY)) return fmaxf(a - b, kMinExp);
         if (k.fused(b)) return fmaxf(__fmaf_rn(m, k.c, -b), kMinExp);
         return k.fused(a) ? fmaxf(-__fmaf_rn(mm, k.c, -a), kMinExp) : exponent(m, mm, k.c);
     }
@@ -436,12 +437,20 @@ struct ThreadStat {
                 for (int j = 0; j < kV / 2; ++j) term(fma2(x[j], c2, b2));
             }
         } else if (m != -INFINITY) {          // else nothing but masked elements so far
+            // such rows are rare: with alternatives in bf16 a loop, whose instructions,
+            // unrolled, cost short rows 5 % in fetching the others (8,192 of 2,000:
+            // 30.6 us, 29.2 so); in fp32 the loop's registers cost 4 %
             const F2 h2 = pack2(0.5f, 0.5f), b2 = pack2(-0.5f * m, -0.5f * m);
             const F2 c2 = pack2(2.0f * k.c, 2.0f * k.c);
-#pragma unroll
+            constexpr int kUnroll = TOP && DT == DPZ_BF16 ? 1 : N;
+#pragma unroll kUnroll
             for (int i = 0; i < N; ++i) {
+                uint4 v = w[0];
+#pragma unroll
+                for (int l = 1; l < N; ++l)
+                    if (i == l) v = w[l];
                 F2 x[kV / 2];
-                El<DT>::pairs(w[i], x);
+                El<DT>::pairs(v, x);
 #pragma unroll
                 for (int j = 0; j < kV / 2; ++j) {
                     const F2 u = mul2(fma2(x[j], h2, b2), c2);
@@ -460,9 +469,8 @@ struct ThreadStat {
 // A thread's S alone (U is left out), against the largest element of its first
 // vectors instead of the running maximum: the reference cancels in the result,
 // and nothing has to be compared or rescaled, a third fewer instructions.
-// Elements so far above the reference that S passes kRefSumMax, NaN, +inf and
-// a reference too large for the fused form show in good(); the thread's
-// vectors then go through ThreadStat.  With S below 2^60 no join of up to 2^11
+// Elements so far above the reference that S passes kRefSumMax, NaN and +inf
+// show in good(); the thread's vectors then go through ThreadStat.  With S below 2^60 no join of up to 2^11
 // threads' sums overflows, and a sum that a join's factor 2^d flushes to zero
 // (d < -126) was at most 2^-66 of the others.
 constexpr float kRefSumMax = 0x1p60f;
@@ -480,19 +488,32 @@ struct RefStat {
             ref = El<DT>::vec_max(w);
             if (ref == -INFINITY) return;     // nothing but masked elements so far
         }
-        const F2 c2 = pack2(k.c, k.c), b2 = pack2(-(ref * k.c), -(ref * k.c));
+        const float rc = ref * k.c;
+        if (k.fused(rc)) {
+            const F2 c2 = pack2(k.c, k.c), b2 = pack2(-rc, -rc);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            F2 x[kV / 2];
-            El<DT>::pairs(w[i], x);
+            for (int i = 0; i < N; ++i) {
+                F2 x[kV / 2];
+                El<DT>::pairs(w[i], x);
 #pragma unroll
-            for (int j = 0; j < kV / 2; ++j) S = add2(S, ex2x2(fma2(x[j], c2, b2)));
+                for (int j = 0; j < kV / 2; ++j) S = add2(S, ex2x2(fma2(x[j], c2, b2)));
+            }
+        } else {
+            const F2 h2 = pack2(0.5f, 0.5f), b2 = pack2(-0.5f * ref, -0.5f * ref);
+            const F2 c2 = pack2(2.0f * k.c, 2.0f * k.c);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                F2 x[kV / 2];
+                El<DT>::pairs(w[i], x);
+#pragma unroll
+                for (int j = 0; j < kV / 2; ++j) S = add2(S, ex2x2(mul2(fma2(x[j], h2, b2), c2)));
+            }
         }
     }
 
-    __device__ __forceinline__ bool good(const StatScale& k) const
+    __device__ __forceinline__ bool good() const
     {
-        return ref == -INFINITY || (k.fused(ref * k.c) && lo2(S) + hi2(S) < kRefSumMax);
+        return ref < INFINITY && lo2(S) + hi2(S) < kRefSumMax;
     }
 
     __device__ __forceinline__ Stat get(const StatScale& k) const
@@ -641,7 +662,7 @@ __device__ __forceinline__ float logprob_of(float x, const Stat& s, const RowRes
     if (r.bad) return quiet_nan();
     if (r.empty) return -INFINITY;
     // of halves, as in exponent()
-    return __fmaf_rn(0.5f * x - 0.5f * s.m, 2.0f * scale, -r.log2S * kLn2);
+    return __fmaf_rn(__fmaf_rn(0.5f, x, -0.5f * s.m), 2.0f * scale, -r.log2S * kLn2);
 }
 
 // ------------------------------------------------------------ gradients
