@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -215,6 +216,27 @@ inline cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 #endif
+
+// Devices on which a kernel's dynamic shared memory limit has been raised,
+// one bit per device (0..255): each launcher keeps one of these per kernel,
+// so a launch after the first costs one atomic load.
+struct SmemRaisedOn {
+    std::atomic<uint64_t> dev[4];
+};
+
+// Raise the kernel's dynamic shared memory limit on the current device, once.
+inline cudaError_t raise_smem(SmemRaisedOn& done, const void* fn, size_t smem)
+{
+    int d = 0;
+    cudaError_t e = cudaGetDevice(&d);
+    if (e != cudaSuccess) return e;
+    const bool cached = d >= 0 && d < 256;
+    const uint64_t bit = cached ? uint64_t(1) << (d & 63) : 0;
+    if (cached && (done.dev[d >> 6].load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess && cached) done.dev[d >> 6].fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // Name of the kernel the last launcher call on this thread launched.
 const char* last_kernel_name();

@@ -4,7 +4,6 @@
 
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -12,27 +11,6 @@
 #include "internal.h"
 
 namespace dpz {
-
-// Devices on which a kernel's dynamic shared memory limit has been raised,
-// one bit per device (0..255): each launcher keeps one of these per kernel,
-// so a launch after the first costs one atomic load.
-struct SmemRaisedOn {
-    std::atomic<uint64_t> dev[4];
-};
-
-// Raise the kernel's dynamic shared memory limit on the current device, once.
-inline cudaError_t raise_smem(SmemRaisedOn& done, const void* fn, size_t smem)
-{
-    int d = 0;
-    cudaError_t e = cudaGetDevice(&d);
-    if (e != cudaSuccess) return e;
-    const bool cached = d >= 0 && d < 256;
-    const uint64_t bit = cached ? uint64_t(1) << (d & 63) : 0;
-    if (cached && (done.dev[d >> 6].load(std::memory_order_acquire) & bit)) return cudaSuccess;
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess && cached) done.dev[d >> 6].fetch_or(bit, std::memory_order_release);
-    return e;
-}
 
 // A row-major matrix of element type dt (DPZ_F32 or DPZ_BF16) whose rows are
 // ld elements apart.
@@ -47,6 +25,16 @@ struct Ids {
     const void* p;
     int it;
 };
+
+#if defined(__CUDACC__)
+// An id as an int, -1 where it names none of V tokens (V < 2^30).
+__device__ __forceinline__ int load_token(const Ids& ids, int64_t i, int64_t V)
+{
+    const int64_t v = ids.it == DPZ_I64 ? static_cast<const int64_t*>(ids.p)[i]
+                                        : (int64_t) static_cast<const int*>(ids.p)[i];
+    return v >= 0 && v < V ? (int)v : -1;
+}
+#endif
 
 cudaError_t launch_embedding(const Mat& table, const Ids& ids, int64_t T, int64_t V, int64_t D,
                              float scale, const Mat& out, cudaStream_t s);

@@ -10,19 +10,6 @@ namespace dpz {
 
 namespace {
 
-__device__ __forceinline__ int64_t load_id(const Ids& ids, int64_t i)
-{
-    return ids.it == DPZ_I64 ? static_cast<const int64_t*>(ids.p)[i]
-                             : (int64_t) static_cast<const int*>(ids.p)[i];
-}
-
-// An id as an int, -1 where it names none of V tokens (V < 2^30).
-__device__ __forceinline__ int load_token(const Ids& ids, int64_t i, int64_t V)
-{
-    const int64_t v = load_id(ids, i);
-    return v >= 0 && v < V ? (int)v : -1;
-}
-
 // One access unit of a row: W = 8 or 4 elements in one word of 8 to 32 bytes
 // (rows aligned to W elements whose length is a multiple of W), or W = 1
 // element.

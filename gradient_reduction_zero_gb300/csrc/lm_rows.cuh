@@ -20,13 +20,6 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-__device__ __forceinline__ int load_token(const Ids& ids, int64_t i, int64_t V)
-{
-    const int64_t v = ids.it == DPZ_I64 ? static_cast<const int64_t*>(ids.p)[i]
-                                        : (int64_t) static_cast<const int*>(ids.p)[i];
-    return v >= 0 && v < V ? (int)v : -1;
-}
-
 // 2^u by the hardware's instruction: at most 2 units in the last place off,
 // which is below the rounding of the exponent that it is given here.
 __device__ __forceinline__ float ex2(float u)

@@ -26,7 +26,6 @@
 // NaN norm and status bits; the update sets DPZ_STATUS_UPDATE_SKIPPED and a
 // NaN norm_out), waits (again bounded) for its loads in flight, and returns
 // without writing the tile.
-#include <atomic>
 
 #include "bulk.cuh"
 #include "device.cuh"
@@ -402,27 +401,6 @@ k_norm_owned_tma(const char* __restrict__ grads, int64_t P, int64_t C,
 
 namespace {
 
-// Devices on which a kernel's dynamic shared memory limit has been raised,
-// one bit per device (0..255): each launcher keeps one of these per kernel,
-// so a launch after the first costs one atomic load.
-struct SmemRaised {
-    std::atomic<uint64_t> dev[4];
-};
-
-// Raise the kernel's dynamic shared memory limit on the current device, once.
-cudaError_t allow_smem(SmemRaised& done, const void* fn, size_t smem)
-{
-    int d = 0;
-    cudaError_t e = cudaGetDevice(&d);
-    if (e != cudaSuccess) return e;
-    const bool cached = d >= 0 && d < 256;
-    const uint64_t bit = cached ? uint64_t(1) << (d & 63) : 0;
-    if (cached && (done.dev[d >> 6].load(std::memory_order_acquire) & bit)) return cudaSuccess;
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess && cached) done.dev[d >> 6].fetch_or(bit, std::memory_order_release);
-    return e;
-}
-
 // The arguments of one launch of the AdamW + all-gather kernel.
 struct UpdateLaunch {
     const void* grads;
@@ -438,10 +416,10 @@ struct UpdateLaunch {
 template <int GDT, int WDT, int NT>
 cudaError_t tma_t(const Arena& a, const AdamArgs& h, const UpdateLaunch& u, cudaStream_t s)
 {
-    static SmemRaised raised;
+    static SmemRaisedOn raised;
     auto fn = k_adamw_bcast_tma<GDT, WDT, NT>;
     const size_t smem = sizeof(TmaTile<GDT, WDT>);
-    const cudaError_t e = allow_smem(raised, reinterpret_cast<const void*>(fn), smem);
+    const cudaError_t e = raise_smem(raised, reinterpret_cast<const void*>(fn), smem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (a.C + kUpdateTile - 1) / kUpdateTile * a.N;
     set_last_kernel_name("dpz_adamw_bcast");
@@ -526,11 +504,11 @@ static cudaError_t fused_tma_t(const Arena& a, const Avg& avg, const AdamArgs& h
                                void* grads, float* master, float* m, float* v, void* weights,
                                void* ws, cudaStream_t s)
 {
-    static SmemRaised raised;
+    static SmemRaisedOn raised;
     auto fn = k_zero1_fused_tma<GDT, WDT, NT, SUMSQ, TILE>;
     const size_t smem = fold_tile_bytes(GDT, WDT, NT > 0 ? NT : a.N, TILE);
     // the run-time-N kernel may take any tile up to kFoldTileMaxBytes
-    const cudaError_t e = allow_smem(raised, reinterpret_cast<const void*>(fn),
+    const cudaError_t e = raise_smem(raised, reinterpret_cast<const void*>(fn),
                                      NT > 0 ? smem : kFoldTileMaxBytes);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (a.C + TILE - 1) / TILE * a.N;
@@ -666,10 +644,10 @@ cudaError_t launch_staged_timeout_selftest(int kernel, void* buf, cudaStream_t s
     static_assert(kSelftestGrads + 144 <= DPZ_SELFTEST_BUF_BYTES, "the arena fits the buffer");
     cudaError_t e = cudaSuccess;
     if (kernel == DPZ_SELFTEST_UPDATE) {
-        static SmemRaised raised;
+        static SmemRaisedOn raised;
         auto fn = k_adamw_bcast_tma<1, 1, 1>;
         const size_t smem = sizeof(TmaTile<1, 1>);
-        e = allow_smem(raised, reinterpret_cast<const void*>(fn), smem);
+        e = raise_smem(raised, reinterpret_cast<const void*>(fn), smem);
         if (e != cudaSuccess) return e;
         set_last_kernel_name("dpz_selftest_staged_timeout");
         fn<<<1, kUpdateThreads, smem, s>>>(grads, a.P, master, m, v, weights, a.P, a.C, 1, h, hdr,
@@ -681,10 +659,10 @@ cudaError_t launch_staged_timeout_selftest(int kernel, void* buf, cudaStream_t s
         fn<<<1, kNormThreads, (size_t)kNormTile * 2, s>>>(grads, a.P, a.C, hdr, ws_partials(ws),
                                                          wait);
     } else if (kernel == DPZ_SELFTEST_STEP) {
-        static SmemRaised raised;
+        static SmemRaisedOn raised;
         auto fn = k_zero1_fused_tma<1, 1, 1, true, kTmaTile>;
         const size_t smem = fold_tile_bytes(1, 1, 1, kTmaTile);
-        e = allow_smem(raised, reinterpret_cast<const void*>(fn), smem);
+        e = raise_smem(raised, reinterpret_cast<const void*>(fn), smem);
         if (e != cudaSuccess) return e;
         Avg avg;
         avg.fN = 1.0f;
