@@ -340,8 +340,10 @@ def _bad_mat(t, what, dev, rows, cols):
 def _mat(t, what: str, dev: int, rows: int = -1, cols: int = -1) -> tuple:
     """(address, row stride, dtype code, rows, columns) of a 2-D matrix of unit
     column stride on GPU `dev`."""
+    if not _ID_CODES:
+        _dtypes()
     shape, strides = t.shape, t.stride()
-    code = _dtypes().get(t.dtype)
+    code = _CODES.get(t.dtype)
     if code is None or len(shape) != 2 or t.get_device() != dev:
         _bad_mat(t, what, dev, rows, cols)
     r, c = shape
@@ -372,7 +374,6 @@ def _dense(t, what: str, dev: int, n: int, k: int = 0, dtype=None):
 
 def _tokens(t, what: str, dev: int, n: int, k: int = 0) -> tuple:
     """(address, id type code) of token ids [n] or [n, k]."""
-    _dtypes()
     code = _ID_CODES.get(t.dtype)
     if code is None:
         raise TypeError(f"{what} must be int32 or int64, not {t.dtype}")
@@ -493,7 +494,7 @@ def _distill_args(logits, teacher_ids, teacher_logits, temperature) -> tuple:
     if K == 0:
         raise ValueError("teacher_ids must have at least one column")
     p, it = _tokens(teacher_ids, "teacher_ids", dev, T, K)
-    tc = _dtypes().get(teacher_logits.dtype)
+    tc = _CODES.get(teacher_logits.dtype)
     if tc is None:
         raise TypeError(f"teacher_logits: unsupported dtype {teacher_logits.dtype}")
     return dev, (px, ld, T, V, xc, p, it,
