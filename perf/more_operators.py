@@ -157,7 +157,7 @@ def prepare(case, seed):
         if own:
             import gradient_reduction_zero_gb300.dpz as dpz
             s["list"], s["out_list"] = dpz.TensorList(s["grads"]), dpz.TensorList(s["out"])
-            s["ws"] = dpz.dp_tensors_workspace(s["list"])
+            s["ws"] = dpz.tensors_workspace(s["list"])
         return s
     Hq, Hk, D = case["Hq"], case["Hk"], case["D"]
     if op.startswith("norm"):
@@ -347,8 +347,8 @@ def _own(s, c):
     import gradient_reduction_zero_gb300.dpz as dpz
     op = c["op"]
     if op == "clip":
-        dpz.dp_tensors_norm(s["list"], s["norm"], s["ws"])
-        dpz.dp_tensors_clip(s["list"], s["norm"], c["clip"], out=s["out_list"])
+        dpz.tensors_norm(s["list"], s["norm"], s["ws"])
+        dpz.tensors_clip(s["list"], s["norm"], c["clip"], out=s["out_list"])
         return dict(norm=s["norm"], slab=s["slab"])
     if op.startswith("norm"):
         kw = dict(wq=s["wq"], wk=s["wk"], eps=EPS, positions=s["positions"],
