@@ -15,7 +15,10 @@ _BINDING = {"AdamWCfg", "DpzError", "dp_allgather", "dp_allreduce_avg", "dp_grad
             "dp_reduce_scatter_avg_bucket", "dp_grad_norm_finalize", "dp_zero1_step",
             "dp_zero1_update", "dp_zero2_update", "make_cfg", "workspace", "zero1_adamw_step",
             "lm_embedding", "lm_embedding_grad", "lm_embedding_workspace", "lm_logprobs",
-            "lm_logprobs_grad", "lm_distill", "lm_distill_grad", "lm_distill_step"}
+            "lm_logprobs_grad", "lm_distill", "lm_distill_grad", "lm_distill_step",
+            "attn_qk_norm_rope", "attn_qk_norm_rope_grad", "attn_qk_norm_rope_workspace",
+            "attn_forward", "attn_grad", "attn_grad_workspace", "TensorList", "tensors_norm",
+            "tensors_clip", "tensors_workspace"}
 
 
 def __getattr__(name):

@@ -124,6 +124,30 @@ CALL(lm_distill_step, "plllipipiifpppplp", 17,
      lm_distill_step(s[0].p, s[1].l, s[2].l, s[3].l, s[4].i, s[5].p, s[6].i, s[7].p, s[8].i,
                      s[9].i, s[10].f, F(11), F(12), F(13), s[14].p, s[15].l, s[16].p))
 
+#define HEADS(k) ((const dpz_heads*)s[k].p)
+
+CALL(attn_qk_norm_rope, "ppllllippifpiplippp", 19,
+     attn_qk_norm_rope(HEADS(0), HEADS(1), s[2].l, s[3].l, s[4].l, s[5].l, s[6].i, s[7].p, s[8].p,
+                       s[9].i, s[10].f, s[11].p, s[12].i, F(13), s[14].l, s[15].i, HEADS(16),
+                       HEADS(17), s[18].p))
+CALL(attn_qk_norm_rope_grad, "ppppllllippifpiplipppppp", 24,
+     attn_qk_norm_rope_grad(HEADS(0), HEADS(1), HEADS(2), HEADS(3), s[4].l, s[5].l, s[6].l, s[7].l,
+                            s[8].i, s[9].p, s[10].p, s[11].i, s[12].f, s[13].p, s[14].i, F(15),
+                            s[16].l, s[17].i, HEADS(18), HEADS(19), s[20].p, s[21].p, s[22].p,
+                            s[23].p))
+CALL(attn_forward, "ppplllllilppiifppp", 18,
+     attn_forward(HEADS(0), HEADS(1), HEADS(2), s[3].l, s[4].l, s[5].l, s[6].l, s[7].l, s[8].i,
+                  s[9].l, s[10].p, s[11].p, s[12].i, s[13].i, s[14].f, HEADS(15), F(16), s[17].p))
+CALL(attn_grad, "pppppplllllilppiifppppp", 23,
+     attn_grad(HEADS(0), HEADS(1), HEADS(2), HEADS(3), F(4), HEADS(5), s[6].l, s[7].l, s[8].l,
+               s[9].l, s[10].l, s[11].i, s[12].l, s[13].p, s[14].p, s[15].i, s[16].i, s[17].f,
+               HEADS(18), HEADS(19), HEADS(20), s[21].p, s[22].p))
+CALL(tensors_norm, "pippp", 5,
+     tensors_norm((const dpz_tensor*)s[0].p, s[1].i, F(2), s[3].p, s[4].p))
+CALL(tensors_clip, "ppipfp", 6,
+     tensors_clip((const dpz_tensor*)s[0].p, (const dpz_tensor*)s[1].p, s[2].i, F(3), s[4].f,
+                     s[5].p))
+
 #define ENTRY(name) {#name, (PyCFunction)(void (*)(void))py_##name, METH_FASTCALL, NULL}
 
 static PyMethodDef methods[] = {
@@ -146,6 +170,12 @@ static PyMethodDef methods[] = {
     ENTRY(lm_distill),
     ENTRY(lm_distill_grad),
     ENTRY(lm_distill_step),
+    ENTRY(attn_qk_norm_rope),
+    ENTRY(attn_qk_norm_rope_grad),
+    ENTRY(attn_forward),
+    ENTRY(attn_grad),
+    ENTRY(tensors_norm),
+    ENTRY(tensors_clip),
     {NULL, NULL, 0, NULL},
 };
 

@@ -1,0 +1,283 @@
+// The global norm over a list of tensors, and the clipping that follows it.
+//
+// Every tensor is cut into chunks of kListChunk bytes, one block each, in the
+// order of the list; block b finds its tensor by bisection of the chunk counts,
+// which are kernel parameters like the addresses (so nothing is copied to the
+// device first, and a captured call keeps its list).  Both kernels move their
+// bytes once and are bound by HBM.  One block per chunk, not persistent blocks:
+// the blocks in flight then sweep one compact window of each tensor.
+//
+// Norm: squares are summed in fp32 by each thread over its at most 128 elements
+// in eight interleaved chains (at most 16 additions each), everything beyond
+// in fp64 in an order that depends on the list alone.
+#include <cmath>
+
+#include "bulk.cuh"
+#include "device.cuh"
+#include "internal.h"
+#include "tensors.h"
+
+namespace dpz {
+
+namespace {
+
+constexpr int kListThreads = 256;
+constexpr int kListVecs = kListChunk / 16 / kListThreads;   // 16-byte vectors of a thread: 16
+constexpr int kListUnroll = 8;
+static_assert(kListVecs % kListUnroll == 0, "whole batches of loads");
+
+// Up to CAP tensors of a launch.  sizes[i]: elements, with the types above them.
+template <int CAP>
+struct List {
+    const char* in[CAP];
+    char* out[CAP];
+    uint64_t sizes[CAP];
+    uint32_t chunk0[CAP];   // first block of tensor i
+    int n;
+};
+
+constexpr int kInBf16 = 62, kOutBf16 = 63;
+constexpr uint64_t kSizeMask = (uint64_t(1) << 62) - 1;
+
+// The chunk of this block: elements [e, e + n) of tensor i.
+struct Chunk {
+    int i;
+    int64_t e, n;
+    bool in_bf16, out_bf16;
+};
+
+template <int CAP>
+__device__ __forceinline__ Chunk my_chunk(const List<CAP>& l)
+{
+    int lo = 0, hi = l.n;   // chunk0[lo] <= block < chunk0[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (l.chunk0[mid] <= blockIdx.x) lo = mid;
+        else hi = mid;
+    }
+    const uint64_t s = l.sizes[lo];
+    const bool ib = s >> kInBf16 & 1;
+    const int64_t per = kListChunk / (ib ? 2 : 4), n = (int64_t)(s & kSizeMask);
+    const int64_t e = (int64_t)(blockIdx.x - l.chunk0[lo]) * per;
+    return {lo, e, n - e < per ? n - e : per, ib, (s >> kOutBf16) != 0};
+}
+
+template <int DT>
+__device__ __forceinline__ float load_elem(const char* p, int64_t i)
+{
+    if (DT == DPZ_BF16)
+        return __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(p)[i] << 16);
+    return reinterpret_cast<const float*>(p)[i];
+}
+
+template <int DT>
+__device__ __forceinline__ void store_elem(char* p, int64_t i, float x)
+{
+    if (DT == DPZ_BF16) reinterpret_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
+    else reinterpret_cast<float*>(p)[i] = x;
+}
+
+// Sum of squares of the thread's part of n elements at p.
+template <int DT>
+__device__ __forceinline__ double chunk_sumsq(const char* p, int n)
+{
+    constexpr int ES = DT == DPZ_BF16 ? 2 : 4, V = 16 / ES;
+    // single elements up to the first 16-byte boundary, 16-byte vectors, a tail
+    const int head = min(n, (int)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / ES);
+    const int vecs = (n - head) / V, tail = n - head - vecs * V;
+    const int t = threadIdx.x;
+    float acc[8] = {};
+    if (t < head) {
+        const float x = load_elem<DT>(p, t);
+        acc[0] = x * x;
+    } else if (t >= 32 && t - 32 < tail) {
+        const float x = load_elem<DT>(p, n - tail + (t - 32));
+        acc[0] = x * x;
+    }
+    const char* v = p + head * ES;
+    const auto add = [&](const uint4& w, int half) {
+        if (DT == DPZ_BF16) {
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                acc[2 * k] = fmaf(bf16_lo(u[k]), bf16_lo(u[k]), acc[2 * k]);
+                acc[2 * k + 1] = fmaf(bf16_hi(u[k]), bf16_hi(u[k]), acc[2 * k + 1]);
+            }
+        } else {
+            const float x[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z),
+                                __uint_as_float(w.w)};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[4 * half + k] = fmaf(x[k], x[k], acc[4 * half + k]);
+        }
+    };
+    for (int b = 0; b < kListVecs; b += kListUnroll) {
+        uint4 w[kListUnroll];
+#pragma unroll
+        for (int k = 0; k < kListUnroll; ++k) {
+            const int at = (b + k) * kListThreads + t;
+            w[k] = at < vecs ? ld16(v + 16 * (int64_t)at) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < kListUnroll; ++k) add(w[k], k & 1);
+    }
+    double s = 0.0;
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) s += (double)acc[k] + (double)acc[k + 1];
+    return s;
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kListThreads)
+k_tensors_sumsq(const __grid_constant__ List<CAP> l, double* __restrict__ partial)
+{
+    pdl_enter();
+    const Chunk c = my_chunk(l);
+    const char* p = l.in[c.i] + c.e * (c.in_bf16 ? 2 : 4);
+    const double s = c.in_bf16 ? chunk_sumsq<DPZ_BF16>(p, (int)c.n)
+                               : chunk_sumsq<DPZ_F32>(p, (int)c.n);
+    const double sum = block_sum(s);
+    if (threadIdx.x == 0) partial[blockIdx.x] = sum;
+}
+
+constexpr int kListFinalThreads = 512;
+
+// sqrt of the sum of n partials, thread t taking t, t + 512, ... in turn.
+__global__ void __launch_bounds__(kListFinalThreads)
+k_tensors_norm(const double* __restrict__ partial, int64_t n, float* norm_out)
+{
+    pdl_enter();
+    double s[8] = {};
+    for (int64_t i = threadIdx.x; i < n; i += 8 * kListFinalThreads)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int64_t at = i + k * kListFinalThreads;
+            if (at < n) s[k] += partial[at];
+        }
+    const double sum =
+        block_sum(((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7])));
+    if (threadIdx.x == 0) *norm_out = (float)sqrt(sum);
+}
+
+// out = R(in * k) for a chunk, one vector of the wider type's 8 elements after
+// another where both addresses allow it.
+template <int IN, int OUT>
+__device__ __forceinline__ void clip_chunk(const char* p, char* q, int n, float k)
+{
+    constexpr int EI = IN == DPZ_BF16 ? 2 : 4, EO = OUT == DPZ_BF16 ? 2 : 4;
+    const int t = threadIdx.x;
+    // elements up to the first 8-element group that is aligned in both
+    const int head = min(n, (int)((8 * EI - (reinterpret_cast<uintptr_t>(p) & (8 * EI - 1))) & (8 * EI - 1)) / EI);
+    const bool vec = ((reinterpret_cast<uintptr_t>(q) + head * EO) & (8 * EO - 1)) == 0;
+    if (!vec) {
+        for (int i = t; i < n; i += kListThreads) store_elem<OUT>(q, i, load_elem<IN>(p, i) * k);
+        return;
+    }
+    const int groups = (n - head) / 8, tail = n - head - groups * 8;
+    if (t < head) store_elem<OUT>(q, t, load_elem<IN>(p, t) * k);
+    else if (t >= 32 && t - 32 < tail)
+        store_elem<OUT>(q, n - tail + t - 32, load_elem<IN>(p, n - tail + t - 32) * k);
+    const char* v = p + head * EI;
+    char* o = q + head * EO;
+    constexpr int kUnroll = IN == DPZ_BF16 ? 8 : 4;
+    for (int b = 0; b < groups; b += kUnroll * kListThreads) {
+        typename Group<IN>::Raw w[kUnroll];
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) {
+            const int at = b + j * kListThreads + t;
+            if (at < groups) w[j] = Group<IN>::load_raw(v + 8 * EI * (int64_t)at);
+        }
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) {
+            const int at = b + j * kListThreads + t;
+            if (at >= groups) break;
+            float x[8];
+            Group<IN>::unpack(w[j], x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= k;
+            store_group<OUT>(o + 8 * EO * (int64_t)at, x);
+        }
+    }
+}
+
+// in_place: nothing is written where the factor is 1.
+template <int CAP>
+__global__ void __launch_bounds__(kListThreads)
+k_tensors_clip(const __grid_constant__ List<CAP> l, const float* __restrict__ norm, float clip)
+{
+    pdl_enter();
+    const float nrm = *norm;
+    const float k = nrm > clip ? __fdiv_rn(clip, nrm) : 1.0f;
+    const Chunk c = my_chunk(l);
+    const char* p = l.in[c.i] + c.e * (c.in_bf16 ? 2 : 4);
+    char* q = l.out[c.i] + c.e * (c.out_bf16 ? 2 : 4);
+    if (k == 1.0f && p == q) return;
+    if (c.in_bf16) {
+        if (c.out_bf16) clip_chunk<DPZ_BF16, DPZ_BF16>(p, q, (int)c.n, k);
+        else clip_chunk<DPZ_BF16, DPZ_F32>(p, q, (int)c.n, k);
+    } else {
+        if (c.out_bf16) clip_chunk<DPZ_F32, DPZ_BF16>(p, q, (int)c.n, k);
+        else clip_chunk<DPZ_F32, DPZ_F32>(p, q, (int)c.n, k);
+    }
+}
+
+template <int CAP>
+int64_t fill(List<CAP>& l, const dpz_tensor* in, const dpz_tensor* out, int n)
+{
+    int64_t chunks = 0;
+    l.n = 0;
+    for (int i = 0; i < n; ++i) {
+        if (in[i].n == 0) continue;
+        const int at = l.n++;
+        l.in[at] = static_cast<const char*>(in[i].p);
+        l.out[at] = out ? static_cast<char*>(out[i].p) : nullptr;
+        l.sizes[at] = (uint64_t)in[i].n | (uint64_t)(in[i].dtype == DPZ_BF16) << kInBf16 |
+                      (uint64_t)(out && out[i].dtype == DPZ_BF16) << kOutBf16;
+        l.chunk0[at] = (uint32_t)chunks;
+        chunks += list_chunks(in[i]);
+    }
+    return chunks;
+}
+
+template <int CAP>
+cudaError_t sumsq(const dpz_tensor* in, int n, double* partial, cudaStream_t s)
+{
+    List<CAP> l;
+    const int64_t chunks = fill(l, in, nullptr, n);
+    return launch_kernel(k_tensors_sumsq<CAP>, dim3((unsigned)chunks), dim3(kListThreads), 0, s,
+                         true, 0u, l, partial);
+}
+
+template <int CAP>
+cudaError_t clip_list(const dpz_tensor* in, const dpz_tensor* out, int n, const float* norm,
+                      float clip, cudaStream_t s)
+{
+    List<CAP> l;
+    const int64_t chunks = fill(l, in, out, n);
+    return launch_kernel(k_tensors_clip<CAP>, dim3((unsigned)chunks), dim3(kListThreads), 0, s,
+                         true, 0u, l, norm, clip);
+}
+
+}  // namespace
+
+cudaError_t launch_tensors_sumsq(const dpz_tensor* in, int n, double* partial, cudaStream_t s)
+{
+    set_last_kernel_name("tensors_sumsq");
+    return n <= kListSmall ? sumsq<kListSmall>(in, n, partial, s) : sumsq<kListMost>(in, n, partial, s);
+}
+
+cudaError_t launch_tensors_norm(const double* partial, int64_t n, float* norm_out, cudaStream_t s)
+{
+    set_last_kernel_name("tensors_norm");
+    return launch_kernel(k_tensors_norm, dim3(1), dim3(kListFinalThreads), 0, s, true, 0u, partial,
+                         n, norm_out);
+}
+
+cudaError_t launch_tensors_clip(const dpz_tensor* in, const dpz_tensor* out, int n,
+                                const float* norm, float clip, cudaStream_t s)
+{
+    set_last_kernel_name("tensors_clip");
+    return n <= kListSmall ? clip_list<kListSmall>(in, out, n, norm, clip, s)
+                           : clip_list<kListMost>(in, out, n, norm, clip, s);
+}
+
+}  // namespace dpz

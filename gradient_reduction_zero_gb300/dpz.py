@@ -18,6 +18,7 @@ HEADER = os.path.join(os.path.dirname(_PKG), "include", "dpz.h")
 F32, BF16, BF16_ACC32 = 0, 1, 2
 I32, I64 = 16, 17
 LM_MAX_TOP, LM_MAX_TEACHER = 32, 256
+MAX_TENSORS = 8192
 OK, ERR_INVALID_ARG, ERR_ALIGN, ERR_CUDA = 0, 1, 2, 3
 MAX_RANKS = 64
 # the per-call status word of a workspace (include/dpz.h)
@@ -83,6 +84,19 @@ _SIGS = {
                         _I),
     "lm_distill_step": ([_VP, _L, _L, _L, _I, _VP, _I, _VP, _I, _I, _F, _FP, _FP, _FP, _VP, _L,
                          _VP], _I),
+    "attn_qk_norm_rope": ([_VP, _VP, _L, _L, _L, _L, _I, _VP, _VP, _I, _F, _VP, _I, _FP, _L, _I,
+                           _VP, _VP, _VP], _I),
+    "attn_qk_norm_rope_workspace_bytes": ([_L, _L, _L, _L], ctypes.c_size_t),
+    "attn_qk_norm_rope_grad": ([_VP, _VP, _VP, _VP, _L, _L, _L, _L, _I, _VP, _VP, _I, _F, _VP, _I,
+                                _FP, _L, _I, _VP, _VP, _VP, _VP, _VP, _VP], _I),
+    "attn_forward": ([_VP, _VP, _VP, _L, _L, _L, _L, _L, _I, _L, _VP, _VP, _I, _I, _F, _VP, _FP,
+                      _VP], _I),
+    "attn_grad_workspace_bytes": ([_L, _L, _L, _L, _L, _L], ctypes.c_size_t),
+    "attn_grad": ([_VP, _VP, _VP, _VP, _FP, _VP, _L, _L, _L, _L, _L, _I, _L, _VP, _VP, _I, _I, _F,
+                   _VP, _VP, _VP, _VP, _VP], _I),
+    "tensors_workspace_bytes": ([_VP, _I], ctypes.c_size_t),
+    "tensors_norm": ([_VP, _I, _FP, _VP, _VP], _I),
+    "tensors_clip": ([_VP, _VP, _I, _FP, _F, _VP], _I),
     "dpz_last_error": ([], ctypes.c_char_p),
     "dpz_version": ([], ctypes.c_char_p),
     "dpz_launch_count": ([], ctypes.c_int64),
@@ -539,6 +553,300 @@ def lm_distill_step(logits, teacher_ids, teacher_logits, dloss, loss, dlogits, l
         raise TypeError("logits and dlogits must have one dtype")
     _check(_C.lm_distill_step(*args, _dense(dloss, "dloss", dev, T), _dense(loss, "loss", dev, T),
                               _dense(lse, "lse", dev, T), pd, ldd, _current_stream(dev, stream)))
+
+
+# ------------------------------------------------------------ the attention block
+
+def _heads(words: list, t, what: str, dev: int, tokens: int, heads: int, D: int, code: int) -> None:
+    """Appends the dpz_heads of a tensor [tokens, heads, D] of unit element stride to
+    `words`."""
+    shape, strides = t.shape, t.stride()
+    if _CODES.get(t.dtype) != code or len(shape) != 3 or t.get_device() != dev \
+            or shape[0] != tokens or shape[1] != heads or shape[2] != D \
+            or (strides[2] != 1 and D > 1):
+        if t.dtype not in _dtypes():
+            raise TypeError(f"{what}: unsupported dtype {t.dtype}")
+        if _CODES[t.dtype] != code:
+            raise TypeError(f"{what} must have the dtype of q, not {t.dtype}")
+        raise ValueError(f"{what} must be [{tokens}, {heads}, {D}] of unit element stride on "
+                         f"cuda:{dev}, not {list(shape)} with strides {list(strides)} on {t.device}")
+    words += (t.data_ptr(), strides[0], strides[1])
+
+
+def _q_of(q) -> tuple:
+    """(GPU, dtype code, tokens, heads, D) of the queries."""
+    dev = q.get_device()
+    if dev != _current_device():     # the other tensors are compared with it
+        _bad_device(q, "q")
+    code = _dtypes().get(q.dtype)
+    if code is None:
+        raise TypeError(f"q: unsupported dtype {q.dtype}")
+    if len(q.shape) != 3:
+        raise ValueError(f"q must be [tokens, heads, D], not {list(q.shape)}")
+    return (dev, code, *q.shape)
+
+
+def _keys_of(k) -> tuple:
+    """(tokens, heads) of the keys."""
+    if len(k.shape) != 3:
+        raise ValueError(f"k must be [tokens, heads, D], not {list(k.shape)}")
+    return k.shape[0], k.shape[1]
+
+
+def _structs(words: list) -> tuple:
+    """A host array of the structs, and the address of each (three words)."""
+    a = (ctypes.c_int64 * len(words))(*words)
+    at = ctypes.addressof(a)
+    return a, [at + 8 * i for i in range(0, len(words), 3)]
+
+
+def _rope_args(q, k, wq, wk, eps, positions, inv_freq, interleaved) -> tuple:
+    """The GPU, the words of q and k and the arguments that the call and its gradient have in
+    common."""
+    dev, code, T, Hq, D = _q_of(q)
+    Hk = _keys_of(k)[1]
+    words: list = []
+    _heads(words, q, "q", dev, T, Hq, D, code)
+    _heads(words, k, "k", dev, T, Hk, D, code)
+    wc, pw = F32, []
+    for w, what in ((wq, "wq"), (wk, "wk")):
+        if w is not None:
+            c = _CODES.get(w.dtype)
+            if c is None or (pw and pw[0] is not None and c != wc):
+                raise TypeError("wq and wk must have one dtype, bfloat16 or float32")
+            wc = c
+        pw.append(None if w is None else _dense(w, what, dev, D, 0, w.dtype))
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq come together")
+    pp, it, pf, R = None, I64, None, 0
+    if positions is not None:
+        pp, it = _tokens(positions, "positions", dev, T)
+        R = 2 * inv_freq.numel()
+        pf = _dense(inv_freq, "inv_freq", dev, R // 2)
+    return dev, words, (T, Hq, Hk, D, code, pw[0], pw[1], wc, eps, pp, it, pf, R,
+                        int(bool(interleaved)))
+
+
+def attn_qk_norm_rope(q, k, q_out, k_out, wq=None, wk=None, positions=None, inv_freq=None,
+                      eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
+    """RMS norm of every head of q [T, Hq, D] and k [T, Hk, D], bf16 or fp32 with any
+    token and head strides, times wq and wk [D] (None: ones), then the rotation
+    of the first 2 * len(inv_freq) elements by positions [T] (int32 or int64)
+    times inv_freq (fp32), in pairs half of them apart, or of neighbours if
+    `interleaved`.  q_out and k_out may be q and k."""
+    dev, words, args = _rope_args(q, k, wq, wk, eps, positions, inv_freq, interleaved)
+    T, Hq, Hk, D, code = args[:5]
+    _heads(words, q_out, "q_out", dev, T, Hq, D, code)
+    _heads(words, k_out, "k_out", dev, T, Hk, D, code)
+    keep, at = _structs(words)
+    _check(_C.attn_qk_norm_rope(at[0], at[1], *args, at[2], at[3], _current_stream(dev, stream)))
+
+
+def attn_qk_norm_rope_workspace(T: int, Hq: int, Hk: int, D: int, device=None):
+    """A device tensor of attn_qk_norm_rope_workspace_bytes(T, Hq, Hk, D) bytes."""
+    nb = lib.attn_qk_norm_rope_workspace_bytes(T, Hq, Hk, D)
+    if nb == 0:
+        raise DpzError(ERR_INVALID_ARG, lib.dpz_last_error().decode())
+    return _torch().empty(nb, dtype=_torch().uint8, device=device or "cuda")
+
+
+def _workspace_of(ws, need: int, dev: int):
+    """The address of a dense workspace of at least `need` bytes."""
+    if ws.get_device() != dev or not ws.is_contiguous() or ws.nbytes < need:
+        raise ValueError(f"ws must be a dense tensor of at least {need} bytes on cuda:{dev}")
+    return ws.data_ptr()
+
+
+def attn_qk_norm_rope_grad(q, k, dq_out, dk_out, dq, dk, ws=None, wq=None, wk=None, dwq=None,
+                           dwk=None, positions=None, inv_freq=None, eps: float = 1e-6,
+                           interleaved: bool = False, stream=None) -> None:
+    """The gradient of attn_qk_norm_rope from its inputs and the gradients dq_out and
+    dk_out of its outputs: dq, dk (which may be dq_out, dk_out) and, where given,
+    dwq, dwk [D] of the weights' dtype.  ws: attn_qk_norm_rope_workspace(T, Hq,
+    Hk, D), needed with dwq or dwk."""
+    dev, words, args = _rope_args(q, k, wq, wk, eps, positions, inv_freq, interleaved)
+    T, Hq, Hk, D, code = args[:5]
+    for t, what, h in ((dq_out, "dq_out", Hq), (dk_out, "dk_out", Hk), (dq, "dq", Hq),
+                       (dk, "dk", Hk)):
+        _heads(words, t, what, dev, T, h, D, code)
+    pd, pws = [], None
+    for d, w, what in ((dwq, wq, "dwq"), (dwk, wk, "dwk")):
+        if d is not None and w is None:
+            raise ValueError(f"{what} without its weight")
+        pd.append(None if d is None else _dense(d, what, dev, D, 0, w.dtype))
+    if dwq is not None or dwk is not None:
+        need = lib.attn_qk_norm_rope_workspace_bytes(T, Hq, Hk, D)
+        if ws is None:
+            raise ValueError("dwq and dwk need ws")
+        pws = _workspace_of(ws, need, dev)
+    keep, at = _structs(words)
+    _check(_C.attn_qk_norm_rope_grad(at[0], at[1], at[2], at[3], *args, at[4], at[5], pd[0], pd[1],
+                                     pws, _current_stream(dev, stream)))
+
+
+def _attn_args(q, k, v, scale, causal, batch, cu_q, cu_k) -> tuple:
+    """The GPU, the words of q, k and v and the arguments that attention and its
+    gradient have in common."""
+    dev, code, Tq, Hq, D = _q_of(q)
+    Tk, Hk = _keys_of(k)
+    words: list = []
+    _heads(words, q, "q", dev, Tq, Hq, D, code)
+    _heads(words, k, "k", dev, Tk, Hk, D, code)
+    _heads(words, v, "v", dev, Tk, Hk, D, code)
+    pq = pk = None
+    it = I32
+    if (cu_q is None) != (cu_k is None):
+        raise ValueError("cu_q and cu_k come together")
+    if cu_q is not None:
+        batch = cu_q.numel() - 1
+        if batch < 1:
+            raise ValueError("cu_q must hold at least two offsets")
+        pq, it = _tokens(cu_q, "cu_q", dev, batch + 1)
+        pk, kt = _tokens(cu_k, "cu_k", dev, batch + 1)
+        if kt != it:
+            raise TypeError("cu_q and cu_k must have one dtype")
+    if scale is None:
+        scale = D ** -0.5 if D else 1.0
+    return dev, words, (Tq, Tk, Hq, Hk, D, code, batch, pq, pk, it, int(bool(causal)), scale)
+
+
+def attn_forward(q, k, v, out, lse=None, scale=None, causal: bool = False, batch: int = 1,
+                 cu_q=None, cu_k=None, stream=None) -> None:
+    """out = softmax(scale * q k^T) v over `batch` sequences of equal length packed one after
+    another, or those between the offsets cu_q and cu_k (int32 or int64, one more
+    than sequences; batch is then not used).  q and out [Tq, Hq, D], k and v
+    [Tk, Hk, D], bf16 or fp32 with any token and head strides, Hq a multiple of
+    Hk, D at most 128; lse [Hq, Tq] fp32, which the gradient needs.  scale None:
+    D ** -0.5.  causal: the last query of a sequence sees all of its keys, the one
+    before it one less."""
+    dev, words, args = _attn_args(q, k, v, scale, causal, batch, cu_q, cu_k)
+    Tq, _, Hq, _, D, code = args[:6]
+    _heads(words, out, "out", dev, Tq, Hq, D, code)
+    keep, at = _structs(words)
+    _check(_C.attn_forward(at[0], at[1], at[2], *args, at[3], _rows_of_heads(lse, "lse", dev, Hq, Tq),
+                           _current_stream(dev, stream)))
+
+
+def _rows_of_heads(t, what: str, dev: int, H: int, T: int):
+    """The address of a dense fp32 [H, T]; None for None."""
+    if t is not None and T == 0:
+        return None
+    return _dense(t, what, dev, H, T)
+
+
+def attn_grad_workspace(Tq: int, Tk: int, batch: int, Hq: int, Hk: int, D: int, device=None):
+    """A device tensor of attn_grad_workspace_bytes(Tq, Tk, batch, Hq, Hk, D) bytes."""
+    nb = lib.attn_grad_workspace_bytes(Tq, Tk, batch, Hq, Hk, D)
+    if nb == 0:
+        raise DpzError(ERR_INVALID_ARG, lib.dpz_last_error().decode())
+    return _torch().empty(nb, dtype=_torch().uint8, device=device or "cuda")
+
+
+def attn_grad(q, k, v, out, lse, dout, dq, dk, dv, ws, scale=None, causal: bool = False,
+              batch: int = 1, cu_q=None, cu_k=None, stream=None) -> None:
+    """The gradients dq, dk and dv of attn_forward's out, from its arguments, its out and
+    lse and dout [Tq, Hq, D].  ws: attn_grad_workspace(Tq, Tk, batch, Hq, Hk, D)
+    or larger."""
+    dev, words, args = _attn_args(q, k, v, scale, causal, batch, cu_q, cu_k)
+    Tq, Tk, Hq, Hk, D, code, B = args[:7]
+    for t, what, n, h in ((out, "out", Tq, Hq), (dout, "dout", Tq, Hq), (dq, "dq", Tq, Hq),
+                          (dk, "dk", Tk, Hk), (dv, "dv", Tk, Hk)):
+        _heads(words, t, what, dev, n, h, D, code)
+    pws = _workspace_of(ws, lib.attn_grad_workspace_bytes(Tq, Tk, B, Hq, Hk, D), dev)
+    keep, at = _structs(words)
+    _check(_C.attn_grad(at[0], at[1], at[2], at[3], _rows_of_heads(lse, "lse", dev, Hq, Tq), at[4],
+                        *args, at[5], at[6], at[7], pws, _current_stream(dev, stream)))
+
+
+# ------------------------------------------------------------ lists of tensors
+
+class TensorList:
+    """A list of dense CUDA tensors (bf16 or fp32, any shapes, contiguous or a
+    permutation of it) for tensors_norm and tensors_clip, marshalled once.
+    It keeps the tensors alive; make a new one when they change."""
+    __slots__ = ("tensors", "device", "_array", "address", "sizes")
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        codes, words, self.sizes, dev = _dtypes(), [], [], None
+        if len(self.tensors) > MAX_TENSORS:
+            raise ValueError(f"{len(self.tensors)} tensors are more than {MAX_TENSORS}")
+        for i, t in enumerate(self.tensors):
+            code, d = codes.get(t.dtype), t.get_device()
+            if code is None:
+                raise TypeError(f"tensor {i}: unsupported dtype {t.dtype}")
+            if dev is None:
+                dev = d
+            if d < 0 or d != dev:
+                raise ValueError(f"tensor {i} must be on one GPU with the others, not on {t.device}")
+            if not t.is_contiguous() and not _is_dense(t):
+                raise ValueError(f"tensor {i} of shape {list(t.shape)} and strides "
+                                 f"{list(t.stride())} is not dense")
+            words += (t.data_ptr(), t.numel(), code)
+            self.sizes.append((t.shape, t.stride()))
+        self.device = dev
+        self._array = (ctypes.c_int64 * max(1, len(words)))(*words)
+        self.address = ctypes.addressof(self._array)
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def _is_dense(t) -> bool:
+    """Whether the elements fill a range of memory, each place once, in some order."""
+    n = 1
+    for step, size in sorted(p for p in zip(t.stride(), t.shape) if p[1] != 1):
+        if step != n:
+            return False
+        n *= size
+    return True
+
+
+def _list_device(tensors: TensorList) -> int:
+    dev = tensors.device
+    if dev is None:
+        return _current_device()
+    if dev != _current_device():
+        raise ValueError(f"the tensors are on cuda:{dev}, which is not the current device")
+    return dev
+
+
+def tensors_workspace(tensors: TensorList, device=None):
+    """A device tensor of tensors_workspace_bytes bytes for the list."""
+    nb = lib.tensors_workspace_bytes(tensors.address, len(tensors))
+    if nb == 0:
+        raise DpzError(ERR_INVALID_ARG, lib.dpz_last_error().decode())
+    if device is None:
+        device = "cuda" if tensors.device is None else tensors.tensors[0].device
+    return _torch().empty(nb, dtype=_torch().uint8, device=device)
+
+
+def tensors_norm(tensors: TensorList, norm_out, ws, stream=None) -> None:
+    """norm_out [1] (fp32) = the L2 norm of all elements of the list.  ws:
+    tensors_workspace(tensors) or larger."""
+    dev = _list_device(tensors)
+    _dtypes()
+    pn = _dense(norm_out, "norm_out", dev, 1)
+    need = lib.tensors_workspace_bytes(tensors.address, len(tensors))
+    _check(_C.tensors_norm(tensors.address, len(tensors), pn, _workspace_of(ws, need, dev),
+                              _current_stream(dev, stream)))
+
+
+def tensors_clip(tensors: TensorList, norm, clip_norm: float, out: TensorList | None = None,
+                    stream=None) -> None:
+    """out[i] = tensors[i] * min(1, clip_norm / norm) (norm [1], fp32), in place without
+    `out`; tensors of `out` have the shapes and strides of their inputs and either dtype."""
+    dev = _list_device(tensors)
+    _dtypes()
+    out = tensors if out is None else out
+    if out is not tensors:
+        if len(out) != len(tensors) or (out.device is not None and out.device != dev):
+            raise ValueError(f"out must be {len(tensors)} tensors on cuda:{dev}")
+        if out.sizes != tensors.sizes:
+            raise ValueError("out must have the shapes and strides of the tensors")
+    _check(_C.tensors_clip(tensors.address, out.address, len(tensors),
+                              _dense(norm, "norm", dev, 1), clip_norm,
+                              _current_stream(dev, stream)))
 
 
 class PreparedCall:

@@ -452,6 +452,158 @@ DPZ_API int lm_distill_step(const void* logits, int64_t ld, int64_t T, int64_t V
                             int tdtype, int K, float temperature, const float* dloss, float* loss,
                             float* lse, void* dlogits, int64_t ld_dlogits, void* stream);
 
+/* ---------------------------------------------------------------------
+ * The attention block of a replica's training step
+ *
+ * Between the vocabulary-sized ends: the norm of each head of queries and keys
+ * with the rotation by position, attention, and their gradients.  They have
+ * no counterpart on the pages and keep the library's rules: asynchronous on
+ * `stream`, nothing allocated, no sum's order left to atomics, so that every
+ * call repeats bit for bit.
+ *
+ *   T, Tq, Tk  tokens, 0 .. 2^30;   Hq, Hk  heads of queries and of keys (and
+ *   values), up to 65535;   D  elements of a head
+ *   A tensor of heads is a dpz_heads: element [t][h][d] at
+ *   p + (t * ld + h * hs + d) elements.  So the parts of a fused projection
+ *   [T][(Hq + 2 Hk) * D], tokens first or heads first, need no copy.  Strides
+ *   are at least D, the elements distinct, the address a multiple of the
+ *   element; those of a single token or head are not looked at.
+ *   Element types are DPZ_F32 or DPZ_BF16, one for all tensors of heads of a
+ *   call; results are rounded to it once.
+ *   Errors are as above: DPZ_ERR_INVALID_ARG for a NULL pointer (a tensor
+ *   without elements may be NULL), a size or stride out of range, an unknown type,
+ *   or buffers of which one is written and that overlap, except where a call
+ *   allows it (tensors of heads may interleave, as column ranges of a larger
+ *   one do); DPZ_ERR_ALIGN for an address that is not a multiple of its element.
+ * ------------------------------------------------------------------- */
+
+typedef struct dpz_heads {
+    void* p;
+    int64_t ld; /* elements between tokens */
+    int64_t hs; /* elements between heads */
+} dpz_heads;
+
+/* Norm of every head of q [T][Hq][D] and k [T][Hk][D] and rotation by position,
+ * D <= 256:
+ *     y = w * x * (mean_d x^2 + eps)^(-1/2),   rounded once after the rotation of
+ *     its first R elements (R even, <= D): pair i (elements i and i + R/2, or
+ *     2 i and 2 i + 1 with `interleaved`) turns by positions[t] * inv_freq[i],
+ *     (a, b) -> (a cos - b sin, b cos + a sin)
+ * wq and wk [D] (wdtype) or NULL for ones; positions [T] (itype, any value),
+ * inv_freq [R/2] fp32 (radians per position, finite); R = 0: no rotation, neither is
+ * read.  The angle is taken modulo a turn exactly for |inv_freq| < 2^40, so
+ * far positions lose nothing.  q_out may be q and k_out k (same address and
+ * strides).  Fastest where addresses and strides are multiples of 16 bytes and R / 2 of 8
+ * elements (4 in fp32). */
+DPZ_API int attn_qk_norm_rope(const dpz_heads* q, const dpz_heads* k, int64_t T, int64_t Hq,
+                              int64_t Hk, int64_t D, int dtype, const void* wq, const void* wk,
+                              int wdtype, float eps, const void* positions, int itype,
+                              const float* inv_freq, int64_t R, int interleaved,
+                              const dpz_heads* q_out, const dpz_heads* k_out, void* stream);
+
+/* Bytes of device workspace of attn_qk_norm_rope_grad; 0 for invalid sizes. */
+DPZ_API size_t attn_qk_norm_rope_workspace_bytes(int64_t T, int64_t Hq, int64_t Hk, int64_t D);
+
+/* Gradient of attn_qk_norm_rope: from its inputs q and k (not its outputs) and the
+ * gradients dq_out and dk_out of its outputs, dq and dk (which may be dq_out
+ * and dk_out) and, where not NULL, dwq and dwk [D] (wdtype), summed over all
+ * tokens and heads in fp32 and joined in fp64, in an order that the sizes and the
+ * alignment fix.  ws: attn_qk_norm_rope_workspace_bytes bytes, 16-byte aligned;
+ * not used without dwq and dwk. */
+DPZ_API int attn_qk_norm_rope_grad(const dpz_heads* q, const dpz_heads* k, const dpz_heads* dq_out,
+                                   const dpz_heads* dk_out, int64_t T, int64_t Hq, int64_t Hk,
+                                   int64_t D, int dtype, const void* wq, const void* wk, int wdtype,
+                                   float eps, const void* positions, int itype,
+                                   const float* inv_freq, int64_t R, int interleaved,
+                                   const dpz_heads* dq, const dpz_heads* dk, void* dwq, void* dwk,
+                                   void* ws, void* stream);
+
+/* Attention over B sequences packed one after another: q and out [Tq][Hq][D],
+ * k and v [Tk][Hk][D], D <= 128, Hq a multiple of Hk (query head h reads key
+ * head h / (Hq / Hk)).  Sequence b has queries [cu_q[b], cu_q[b+1]) and keys
+ * [cu_k[b], cu_k[b+1]): offsets [B + 1] of type itype in device memory,
+ * ascending, within [0, Tq] and [0, Tk] (values outside are taken as the
+ * nearest bound; sequences that overlap give undefined results within the outputs).
+ * cu_q and cu_k NULL: B sequences of Tq / B and Tk / B rows.
+ *     s_ij = scale * q_i . k_j,   p = softmax_j(s),   out_i = sum_j p_ij v_j,
+ *     lse[h][i] = log sum_j exp(s_ij)        (natural; fp32 [Hq][Tq] or NULL)
+ * causal: of nq queries and nk keys, query i sees keys j <= i + nk - nq (the
+ * last query sees all).  A query that sees no key has out 0 and lse -inf.
+ * Rows outside every sequence are neither read nor written.  scale in (0, 1e30].
+ * Scores, softmax and sums are fp32; for bf16 tensors the probabilities are
+ * rounded to bf16 before their product with v, as operands of the tensor
+ * cores.  A score of NaN or +inf makes its row NaN.  A value row that holds NaN or an
+ * infinity may make NaN of any query of its sequence, also of one that the
+ * causal mask keeps from seeing it (0 times infinity); keys and values behind a
+ * sequence's end never do.
+ * bf16 with addresses and strides that are multiples of 16 bytes runs on the
+ * tensor cores. */
+DPZ_API int attn_forward(const dpz_heads* q, const dpz_heads* k, const dpz_heads* v, int64_t Tq,
+                         int64_t Tk, int64_t Hq, int64_t Hk, int64_t D, int dtype, int64_t B,
+                         const void* cu_q, const void* cu_k, int itype, int causal, float scale,
+                         const dpz_heads* out, float* lse, void* stream);
+
+/* Bytes of device workspace of attn_grad; 0 for invalid sizes. */
+DPZ_API size_t attn_grad_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hk,
+                                         int64_t D);
+
+/* Gradient of attn_forward's out: from its inputs, its out and lse, and dout
+ * [Tq][Hq][D], the gradients dq, dk and dv.  The probabilities are computed again,
+ * p_ij = exp(s_ij - lse_i):
+ *     delta_i = dout_i . out_i,   ds_ij = p_ij (dout_i . v_j - delta_i)
+ *     dq_i = scale sum_j ds_ij k_j,   dk_j = scale sum_i ds_ij q_i,
+ *     dv_j = sum_i p_ij dout_i
+ * dk and dv are summed over the query heads that share a key head.  A query
+ * that sees no key, or whose lse is -inf, has dq 0 and adds nothing.  For bf16
+ * tensors p and ds are rounded to bf16 as operands of the tensor cores.  lse's own
+ * rounding is an error of p of up to 2^-24 |lse|, relative.  ws:
+ * attn_grad_workspace_bytes bytes, 16-byte aligned. */
+DPZ_API int attn_grad(const dpz_heads* q, const dpz_heads* k, const dpz_heads* v,
+                      const dpz_heads* out, const float* lse, const dpz_heads* dout, int64_t Tq,
+                      int64_t Tk, int64_t Hq, int64_t Hk, int64_t D, int dtype, int64_t B,
+                      const void* cu_q, const void* cu_k, int itype, int causal, float scale,
+                      const dpz_heads* dq, const dpz_heads* dk, const dpz_heads* dv, void* ws,
+                      void* stream);
+
+/* ---------------------------------------------------------------------
+ * The global norm and clip of a list of tensors
+ *
+ * dp_grad_global_norm and the step's clip work on an arena.  These calls do
+ * the same for gradients that a program holds as separate tensors, of any
+ * sizes and both types, and can write the clipped values into the arena's
+ * slab on the way.
+ * ------------------------------------------------------------------- */
+
+#define DPZ_MAX_TENSORS 8192
+
+/* A dense tensor of n elements in device memory (n = 0: p is not looked at).
+ * The list itself is host memory, read during the call. */
+typedef struct dpz_tensor {
+    void* p;
+    int64_t n;
+    int64_t dtype; /* DPZ_F32 or DPZ_BF16 */
+} dpz_tensor;
+
+/* Bytes of device workspace of tensors_norm; 0 for an invalid list. */
+DPZ_API size_t tensors_workspace_bytes(const dpz_tensor* tensors, int n);
+
+/* *norm_out = sqrt(sum of the squares of all elements of n <= DPZ_MAX_TENSORS
+ * tensors), fp32 in device memory.  Squares are taken and summed in fp32 within
+ * 64 KB of a tensor by each thread, and in fp64 beyond, in an order that depends on the
+ * list alone.  So an element beyond 1.8e19 gives +inf and one below 1e-23
+ * nothing, as in dp_grad_global_norm; NaN gives NaN.  ws:
+ * tensors_workspace_bytes bytes, 16-byte aligned. */
+DPZ_API int tensors_norm(const dpz_tensor* tensors, int n, float* norm_out, void* ws,
+                            void* stream);
+
+/* out[i] = R(tensors[i] * s), s = clip_norm / *norm if *norm > clip_norm, else 1
+ * (as in the AdamW step's clip; a NaN norm clips nothing).  out[i] has the
+ * elements of tensors[i], of either type, and may be tensors[i] itself (same
+ * address and type), which is then not written where s = 1.  Other overlaps of an output
+ * are refused.  clip_norm > 0 and finite. */
+DPZ_API int tensors_clip(const dpz_tensor* tensors, const dpz_tensor* out, int n,
+                            const float* norm, float clip_norm, void* stream);
+
 /* The calling thread's last error message ("" if none). */
 DPZ_API const char* dpz_last_error(void);
 
