@@ -22,10 +22,10 @@ LIB = os.path.join(PKG, "libdpz.so")
 
 SOURCES = ["api.cpp", "reduce.cu", "adamw.cu", "staged.cu", "norm_static.cu", "lm_api.cpp",
            "lm_embed.cu", "lm_logprobs.cu", "lm_distill.cu", "attn_api.cpp", "attn_rope.cu",
-           "attn_any.cu", "tensors_api.cpp", "tensors.cu"]
+           "attn_any.cu", "attn_tc.cu", "tensors_api.cpp", "tensors.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("internal.h", "api_util.h", "api_check.h", "lm.h",
                                           "lm_shape.h", "lm_rows.cuh", "device.cuh", "bulk.cuh",
-                                          "attn.h", "tensors.h")] + \
+                                          "attn.h", "tc.cuh", "tensors.h")] + \
     [os.path.join(INCLUDE, "dpz.h")]
 
 NVCC_FLAGS = [

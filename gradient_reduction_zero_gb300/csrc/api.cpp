@@ -179,12 +179,13 @@ DPZ_API int dpz_selftest_average_division(int N, unsigned long long* mismatches,
 DPZ_API int dpz_device_status(int* flag_out)
 {
     if (flag_out == nullptr) return fail(DPZ_ERR_INVALID_ARG, "flag_out is NULL");
-    unsigned f = 0;
-    const cudaError_t e = read_and_clear_pipeline_error(&f);
+    unsigned f = 0, tc = 0;
+    cudaError_t e = read_and_clear_pipeline_error(&f);
+    if (e == cudaSuccess) e = read_and_clear_tc_lost(&tc);
     if (e != cudaSuccess)
         return fail(DPZ_ERR_CUDA, "reading the device error flag failed: %s",
                     cudaGetErrorString(e));
-    *flag_out = f != 0;
+    *flag_out = f != 0 || tc != 0;
     return ok();
 }
 

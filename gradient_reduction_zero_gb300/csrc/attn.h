@@ -77,6 +77,12 @@ cudaError_t launch_attn_any(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attn_any_dq(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attn_any_dkv(const AttnArgs& a, cudaStream_t s);
 
+// The same on the tensor cores, for the calls that attn_tc_takes says.
+bool attn_tc_takes(const AttnArgs& a, bool grad);
+cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_attn_tc_dq(const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_attn_tc_dkv(const AttnArgs& a, cudaStream_t s);
+
 #if defined(__CUDACC__)
 // Where a block's tile of rows lies: rows [row0, row0 + rows) of the sequence
 // that has queries [q0, q0 + nq) and keys [k0, k0 + nk).

@@ -304,7 +304,9 @@ DPZ_API int attn_forward(const dpz_heads* q, const dpz_heads* k, const dpz_heads
     if (Tq == 0) return ok();
     a.lse = lse;
     cudaStream_t s = as_stream(stream);
-    DPZ_TRY(launch(s, [&] { return launch_attn_any(a, s); }));
+    DPZ_TRY(launch(s, [&] {
+        return attn_tc_takes(a, false) ? launch_attn_tc(a, s) : launch_attn_any(a, s);
+    }));
     return ok();
 }
 
@@ -343,8 +345,11 @@ DPZ_API int attn_grad(const dpz_heads* q, const dpz_heads* k, const dpz_heads* v
     a.delta = static_cast<float*>(ws);
     cudaStream_t s = as_stream(stream);
     // the queries' gradient leaves delta in the workspace for the keys' and values'
-    if (Tq > 0) DPZ_TRY(launch(s, [&] { return launch_attn_any_dq(a, s); }));
-    if (Tk > 0) DPZ_TRY(launch(s, [&] { return launch_attn_any_dkv(a, s); }));
+    const bool tc = attn_tc_takes(a, true);
+    if (Tq > 0)
+        DPZ_TRY(launch(s, [&] { return tc ? launch_attn_tc_dq(a, s) : launch_attn_any_dq(a, s); }));
+    if (Tk > 0)
+        DPZ_TRY(launch(s, [&] { return tc ? launch_attn_tc_dkv(a, s) : launch_attn_any_dkv(a, s); }));
     return ok();
 }
 

@@ -1,0 +1,997 @@
+// Attention and its gradient on the tensor cores, for bf16 tensors whose
+// addresses and strides are multiples of 16 bytes and heads of a multiple of 8
+// elements up to 128.  The formulas are at the top of attn_any.cu.
+//
+// Tiles of 128 rows by 128 keys.  Each block is made of warps with one task:
+// one issues the TMA loads, one the products, and the others each hold 32 rows
+// of a tile, a thread to a row, so that a row's maximum and sum need no exchange.
+// Scores and accumulators are in tensor memory; probabilities and score gradients
+// go back there in bf16 as the left operand of the next product.  What
+// would lie in a tile beyond a sequence's end is not zero in memory: it is masked
+// where it is a column of scores, cleared in shared memory where a product
+// sums over it, and otherwise a row of its own that is not stored.
+#include <cmath>
+#include <type_traits>
+
+#include "attn.h"
+#include "bulk.cuh"
+#include "device.cuh"
+#include "lm_shape.h"
+#include "tc.cuh"
+
+namespace dpz {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ unsigned g_tc_lost;   // a bounded wait ran out since the last look
+
+__device__ __forceinline__ float ex2(float u)
+{
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(u));
+    return e;
+}
+
+// Paired fp32 operations, one instruction for two.
+using F2 = uint64_t;
+__device__ __forceinline__ F2 pack2(float lo, float hi)
+{
+    F2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ float lo2(F2 a) { return __uint_as_float((uint32_t)a); }
+__device__ __forceinline__ float hi2(F2 a) { return __uint_as_float((uint32_t)(a >> 32)); }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b)
+{
+    F2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b)
+{
+    F2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// The end of a block: after a wait that ran out, time for what is in flight.
+__device__ __forceinline__ void tc_finish(volatile int* lost, uint32_t tmem, bool frees)
+{
+    __syncthreads();
+    if (*lost != 0) {
+        if (threadIdx.x == 0) atomicExch(&g_tc_lost, 1u);
+        const long long t0 = clock64();
+        while (clock64() - t0 < kWaitLimitCycles / 8) {}
+        __syncthreads();
+    }
+    tc_fence_after();
+    if (frees) tmem_free(tmem);
+}
+
+// The maps of a call's tensors: blocks of 64 elements of `heads` heads of
+// `tokens` tokens.
+struct Maps {
+    CUtensorMap q, k, v, dout;
+};
+
+// Heads that share a tile in the forward pass, tokens of a tile.
+struct Packing {
+    int heads, tokens;
+};
+
+// Columns [0, n) of the warp's rows, times k, as bf16 to rows of a tensor in memory.
+__device__ __forceinline__ void store_row(uint32_t tmem, int n, float k, char* row, bool live)
+{
+    for (int c = 0; c < n; c += 32) {
+        uint32_t r[32];
+        tmem_load32(tmem + c, r);
+        tmem_wait(r);
+        if (!live) continue;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            if (c + 8 * v >= n) break;
+            uint4 w;
+            uint32_t* u = &w.x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                u[i] = pack_bf16x2(__uint_as_float(r[8 * v + 2 * i]) * k,
+                                   __uint_as_float(r[8 * v + 2 * i + 1]) * k);
+            *reinterpret_cast<uint4*>(row + 2 * (c + 8 * v)) = w;
+        }
+    }
+}
+
+__device__ __forceinline__ void zero_row(int n, char* row, bool live)
+{
+    if (!live) return;
+    for (int c = 0; c < n; c += 8)
+        *reinterpret_cast<uint4*>(row + 2 * c) = make_uint4(0, 0, 0, 0);
+}
+
+__device__ __forceinline__ char* row_of(const Heads& x, int64_t t, int h)
+{
+    return x.p + 2 * (t * x.ld + (int64_t)h * x.hs);
+}
+
+// ------------------------------------------------------------ forward
+//
+// A block has two tiles of 128 rows, which share the keys and values it loads:
+// while the softmax warps of one are at work, the tensor cores have the other's
+// products.  A tile's rows are tokens times the query heads of one key head
+// (row = token * heads + head), where these divide 128 well enough, so that grouped
+// heads share keys and few queries fill a tile.
+//
+// Tensor memory, in columns of 32 bits: scores of the tiles at 0 and 128, each
+// overwritten by its probabilities; outputs at 256 and 384.
+
+constexpr int kFwdThreads = 320;    // 8 softmax warps, TMA, products
+
+template <int BLOCKS>
+struct FwdShape {
+    static constexpr int kTile = BLOCKS * kTcBlock;
+    static constexpr int kStages = 2;
+    static constexpr int kQ = 0, kK = 2 * kTile, kV = kK + kStages * kTile;
+    static constexpr int kBars = kV + kStages * kTile;
+    static constexpr int kBytes = kBars + 256 + 1024;   // the base is rounded up to 1024
+};
+
+struct FwdBars {
+    uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2];
+    uint32_t tmem;
+    int lost;
+};
+static_assert(sizeof(FwdBars) <= 256, "the barriers' place");
+
+// One tile of scores: probabilities to tensor memory, maximum and sum of the row.
+struct RowStats {
+    float top, shift, sum;   // running maximum, its product with the factor, sum
+};
+
+template <int BLOCKS>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+k_attn_tc(const __grid_constant__ Maps maps, AttnArgs a, Packing pk)
+{
+    using S = FwdShape<BLOCKS>;
+    extern __shared__ char smem_raw[];
+    char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+    FwdBars& bar = *reinterpret_cast<FwdBars*>(smem + S::kBars);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait_prior();
+    if (warp == 9) {
+        // before the next kernel may be placed beside this block and ask for its own
+        tmem_alloc(&bar.tmem);
+    } else if (threadIdx.x == 0) {
+        mbar_init(&bar.q_full, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.k_full[i], 1);
+            mbar_init(&bar.k_empty[i], 1);
+            mbar_init(&bar.v_full[i], 1);
+            mbar_init(&bar.v_empty[i], 1);
+            mbar_init(&bar.s_full[i], 1);
+            mbar_init(&bar.p_full[i], 4);
+            mbar_init(&bar.o_done[i], 1);
+        }
+        bar.lost = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_launch_dependents();
+    volatile int* lost = &bar.lost;
+    const uint32_t tmem = bar.tmem;
+
+    // the tiles at the end of a sequence see the most keys and go first
+    const Tile t = find_tile(a, gridDim.x - 1 - blockIdx.x, 2 * pk.tokens, false);
+    const int h0 = (int)blockIdx.y * pk.heads, hk = h0 / (a.Hq / a.Hk);
+    const int ksteps = (a.D + 15) / 16, width = ksteps * 16;
+    // keys that each tile sees, in tiles of 128
+    int end[2], tiles[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row0 = t.row0 + i * pk.tokens;
+        end[i] = !t.any || row0 >= t.nq ? 0
+                 : !a.causal            ? t.nk
+                                        : max(0, min(t.nk, min(row0 + pk.tokens, t.nq) + t.nk - t.nq));
+        tiles[i] = (end[i] + kTcRows - 1) / kTcRows;
+    }
+    const int n = max(tiles[0], tiles[1]);
+
+    if (warp == 8) {
+        // ---- loads
+        if (lane == 0 && n > 0) {
+            const uint32_t q_bytes = (uint32_t)(pk.heads * pk.tokens) * 128 * BLOCKS;
+            mbar_expect_tx(&bar.q_full, q_bytes * ((tiles[0] > 0) + (tiles[1] > 0)));
+            for (int i = 0; i < 2; ++i)
+                for (int b = 0; b < BLOCKS && tiles[i] > 0; ++b)
+                    tma_load(smem + S::kQ + i * S::kTile + b * kTcBlock, &maps.q, &bar.q_full,
+                             b * kTcCols, h0, (int)(t.q0 + t.row0) + i * pk.tokens);
+            bool going = true;
+            int j = 0;
+            for (; j < n && going; ++j) {
+                const int st = j & 1, round = j >> 1;
+                if (round > 0) going = tc_wait(&bar.k_empty[st], (round - 1) & 1, lost);
+                if (!going) break;
+                mbar_expect_tx(&bar.k_full[st], S::kTile);
+                for (int b = 0; b < BLOCKS; ++b)
+                    tma_load(smem + S::kK + st * S::kTile + b * kTcBlock, &maps.k, &bar.k_full[st],
+                             b * kTcCols, hk, (int)t.k0 + j * kTcRows);
+                if (round > 0) going = tc_wait(&bar.v_empty[st], (round - 1) & 1, lost);
+                if (!going) break;
+                mbar_expect_tx(&bar.v_full[st], S::kTile);
+                for (int b = 0; b < BLOCKS; ++b)
+                    tma_load(smem + S::kV + st * S::kTile + b * kTcBlock, &maps.v, &bar.v_full[st],
+                             b * kTcCols, hk, (int)t.k0 + j * kTcRows);
+            }
+        }
+    } else if (warp == 9) {
+        // ---- products
+        const uint32_t s_desc = tc_idesc(kTcRows, false), o_desc = tc_idesc(width, true);
+        bool going = n > 0 && tc_wait_warp(&bar.q_full, 0, lost);
+        going = going && tc_wait_warp(&bar.k_full[0], 0, lost);
+        if (going) {
+            if (lane == 0) {
+                for (int i = 0; i < 2; ++i)
+                    if (tiles[i] > 0) {
+                        tc_dot(tmem + i * 128, smem + S::kQ + i * S::kTile, smem + S::kK, ksteps,
+                               s_desc);
+                        tc_commit(&bar.s_full[i]);
+                    }
+                tc_commit(&bar.k_empty[0]);
+            }
+            __syncwarp();
+        }
+        for (int j = 0; j < n && going; ++j) {
+            const int st = j & 1, par = (j >> 1) & 1, nst = st ^ 1, npar = ((j + 1) >> 1) & 1;
+            going = tc_wait_warp(&bar.v_full[st], par, lost);
+            if (!going) break;
+            const char* v = smem + S::kV + st * S::kTile;
+            const int rows = t.nk - j * kTcRows;
+            if (rows < kTcRows) {
+                clear_rows(smem + S::kV + st * S::kTile, rows, BLOCKS);
+                fence_async_proxy();
+                __syncwarp();
+            }
+            if (j + 1 < n) going = tc_wait_warp(&bar.k_full[nst], npar, lost);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (!going || j >= tiles[i]) continue;
+                going = tc_wait_warp(&bar.p_full[i], j & 1, lost);
+                if (!going) continue;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t p = tmem + i * 128;
+                    tc_rows(tmem + 256 + i * 128, [&](int k) { return p + 8 * k; }, v, o_desc, j > 0);
+                    tc_commit(&bar.o_done[i]);
+                }
+                __syncwarp();
+                if (j + 1 < tiles[i]) {
+                    // the next scores take the probabilities' place
+                    going = tc_wait_warp(&bar.o_done[i], j & 1, lost);
+                    if (!going) continue;
+                    if (lane == 0) {
+                        tc_dot(tmem + i * 128, smem + S::kQ + i * S::kTile,
+                               smem + S::kK + nst * S::kTile, ksteps, s_desc);
+                        tc_commit(&bar.s_full[i]);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (lane == 0 && going) {
+                tc_commit(&bar.v_empty[st]);
+                if (j + 1 < n) tc_commit(&bar.k_empty[nst]);
+            }
+        }
+    } else {
+        // ---- softmax: warps 0-3 have tile 0, warps 4-7 tile 1
+        const int i = warp >> 2, r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_at = tmem + i * 128 + lanes, o_at = tmem + 256 + i * 128 + lanes;
+        const int row = t.row0 + i * pk.tokens + r / pk.heads, head = h0 + r % pk.heads;
+        const bool live = t.any && r < pk.heads * pk.tokens && row < t.nq;
+        // rows that are not stored need no mask
+        const int seen = live && a.causal ? min(t.nk, row + t.nk - t.nq + 1) : t.nk;
+        const int my_tiles = i ? tiles[1] : tiles[0];
+        const float c2 = a.scale * kLog2e;
+        float top = -INFINITY, shift = 0.0f;
+        F2 sum[2] = {0, 0};
+        bool going = true;
+        for (int j = 0; j < my_tiles; ++j) {
+            going = tc_wait_warp(&bar.s_full[i], j & 1, lost);
+            if (!going) break;
+            tc_fence_after();
+            uint32_t s[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_load32(s_at + 32 * c, s + 32 * c);
+            tmem_wait(s);
+            const int most = seen - j * kTcRows;     // columns below it are visible
+            if (__any_sync(0xffffffffu, most < kTcRows)) {
+#pragma unroll
+                for (int c = 0; c < 128; ++c)
+                    if (c >= most) s[c] = 0xff800000u;
+            }
+            float m[4] = {top, top, top, top};
+#pragma unroll
+            for (int c = 0; c < 128; c += 8)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    m[e] = fmaxf(m[e], fmaxf(__uint_as_float(s[c + e]), __uint_as_float(s[c + 4 + e])));
+            const float next = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+            // the shift follows the maximum only once it lags by a factor of 2^8,
+            // which bf16 probabilities and fp32 sums do not notice
+            const float want = next == -INFINITY ? 0.0f : next * c2;
+            const bool move = top == -INFINITY ? next > -INFINITY : want - shift > 8.0f;
+            if (__any_sync(0xffffffffu, move)) {
+                const float fade = top == -INFINITY ? 0.0f : ex2(shift - want);
+                if (j > 0) {
+                    going = tc_wait_warp(&bar.o_done[i], (j - 1) & 1, lost);
+                    if (!going) break;
+                    tc_fence_after();
+                    for (int c = 0; c < width; c += 32) {
+                        uint32_t o[32];
+                        tmem_load32(o_at + c, o);
+                        tmem_wait(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * fade);
+                        tmem_store32(o_at + c, o);
+                    }
+                    sum[0] = mul2(sum[0], pack2(fade, fade));
+                    sum[1] = mul2(sum[1], pack2(fade, fade));
+                }
+                top = next;
+                shift = want;
+            }
+            const F2 cc = pack2(c2, c2), mm = pack2(-shift, -shift);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t p[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const int c = 64 * h + 2 * e;
+                    const F2 u = fma2((F2)s[c + 1] << 32 | s[c], cc, mm);
+                    const float x = ex2(lo2(u)), y = ex2(hi2(u));
+                    sum[e & 1] = add2(sum[e & 1], pack2(x, y));
+                    p[e] = pack_bf16x2(x, y);
+                }
+                tmem_store32(s_at + 32 * h, p);
+            }
+            tmem_wait_stores();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.p_full[i]);
+        }
+        if (going && my_tiles > 0) going = tc_wait_warp(&bar.o_done[i], (my_tiles - 1) & 1, lost);
+        const F2 both = add2(sum[0], sum[1]);
+        const float total = lo2(both) + hi2(both);
+        char* out = live ? row_of(a.out, t.q0 + row, head) : nullptr;
+        if (going && my_tiles > 0) {
+            tc_fence_after();
+            store_row(o_at, a.D, total == 0.0f ? 0.0f : 1.0f / total, out, live);
+        } else if (going) {
+            zero_row(a.D, out, live);
+        }
+        if (a.lse != nullptr && live)
+            a.lse[(int64_t)head * a.Tq + t.q0 + row] =
+                !going ? __int_as_float(0x7fc00000)
+                : total == 0.0f ? -INFINITY : (shift + log2f(total)) * kLn2;
+    }
+
+    tc_finish(lost, tmem, warp == 9);
+}
+
+// ------------------------------------------------------------ gradient of the queries
+//
+// A block has 128 queries of one head and walks over the keys:
+//   scores and dout v^T (tensor memory, columns 0 and 128) -> ds in bf16 (384)
+//   -> dq += ds k (256).
+// The compute warps copy both products to registers before they work on them, so
+// the next tile's two run meanwhile, and dq's behind them.  Warps 0-3 have the
+// first 64 keys of a tile, 4-7 the others.
+
+constexpr int kGradThreads = 320;
+
+struct GradBars {
+    uint64_t once_full, in_full[2], in_empty[2], s_full, s_free, g_full, p_full, d_full, d_free;
+    uint32_t tmem;
+    int lost;
+};
+static_assert(sizeof(GradBars) <= 256, "the barriers' place");
+
+template <int BLOCKS>
+struct GradShape {
+    static constexpr int kTile = BLOCKS * kTcBlock;
+    static constexpr int kA = 0, kB = kTile;                 // what stays: q, dout or k, v
+    static constexpr int kIn = 2 * kTile;                    // two stages of the others
+    static constexpr int kRows = kIn + 4 * kTile;            // 2 x 2 x 128 floats
+    static constexpr int kBars = kRows + 2048;
+    static constexpr int kBytes = kBars + 256 + 1024;
+};
+
+__device__ __forceinline__ void grad_init(GradBars& bar)
+{
+    mbar_init(&bar.once_full, 1);
+    for (int i = 0; i < 2; ++i) {
+        mbar_init(&bar.in_full[i], 1);
+        mbar_init(&bar.in_empty[i], 1);
+    }
+    mbar_init(&bar.s_full, 1);
+    mbar_init(&bar.s_free, 8);
+    mbar_init(&bar.g_full, 1);
+    mbar_init(&bar.p_full, 8);
+    mbar_init(&bar.d_full, 8);
+    mbar_init(&bar.d_free, 1);
+    bar.lost = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+
+template <int BLOCKS>
+__global__ void __launch_bounds__(kGradThreads, 1)
+k_attn_tc_dq(const __grid_constant__ Maps maps, AttnArgs a)
+{
+    using S = GradShape<BLOCKS>;
+    extern __shared__ char smem_raw[];
+    char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+    GradBars& bar = *reinterpret_cast<GradBars*>(smem + S::kBars);
+    float* delta_s = reinterpret_cast<float*>(smem + S::kRows);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait_prior();
+    if (warp == 9) tmem_alloc(&bar.tmem);
+    else if (threadIdx.x == 0) grad_init(bar);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_launch_dependents();
+    volatile int* lost = &bar.lost;
+    const uint32_t tmem = bar.tmem;
+
+    const Tile t = find_tile(a, gridDim.x - 1 - blockIdx.x, kTcRows, false);
+    const int h = blockIdx.y, hk = h / (a.Hq / a.Hk);
+    const int ksteps = (a.D + 15) / 16, width = ksteps * 16;
+    const int end = !t.any ? 0
+                    : !a.causal ? t.nk
+                                : max(0, min(t.nk, min(t.row0 + kTcRows, t.nq) + t.nk - t.nq));
+    const int n = (end + kTcRows - 1) / kTcRows;
+
+    if (warp == 8) {
+        if (lane == 0 && n > 0) {
+            mbar_expect_tx(&bar.once_full, 2 * S::kTile);
+            for (int b = 0; b < BLOCKS; ++b) {
+                tma_load(smem + S::kA + b * kTcBlock, &maps.q, &bar.once_full, b * kTcCols, h,
+                         (int)t.q0 + t.row0);
+                tma_load(smem + S::kB + b * kTcBlock, &maps.dout, &bar.once_full, b * kTcCols, h,
+                         (int)t.q0 + t.row0);
+            }
+            for (int j = 0; j < n; ++j) {
+                const int st = j & 1, round = j >> 1;
+                if (round > 0 && !tc_wait(&bar.in_empty[st], (round - 1) & 1, lost)) break;
+                char* in = smem + S::kIn + st * 2 * S::kTile;
+                mbar_expect_tx(&bar.in_full[st], 2 * S::kTile);
+                for (int b = 0; b < BLOCKS; ++b) {
+                    tma_load(in + b * kTcBlock, &maps.k, &bar.in_full[st], b * kTcCols, hk,
+                             (int)t.k0 + j * kTcRows);
+                    tma_load(in + S::kTile + b * kTcBlock, &maps.v, &bar.in_full[st], b * kTcCols,
+                             hk, (int)t.k0 + j * kTcRows);
+                }
+            }
+        }
+    } else if (warp == 9) {
+        const uint32_t s_desc = tc_idesc(kTcRows, false), o_desc = tc_idesc(width, true);
+        bool going = n > 0 && tc_wait_warp(&bar.once_full, 0, lost);
+        // dq += ds k of tile j
+        const auto add_dq = [&](int j) {
+            going = tc_wait_warp(&bar.d_full, j & 1, lost);
+            if (!going) return;
+            tc_fence_after();
+            if (lane == 0) {
+                tc_rows(tmem + 256, [&](int k) { return tmem + 384 + 8 * k; },
+                        smem + S::kIn + (j & 1) * 2 * S::kTile, o_desc, j > 0);
+                tc_commit(&bar.d_free);
+                tc_commit(&bar.in_empty[j & 1]);
+            }
+            __syncwarp();
+        };
+        for (int j = 0; j < n && going; ++j) {
+            const int st = j & 1;
+            going = tc_wait_warp(&bar.in_full[st], (j >> 1) & 1, lost);
+            if (!going) break;
+            char* in = smem + S::kIn + st * 2 * S::kTile;
+            const int rows = t.nk - j * kTcRows;
+            if (rows < kTcRows) {     // dq sums over the keys
+                clear_rows(in, rows, BLOCKS);
+                fence_async_proxy();
+                __syncwarp();
+            }
+            if (j > 0) going = tc_wait_warp(&bar.s_free, (j - 1) & 1, lost);
+            if (!going) break;
+            tc_fence_after();
+            if (lane == 0) {
+                tc_dot(tmem, smem + S::kA, in, ksteps, s_desc);
+                tc_dot(tmem + 128, smem + S::kB, in + S::kTile, ksteps, s_desc);
+                tc_commit(&bar.s_full);
+            }
+            __syncwarp();
+            if (j > 0) add_dq(j - 1);
+        }
+        if (going && n > 0) add_dq(n - 1);
+    } else {
+        const int r = (warp & 3) * 32 + lane, half = warp >> 2;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const int row = t.row0 + r;
+        const bool live = t.any && row < t.nq;
+        // delta of 16 rows, two at a time
+        for (int q = 0; q < 16; q += 2) {
+            const int rr = warp * 16 + q + (lane >> 4), d = (lane & 15) * 8;
+            float y = 0.0f;
+            if (t.any && t.row0 + rr < t.nq && d < a.D) {
+                const int64_t at = t.q0 + t.row0 + rr;
+                const uint4 u = *reinterpret_cast<const uint4*>(row_of(a.dout, at, h) + 2 * d);
+                const uint4 w = *reinterpret_cast<const uint4*>(row_of(a.out, at, h) + 2 * d);
+                const uint32_t us[4] = {u.x, u.y, u.z, u.w}, ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    y = fmaf(bf16_hi(us[e]), bf16_hi(ws[e]), fmaf(bf16_lo(us[e]), bf16_lo(ws[e]), y));
+            }
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+            if ((lane & 15) == 0) {
+                delta_s[rr] = y;
+                if (t.any && t.row0 + rr < t.nq) a.delta[(int64_t)h * a.Tq + t.q0 + t.row0 + rr] = y;
+            }
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");    // the compute warps
+        const float delta = delta_s[r];
+        const float lse = live ? a.lse[(int64_t)h * a.Tq + t.q0 + row] : -INFINITY;
+        const bool none = lse == -INFINITY;
+        const int seen = none ? 0 : a.causal ? min(t.nk, row + t.nk - t.nq + 1) : t.nk;
+        const float c2 = a.scale * kLog2e;
+        const F2 cc = pack2(c2, c2), nl = pack2(-lse * kLog2e, -lse * kLog2e);
+        const F2 nd = pack2(-delta, -delta);
+        bool going = true;
+        for (int j = 0; j < n; ++j) {
+            going = tc_wait_warp(&bar.s_full, j & 1, lost);
+            if (!going) break;
+            tc_fence_after();
+            uint32_t x[128];      // 64 scores, 64 of dout v^T
+            tmem_load32(tmem + lanes + 64 * half, x);
+            tmem_load32(tmem + lanes + 64 * half + 32, x + 32);
+            tmem_load32(tmem + lanes + 128 + 64 * half, x + 64);
+            tmem_load32(tmem + lanes + 128 + 64 * half + 32, x + 96);
+            tmem_wait(x);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.s_free);
+            uint32_t ds[32];
+            const int most = seen - j * kTcRows - 64 * half;
+            const bool mask = __any_sync(0xffffffffu, most < 64);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                const F2 u = fma2((F2)x[2 * e + 1] << 32 | x[2 * e], cc, nl);
+                const F2 p = pack2(ex2(lo2(u)), ex2(hi2(u)));
+                const F2 d = mul2(p, add2((F2)x[64 + 2 * e + 1] << 32 | x[64 + 2 * e], nd));
+                ds[e] = pack_bf16x2(lo2(d), hi2(d));
+            }
+            if (mask) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    ds[e] = 2 * e + 1 < most ? ds[e] : 2 * e < most ? ds[e] & 0xffffu : 0u;
+            }
+            if (j > 0) going = tc_wait_warp(&bar.d_free, (j - 1) & 1, lost);
+            if (!going) break;
+            tc_fence_after();
+            tmem_store32(tmem + lanes + 384 + 32 * half, ds);
+            tmem_wait_stores();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.d_full);
+        }
+        if (going && n > 0) going = tc_wait_warp(&bar.d_free, (n - 1) & 1, lost);
+        if (going) {
+            tc_fence_after();
+            // a thread's half of its row, in whole 32 columns
+            const int first = half * BLOCKS * 32, cols = min(a.D - first, BLOCKS * 32);
+            char* out = live ? row_of(a.dq, t.q0 + row, h) + 2 * first : nullptr;
+            if (n > 0) store_row(tmem + lanes + 256 + first, cols, a.scale, out, live);
+            else zero_row(cols, out, live);
+        }
+    }
+    tc_finish(lost, tmem, warp == 9);
+}
+
+// ------------------------------------------------------------ gradients of keys and values
+//
+// A block has 128 keys of one key head and walks over the queries of all query
+// heads that share it.  Scores are transposed, keys along the rows, so that both
+// probabilities and ds are left operands as they are:
+//   s^T = k q^T (0) -> p^T in bf16 -> dv += p^T dout (256)
+//   dp^T = v dout^T (128) -> ds^T in bf16 -> dk += ds^T q (384, or 320 for 64 columns)
+// p^T and ds^T take the places of what they were made from, each warp writing
+// over columns that only it has read.  The products alternate with the
+// compute warps' two halves: dv and the next scores run while ds is computed, dk
+// and the next dp while p is.
+
+template <int BLOCKS>
+__global__ void __launch_bounds__(kGradThreads, 1)
+k_attn_tc_dkv(const __grid_constant__ Maps maps, AttnArgs a)
+{
+    using S = GradShape<BLOCKS>;
+    constexpr uint32_t kDv = 256, kDk = BLOCKS == 2 ? 384 : 320;
+    extern __shared__ char smem_raw[];
+    char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+    GradBars& bar = *reinterpret_cast<GradBars*>(smem + S::kBars);
+    float* rows_s = reinterpret_cast<float*>(smem + S::kRows);   // [stage][-lse log2e, -delta][128]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait_prior();
+    if (warp == 9) tmem_alloc(&bar.tmem);
+    else if (threadIdx.x == 0) grad_init(bar);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_launch_dependents();
+    volatile int* lost = &bar.lost;
+    const uint32_t tmem = bar.tmem;
+
+    // the first keys of a sequence are seen by the most queries: tiles in order
+    const Tile t = find_tile(a, blockIdx.x, kTcRows, true);
+    const int hk = blockIdx.y, G = a.Hq / a.Hk;
+    const int ksteps = (a.D + 15) / 16, width = ksteps * 16;
+    // the tiles of queries from the first that sees this tile's first key
+    const int first = a.causal ? max(0, t.row0 - (t.nk - t.nq)) / kTcRows * kTcRows : 0;
+    const int per = t.any && first < t.nq ? (t.nq - first + kTcRows - 1) / kTcRows : 0;
+    const int n = per * G;
+
+    if (warp == 8) {
+        if (n > 0) {
+            if (lane == 0) {
+                mbar_expect_tx(&bar.once_full, 2 * S::kTile);
+                for (int b = 0; b < BLOCKS; ++b) {
+                    tma_load(smem + S::kA + b * kTcBlock, &maps.k, &bar.once_full, b * kTcCols, hk,
+                             (int)t.k0 + t.row0);
+                    tma_load(smem + S::kB + b * kTcBlock, &maps.v, &bar.once_full, b * kTcCols, hk,
+                             (int)t.k0 + t.row0);
+                }
+            }
+            int h = hk * G, i0 = first;
+            for (int j = 0; j < n; ++j) {
+                const int st = j & 1, round = j >> 1;
+                float nl[4], nd[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int row = i0 + 32 * e + lane;
+                    const int64_t at = (int64_t)h * a.Tq + t.q0 + row;
+                    const float l = row < t.nq ? a.lse[at] : -INFINITY;
+                    nl[e] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+                    nd[e] = row < t.nq ? -a.delta[at] : 0.0f;
+                }
+                if (round > 0 && !tc_wait_warp(&bar.in_empty[st], (round - 1) & 1, lost)) break;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    rows_s[st * 256 + 32 * e + lane] = nl[e];
+                    rows_s[st * 256 + 128 + 32 * e + lane] = nd[e];
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    char* in = smem + S::kIn + st * 2 * S::kTile;
+                    mbar_expect_tx(&bar.in_full[st], 2 * S::kTile);
+                    for (int b = 0; b < BLOCKS; ++b) {
+                        tma_load(in + b * kTcBlock, &maps.q, &bar.in_full[st], b * kTcCols, h,
+                                 (int)t.q0 + i0);
+                        tma_load(in + S::kTile + b * kTcBlock, &maps.dout, &bar.in_full[st],
+                                 b * kTcCols, h, (int)t.q0 + i0);
+                    }
+                }
+                i0 += kTcRows;
+                if (i0 >= t.nq) {
+                    i0 = first;
+                    ++h;
+                }
+            }
+        }
+    } else if (warp == 9) {
+        const uint32_t s_desc = tc_idesc(kTcRows, false), o_desc = tc_idesc(width, true);
+        const auto operand = [&](uint32_t at) {
+            return [=](int k) { return at + 8 * (k & 3) + 64 * (k >> 2); };
+        };
+        bool going = n > 0 && tc_wait_warp(&bar.once_full, 0, lost);
+        // waits for tile j, clears what lies beyond the sequence, issues its scores
+        const auto scores = [&](int j) {
+            const int st = j & 1, rows = t.nq - (first + j % per * kTcRows);
+            going = tc_wait_warp(&bar.in_full[st], (j >> 1) & 1, lost);
+            if (!going) return;
+            char* in = smem + S::kIn + st * 2 * S::kTile;
+            if (rows < kTcRows) {     // dk and dv sum over the queries
+                clear_rows(in, rows, BLOCKS);
+                clear_rows(in + S::kTile, rows, BLOCKS);
+                fence_async_proxy();
+                __syncwarp();
+            }
+            if (lane == 0) {
+                tc_dot(tmem, smem + S::kA, in, ksteps, s_desc);
+                tc_commit(&bar.s_full);
+            }
+            __syncwarp();
+        };
+        const auto grads = [&](int j) {
+            if (lane == 0) {
+                tc_dot(tmem + 128, smem + S::kB, smem + S::kIn + (j & 1) * 2 * S::kTile + S::kTile,
+                       ksteps, s_desc);
+                tc_commit(&bar.g_full);
+            }
+            __syncwarp();
+        };
+        if (going) scores(0);
+        if (going) grads(0);
+        for (int j = 0; j < n && going; ++j) {
+            const char* in = smem + S::kIn + (j & 1) * 2 * S::kTile;
+            going = tc_wait_warp(&bar.p_full, j & 1, lost);
+            if (!going) break;
+            tc_fence_after();
+            if (lane == 0) {
+                tc_rows(tmem + kDv, operand(tmem), in + S::kTile, o_desc, j > 0);
+                tc_commit(&bar.d_free);
+            }
+            __syncwarp();
+            if (j + 1 < n) {
+                // the next scores take the probabilities' place
+                going = tc_wait_warp(&bar.d_free, 0, lost);
+                if (going) scores(j + 1);
+            } else {
+                going = tc_wait_warp(&bar.d_free, 0, lost);
+            }
+            if (!going) break;
+            going = tc_wait_warp(&bar.d_full, j & 1, lost);
+            if (!going) break;
+            tc_fence_after();
+            if (lane == 0) {
+                tc_rows(tmem + kDk, operand(tmem + 128), in, o_desc, j > 0);
+                tc_commit(&bar.in_empty[j & 1]);
+                tc_commit(&bar.d_free);
+            }
+            __syncwarp();
+            going = tc_wait_warp(&bar.d_free, 1, lost);
+            if (going && j + 1 < n) grads(j + 1);
+        }
+        // the compute warps wait here for the last product
+        if (going && n > 0 && lane == 0) tc_commit(&bar.s_full);
+    } else {
+        const int r = (warp & 3) * 32 + lane, half = warp >> 2;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const int row = t.row0 + r;
+        const bool live = t.any && row < t.nk;
+        const float c2 = a.scale * kLog2e;
+        const F2 cc = pack2(c2, c2);
+        bool going = true;
+        for (int j = 0; j < n; ++j) {
+            const int st = j & 1, i0 = first + j % per * kTcRows;
+            const float* nl = rows_s + st * 256 + 64 * half;
+            const float* nd = nl + 128;
+            going = tc_wait_warp(&bar.in_full[st], (j >> 1) & 1, lost) &&
+                    tc_wait_warp(&bar.s_full, j & 1, lost);
+            if (!going) break;
+            tc_fence_after();
+            uint32_t s[64];
+            tmem_load32(tmem + lanes + 64 * half, s);
+            tmem_load32(tmem + lanes + 64 * half + 32, s + 32);
+            tmem_wait(s);
+            // columns from `from` on see this row's key
+            const int from = a.causal ? row - (t.nk - t.nq) - i0 - 64 * half : 0;
+            const bool mask = __any_sync(0xffffffffu, from > 0);
+            uint32_t p[32];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+                const float4 l = *reinterpret_cast<const float4*>(nl + 2 * e);
+                const F2 u = fma2((F2)s[2 * e + 1] << 32 | s[2 * e], cc, pack2(l.x, l.y));
+                const F2 v = fma2((F2)s[2 * e + 3] << 32 | s[2 * e + 2], cc, pack2(l.z, l.w));
+                float y[4] = {ex2(lo2(u)), ex2(hi2(u)), ex2(lo2(v)), ex2(hi2(v))};
+                if (mask) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (2 * e + k < from) y[k] = 0.0f;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s[2 * e + k] = __float_as_uint(y[k]);
+                p[e] = pack_bf16x2(y[0], y[1]);
+                p[e + 1] = pack_bf16x2(y[2], y[3]);
+            }
+            tmem_store32(tmem + lanes + 64 * half, p);
+            tmem_wait_stores();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.p_full);
+            going = tc_wait_warp(&bar.g_full, j & 1, lost);
+            if (!going) break;
+            tc_fence_after();
+            uint32_t g[64];
+            tmem_load32(tmem + lanes + 128 + 64 * half, g);
+            tmem_load32(tmem + lanes + 128 + 64 * half + 32, g + 32);
+            tmem_wait(g);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+                const float4 l = *reinterpret_cast<const float4*>(nd + 2 * e);
+                F2 u = mul2((F2)s[2 * e + 1] << 32 | s[2 * e],
+                            add2((F2)g[2 * e + 1] << 32 | g[2 * e], pack2(l.x, l.y)));
+                F2 v = mul2((F2)s[2 * e + 3] << 32 | s[2 * e + 2],
+                            add2((F2)g[2 * e + 3] << 32 | g[2 * e + 2], pack2(l.z, l.w)));
+                p[e] = pack_bf16x2(lo2(u), hi2(u));
+                p[e + 1] = pack_bf16x2(lo2(v), hi2(v));
+            }
+            if (mask) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    p[e] = 2 * e >= from ? p[e] : 2 * e + 1 >= from ? p[e] & 0xffff0000u : 0u;
+            }
+            tmem_store32(tmem + lanes + 128 + 64 * half, p);
+            tmem_wait_stores();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.d_full);
+        }
+        if (going && n > 0) going = tc_wait_warp(&bar.s_full, n & 1, lost);
+        if (going) {
+            tc_fence_after();
+            const int begin = half * BLOCKS * 32, cols = min(a.D - begin, BLOCKS * 32);
+            char* dv = live ? row_of(a.dv, t.k0 + row, hk) + 2 * begin : nullptr;
+            char* dk = live ? row_of(a.dk, t.k0 + row, hk) + 2 * begin : nullptr;
+            if (n > 0) {
+                store_row(tmem + lanes + kDv + begin, cols, 1.0f, dv, live);
+                store_row(tmem + lanes + kDk + begin, cols, a.scale, dk, live);
+            } else {
+                zero_row(cols, dv, live);
+                zero_row(cols, dk, live);
+            }
+        }
+    }
+    tc_finish(lost, tmem, warp == 9);
+}
+
+// ------------------------------------------------------------ launches
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's encoder of tensor maps, looked up once.
+EncodeFn encoder()
+{
+    static const EncodeFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult res = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &res) != cudaSuccess ||
+            res != cudaDriverEntryPointSuccess) {
+            (void)cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
+}
+
+// Elements, heads and tokens of x; a box is 64 elements of `heads` heads of
+// `tokens` tokens.  What lies outside reads as zeros.
+bool make_map(CUtensorMap* m, const Heads& x, int64_t T, int H, int D, int heads, int tokens)
+{
+    const EncodeFn fn = encoder();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
+    const cuuint64_t strides[2] = {(cuuint64_t)x.hs * 2, (cuuint64_t)x.ld * 2};
+    const cuuint32_t box[3] = {kTcCols, (cuuint32_t)heads, (cuuint32_t)tokens};
+    const cuuint32_t step[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, x.p, dims, strides, box, step,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool aligned(const Heads& x)
+{
+    return reinterpret_cast<uintptr_t>(x.p) % 16 == 0 && x.ld % 8 == 0 && x.hs % 8 == 0 &&
+           x.ld < int64_t(1) << 38 && x.hs < int64_t(1) << 38;
+}
+
+// Query heads that share a tile, and its tokens.
+Packing packing_of(const AttnArgs& a)
+{
+    const int G = a.Hq / a.Hk;
+    const int heads = G <= 32 ? G : 1;
+    return {heads, kTcRows / heads};
+}
+
+template <class Kernel, class... Args>
+cudaError_t launch_tc(Kernel fn, SmemRaisedOn& raised, size_t smem, int64_t blocks, int heads,
+                      int threads, cudaStream_t s, Args... args)
+{
+    const cudaError_t e = raise_smem(raised, reinterpret_cast<const void*>(fn), smem);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(fn, dim3((unsigned)blocks, (unsigned)heads), dim3(threads), smem, s, true,
+                         0u, args...);
+}
+
+template <class F>
+cudaError_t by_blocks(int D, F&& f)
+{
+    return D <= kTcCols ? f(std::integral_constant<int, 1>{}) : f(std::integral_constant<int, 2>{});
+}
+
+}  // namespace
+
+bool attn_tc_takes(const AttnArgs& a, bool grad)
+{
+    return a.dt == DPZ_BF16 && a.D % 8 == 0 && a.Tq > 0 && a.Tk > 0 && aligned(a.q) &&
+           aligned(a.k) && aligned(a.v) && aligned(a.out) &&
+           (!grad || (aligned(a.dout) && aligned(a.dq) && aligned(a.dk) && aligned(a.dv)));
+}
+
+cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t s)
+{
+    set_last_kernel_name("attn_forward");
+    const Packing pk = packing_of(a);
+    Maps m;
+    if (!make_map(&m.q, a.q, a.Tq, a.Hq, a.D, pk.heads, pk.tokens) ||
+        !make_map(&m.k, a.k, a.Tk, a.Hk, a.D, 1, kTcRows) ||
+        !make_map(&m.v, a.v, a.Tk, a.Hk, a.D, 1, kTcRows))
+        return launch_attn_any(a, s);
+    m.dout = m.q;
+    return by_blocks(a.D, [&](auto n) {
+        static SmemRaisedOn raised;
+        return launch_tc(k_attn_tc<n>, raised, FwdShape<n>::kBytes,
+                         tiles_bound(a.cu_q, a.Tq, a.B, 2 * pk.tokens), a.Hq / pk.heads,
+                         kFwdThreads, s, m, a, pk);
+    });
+}
+
+namespace {
+
+bool grad_maps(Maps* m, const AttnArgs& a)
+{
+    return make_map(&m->q, a.q, a.Tq, a.Hq, a.D, 1, kTcRows) &&
+           make_map(&m->k, a.k, a.Tk, a.Hk, a.D, 1, kTcRows) &&
+           make_map(&m->v, a.v, a.Tk, a.Hk, a.D, 1, kTcRows) &&
+           make_map(&m->dout, a.dout, a.Tq, a.Hq, a.D, 1, kTcRows);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tc_dq(const AttnArgs& a, cudaStream_t s)
+{
+    set_last_kernel_name("attn_grad_dq");
+    Maps m;
+    if (!grad_maps(&m, a)) return launch_attn_any_dq(a, s);
+    return by_blocks(a.D, [&](auto n) {
+        static SmemRaisedOn raised;
+        return launch_tc(k_attn_tc_dq<n>, raised, GradShape<n>::kBytes,
+                         tiles_bound(a.cu_q, a.Tq, a.B, kTcRows), a.Hq, kGradThreads, s, m, a);
+    });
+}
+
+cudaError_t launch_attn_tc_dkv(const AttnArgs& a, cudaStream_t s)
+{
+    set_last_kernel_name("attn_grad_dkv");
+    Maps m;
+    if (!grad_maps(&m, a)) return launch_attn_any_dkv(a, s);
+    return by_blocks(a.D, [&](auto n) {
+        static SmemRaisedOn raised;
+        return launch_tc(k_attn_tc_dkv<n>, raised, GradShape<n>::kBytes,
+                         tiles_bound(a.cu_k, a.Tk, a.B, kTcRows), a.Hk, kGradThreads, s, m, a);
+    });
+}
+
+cudaError_t read_and_clear_tc_lost(unsigned* flag)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(flag, g_tc_lost, sizeof(unsigned));
+    if (e != cudaSuccess || *flag == 0) return e;
+    const unsigned zero = 0;
+    return cudaMemcpyToSymbol(g_tc_lost, &zero, sizeof(unsigned));
+}
+
+}  // namespace dpz

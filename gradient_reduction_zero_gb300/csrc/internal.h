@@ -156,6 +156,8 @@ cudaError_t launch_zero1_fused_tma(const Arena& a, const Avg& avg, const AdamArg
                                    bool store_avg, void* grads, float* master, float* m, float* v,
                                    void* weights, void* ws, cudaStream_t s);
 cudaError_t read_and_clear_pipeline_error(unsigned* flag);
+// The same flag of the attention kernels on the tensor cores (attn_tc.cu).
+cudaError_t read_and_clear_tc_lost(unsigned* flag);
 // Launch one staged kernel (DPZ_SELFTEST_* of dpz.h) on the one-tile arena
 // laid out in `buf` (DPZ_SELFTEST_BUF_BYTES), with a barrier that never
 // completes and a short wait bound, so that its wait runs out.  Where the

@@ -611,8 +611,9 @@ DPZ_API const char* dpz_last_error(void);
 DPZ_API const char* dpz_version(void);
 
 /* Device-side error flag of the current device, read and cleared: 1 if any
- * bulk-copy staged kernel (see DPZ_WS_STATUS_OFFSET) gave up on a tile since
- * the last call, else 0.  Synchronous: call it after the work in question has
+ * bulk-copy staged kernel (see DPZ_WS_STATUS_OFFSET) gave up on a tile, or any
+ * attention kernel on a wait of its own (its rows of out or of the gradients are
+ * then not written, and lse is NaN there), since the last call, else 0.  Synchronous: call it after the work in question has
  * finished (for example after cudaStreamSynchronize), not inside a stream
  * capture.  Returns DPZ_ERR_INVALID_ARG for a NULL flag_out, DPZ_ERR_CUDA if
  * the read fails. */
