@@ -65,7 +65,8 @@ struct AttnArgs {
     int64_t Tq, Tk;
     int Hq, Hk, D, dt;
     int64_t B;
-    const void *cu_q, *cu_k;    // NULL: B sequences of equal length
+    const void *cu_q, *cu_k;    // NULL: B sequences of equal length,
+    int len_q, len_k;           // these
     int itype;
     int causal;
     float scale;
@@ -100,14 +101,13 @@ __device__ __forceinline__ int64_t cu_at(const void* cu, int itype, int64_t i, i
     return v < 0 ? 0 : v > T ? T : v;
 }
 
-// The bounds of sequence b: first row and length among T rows of B sequences.
-__device__ __forceinline__ void seq_bounds(const void* cu, int itype, int64_t b, int64_t B,
-                                           int64_t T, int64_t* first, int* n)
+// The bounds of sequence b: first row and length among T rows; `len` each without offsets.
+__device__ __forceinline__ void seq_bounds(const void* cu, int itype, int64_t b, int len, int64_t T,
+                                           int64_t* first, int* n)
 {
     if (cu == nullptr) {
-        const int64_t len = T / B;
         *first = b * len;
-        *n = (int)len;
+        *n = len;
         return;
     }
     const int64_t a = cu_at(cu, itype, b, T), e = cu_at(cu, itype, b + 1, T);
@@ -118,46 +118,51 @@ __device__ __forceinline__ void seq_bounds(const void* cu, int itype, int64_t b,
 // Tile number `tile` of all sequences' tiles of `per` rows, over the queries
 // (of_keys false) or the keys.  Called by whole warps with equal arguments: with
 // offsets, 32 sequences' numbers of tiles are summed at a time.  The number
-// of tiles is at most tiles_bound().
-__device__ __forceinline__ Tile find_tile(const AttnArgs& a, int64_t tile, int per, bool of_keys)
+// of tiles is at most tiles_bound(), below 2^31.
+__device__ __forceinline__ Tile find_tile(const AttnArgs& a, int tile, int per, bool of_keys)
 {
     const void* cu = of_keys ? a.cu_k : a.cu_q;
     const int64_t T = of_keys ? a.Tk : a.Tq;
+    const int len = of_keys ? a.len_k : a.len_q;
     Tile t{};
-    int64_t b = -1;
+    int b = -1;
     if (cu == nullptr) {
-        const int64_t each = (T / a.B + per - 1) / per;
-        if (each > 0 && tile / each < a.B) {
-            b = tile / each;
-            t.row0 = (int)(tile % each) * per;
+        const unsigned each = (unsigned)(len + per - 1) / (unsigned)per;
+        if (each > 0) {
+            const unsigned q = (unsigned)tile / each;
+            if (q < a.B) {
+                b = (int)q;
+                t.row0 = (int)((unsigned)tile - q * each) * per;
+            }
         }
     } else {
         const int lane = threadIdx.x & 31;
+        int left = tile;
         for (int64_t base = 0; base < a.B; base += 32) {
             int64_t first;
-            int len = 0;
-            if (base + lane < a.B) seq_bounds(cu, a.itype, base + lane, a.B, T, &first, &len);
-            const int mine = (int)(((int64_t)len + per - 1) / per);
-            int64_t upto = mine;
+            int n = 0;
+            if (base + lane < a.B) seq_bounds(cu, a.itype, base + lane, 0, T, &first, &n);
+            const int mine = (int)((unsigned)(n + per - 1) / (unsigned)per);
+            int upto = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+                const int v = __shfl_up_sync(0xffffffffu, upto, o);
                 if (lane >= o) upto += v;
             }
-            const unsigned past = __ballot_sync(0xffffffffu, upto > tile);
+            const unsigned past = __ballot_sync(0xffffffffu, upto > left);
             if (past != 0) {
                 const int l = __ffs((int)past) - 1;
-                b = base + l;
-                t.row0 = (int)(tile - __shfl_sync(0xffffffffu, upto - mine, l)) * per;
+                b = (int)base + l;
+                t.row0 = (left - __shfl_sync(0xffffffffu, upto - mine, l)) * per;
                 break;
             }
-            tile -= __shfl_sync(0xffffffffu, upto, 31);
+            left -= __shfl_sync(0xffffffffu, upto, 31);
         }
     }
     t.any = b >= 0;
     if (t.any) {
-        seq_bounds(a.cu_q, a.itype, b, a.B, a.Tq, &t.q0, &t.nq);
-        seq_bounds(a.cu_k, a.itype, b, a.B, a.Tk, &t.k0, &t.nk);
+        seq_bounds(a.cu_q, a.itype, b, a.len_q, a.Tq, &t.q0, &t.nq);
+        seq_bounds(a.cu_k, a.itype, b, a.len_k, a.Tk, &t.k0, &t.nk);
     }
     return t;
 }

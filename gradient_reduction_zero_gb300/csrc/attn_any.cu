@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kAnyThreads) k_attn_any(AttnArgs a)
     float* q = reinterpret_cast<float*>(smem4);
     float *k = q + kRows, *v = k + kRows, *p = v + kRows;
     // the tiles at the end of a sequence see the most keys and go first
-    const Tile t = find_tile(a, gridDim.x - 1 - blockIdx.x, kAnyTile, false);
+    const Tile t = find_tile(a, (int)(gridDim.x - 1 - blockIdx.x), kAnyTile, false);
     if (!t.any) return;
     const int h = blockIdx.y, hk = h / (a.Hq / a.Hk);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kAnyThreads) k_attn_any_dq(AttnArgs a)
     constexpr int kRows = kAnyTile * (DP + 4), DS = DP + 4;
     float* q = reinterpret_cast<float*>(smem4);
     float *dout = q + kRows, *k = dout + kRows, *v = k + kRows, *p = v + kRows;
-    const Tile t = find_tile(a, gridDim.x - 1 - blockIdx.x, kAnyTile, false);
+    const Tile t = find_tile(a, (int)(gridDim.x - 1 - blockIdx.x), kAnyTile, false);
     if (!t.any) return;
     const int h = blockIdx.y, hk = h / (a.Hq / a.Hk);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kAnyThreads) k_attn_any_dkv(AttnArgs a)
     float *v = k + kRows, *q = v + kRows, *dout = q + kRows, *p = dout + kRows,
           *ds = p + kAnyTile * kAnyPs;
     // the first keys of a sequence are seen by the most queries: tiles in order
-    const Tile t = find_tile(a, blockIdx.x, kAnyTile, true);
+    const Tile t = find_tile(a, (int)blockIdx.x, kAnyTile, true);
     if (!t.any) return;
     const int hk = blockIdx.y, G = a.Hq / a.Hk;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;

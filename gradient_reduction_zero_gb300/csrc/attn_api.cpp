@@ -198,6 +198,8 @@ int attn_common(AttnArgs* a, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk, int
     a->B = B;
     a->cu_q = cu_q;
     a->cu_k = cu_k;
+    a->len_q = (int)(Tq / B);
+    a->len_k = (int)(Tk / B);
     a->itype = itype;
     a->causal = causal != 0;
     a->scale = scale;

@@ -123,6 +123,75 @@ __device__ __forceinline__ char* row_of(const Heads& x, int64_t t, int h)
     return x.p + 2 * (t * x.ld + (int64_t)h * x.hs);
 }
 
+// ------------------------------------------------------------ work
+//
+// Blocks stay, one per SM, and take items (a tile of a sequence and its heads) in turn, the
+// longest first.  The loading warp finds an item's sequence and passes it on
+// through a small ring, so that the search, the loads and the first scores of the next
+// item run behind the softmax and the stores of this one.
+
+struct Item {
+    int64_t q0, k0;
+    int nq, nk, row0, head;
+    int tiles[2];      // of the other axis, for each tile of the block; [0] < 0: no more items
+};
+
+constexpr int kRing = 4;
+
+struct Ring {
+    uint64_t full[kRing], empty[kRing];
+    Item item[kRing];
+};
+
+__device__ __forceinline__ void ring_init(Ring& r, uint32_t readers)
+{
+    for (int i = 0; i < kRing; ++i) {
+        mbar_init(&r.full[i], 1);
+        mbar_init(&r.empty[i], readers);
+    }
+}
+
+// A position in a ring of N places that are filled and emptied in turn: its place, and
+// the parity of the place's phase.
+template <int N>
+struct Turn {
+    int at = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++at == N) {
+            at = 0;
+            parity ^= 1;
+        }
+    }
+};
+
+// Puts an item (all lanes have it); false if the wait ran out.
+__device__ __forceinline__ bool ring_put(Ring& r, Turn<kRing>& turn, const Item& item,
+                                         volatile int* lost)
+{
+    // a place is free at first: the parity of the phase before the first is 1
+    if (!tc_wait_warp(&r.empty[turn.at], turn.parity ^ 1, lost)) return false;
+    if ((threadIdx.x & 31) == 0) {
+        r.item[turn.at] = item;
+        mbar_arrive(&r.full[turn.at]);
+    }
+    __syncwarp();
+    turn.next();
+    return true;
+}
+
+// Takes the next item, by a warp; false at the end.
+__device__ __forceinline__ bool ring_take(Ring& r, Turn<kRing>& turn, Item& item, volatile int* lost)
+{
+    if (!tc_wait_warp(&r.full[turn.at], turn.parity, lost)) return false;
+    item = r.item[turn.at];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&r.empty[turn.at]);
+    turn.next();
+    return item.tiles[0] >= 0;
+}
+
 // ------------------------------------------------------------ forward
 //
 // A block has two tiles of 128 rows, which share the keys and values it loads:
@@ -131,262 +200,359 @@ __device__ __forceinline__ char* row_of(const Heads& x, int64_t t, int h)
 // (row = token * heads + head), where these divide 128 well enough, so that grouped
 // heads share keys and few queries fill a tile.
 //
-// Tensor memory, in columns of 32 bits: scores of the tiles at 0 and 128, each
-// overwritten by its probabilities; outputs at 256 and 384.
+// The softmax keeps no running maximum.  The first tile's maximum is the row's
+// shift; a later tile is summed against it as it comes, and only if the tile's sum
+// passes 2^16 is the tile read again, its maximum taken and what the row has so far
+// scaled.  bf16 probabilities have fp32's range, so nothing is lost below that, and
+// the exponentials need not wait for a pass over the scores.
+//
+// Tensor memory, in columns of 32 bits: scores of the tiles at 0 and 128; outputs
+// at 256 and 256 + 64 BLOCKS; probabilities at 384 and 448, or, with 128 columns of
+// outputs, over the scores.
 
-constexpr int kFwdThreads = 320;    // 8 softmax warps, TMA, products
+constexpr int kFwdThreads = 320;    // 8 softmax warps, loads, products
 
 template <int BLOCKS>
 struct FwdShape {
     static constexpr int kTile = BLOCKS * kTcBlock;
-    static constexpr int kStages = 2;
-    static constexpr int kQ = 0, kK = 2 * kTile, kV = kK + kStages * kTile;
+    static constexpr int kQs = BLOCKS == 1 ? 2 : 1;       // pairs of query tiles
+    static constexpr int kStages = BLOCKS == 1 ? 3 : 2;   // of keys, and of values
+    static constexpr int kQ = 0, kK = kQs * 2 * kTile, kV = kK + kStages * kTile;
     static constexpr int kBars = kV + kStages * kTile;
-    static constexpr int kBytes = kBars + 256 + 1024;   // the base is rounded up to 1024
+    static constexpr int kBytes = kBars + 1024 + 1024;    // the base is rounded up to 1024
+    static constexpr bool kOver = BLOCKS == 2;            // probabilities over the scores
 };
 
 struct FwdBars {
-    uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2];
+    Ring ring;
+    uint64_t q_full[2], q_empty[2], k_full[3], k_empty[3], v_full[3], v_empty[3];
+    uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
     uint32_t tmem;
     int lost;
 };
-static_assert(sizeof(FwdBars) <= 256, "the barriers' place");
+static_assert(sizeof(FwdBars) <= 1024, "the barriers' place");
 
-// One tile of scores: probabilities to tensor memory, maximum and sum of the row.
-struct RowStats {
-    float top, shift, sum;   // running maximum, its product with the factor, sum
-};
+template <int BLOCKS>
+__device__ __forceinline__ uint32_t fwd_p(uint32_t tmem, int i)
+{
+    return FwdShape<BLOCKS>::kOver ? tmem + 128 * i : tmem + 384 + 64 * i;
+}
+
+// The largest score of each row among the 128 columns below `most`.
+__device__ __forceinline__ float tile_max(uint32_t at, int most)
+{
+    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t s[32];
+        tmem_load32(at + 32 * c, s);
+        tmem_wait(s);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            m[e & 3] = fmaxf(m[e & 3], 32 * c + e < most ? __uint_as_float(s[e]) : -INFINITY);
+    }
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// Probabilities of 32 columns, in pairs, and what they add to the sums.
+__device__ __forceinline__ void exp32(const uint32_t* s, F2 cc, F2 mm, F2 sum[2], uint32_t* p)
+{
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const F2 u = fma2((F2)s[2 * e + 1] << 32 | s[2 * e], cc, mm);
+        const float x = ex2(lo2(u)), y = ex2(hi2(u));
+        sum[e & 1] = add2(sum[e & 1], pack2(x, y));
+        p[e] = pack_bf16x2(x, y);
+    }
+}
 
 template <int BLOCKS>
 __global__ void __launch_bounds__(kFwdThreads, 1)
-k_attn_tc(const __grid_constant__ Maps maps, AttnArgs a, Packing pk)
+k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a, Packing pk,
+          int pairs, int64_t items)
 {
     using S = FwdShape<BLOCKS>;
     extern __shared__ char smem_raw[];
     char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     FwdBars& bar = *reinterpret_cast<FwdBars*>(smem + S::kBars);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    pdl_wait_prior();
-    if (warp == 9) {
-        // before the next kernel may be placed beside this block and ask for its own
-        tmem_alloc(&bar.tmem);
-    } else if (threadIdx.x == 0) {
-        mbar_init(&bar.q_full, 1);
+    if (threadIdx.x == 0) {
+        ring_init(bar.ring, 9);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.q_full[i], 1);
+            mbar_init(&bar.q_empty[i], 1);
+            mbar_init(&bar.s_full[i], 1);
+            mbar_init(&bar.p_full[i], 4);
+            mbar_init(&bar.o_done[i], 1);
+            mbar_init(&bar.o_free[i], 4);
+        }
+        for (int i = 0; i < S::kStages; ++i) {
             mbar_init(&bar.k_full[i], 1);
             mbar_init(&bar.k_empty[i], 1);
             mbar_init(&bar.v_full[i], 1);
             mbar_init(&bar.v_empty[i], 1);
-            mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.p_full[i], 4);
-            mbar_init(&bar.o_done[i], 1);
         }
         bar.lost = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        tma_prefetch(&maps.q);
+        tma_prefetch(&maps.k);
+        tma_prefetch(&maps.v);
     }
+    pdl_wait_prior();
+    // before the next kernel may be placed beside this block and ask for its own
+    if (warp == 9) tmem_alloc(&bar.tmem);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     pdl_launch_dependents();
     volatile int* lost = &bar.lost;
     const uint32_t tmem = bar.tmem;
-
-    // the tiles at the end of a sequence see the most keys and go first
-    const Tile t = find_tile(a, gridDim.x - 1 - blockIdx.x, 2 * pk.tokens, false);
-    const int h0 = (int)blockIdx.y * pk.heads, hk = h0 / (a.Hq / a.Hk);
+    const int groups = a.Hq / pk.heads;           // of heads that share a tile
     const int ksteps = (a.D + 15) / 16, width = ksteps * 16;
-    // keys that each tile sees, in tiles of 128
-    int end[2], tiles[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int row0 = t.row0 + i * pk.tokens;
-        end[i] = !t.any || row0 >= t.nq ? 0
-                 : !a.causal            ? t.nk
-                                        : max(0, min(t.nk, min(row0 + pk.tokens, t.nq) + t.nk - t.nq));
-        tiles[i] = (end[i] + kTcRows - 1) / kTcRows;
-    }
-    const int n = max(tiles[0], tiles[1]);
+    Turn<kRing> turn;
 
     if (warp == 8) {
-        // ---- loads
-        if (lane == 0 && n > 0) {
-            const uint32_t q_bytes = (uint32_t)(pk.heads * pk.tokens) * 128 * BLOCKS;
-            mbar_expect_tx(&bar.q_full, q_bytes * ((tiles[0] > 0) + (tiles[1] > 0)));
-            for (int i = 0; i < 2; ++i)
-                for (int b = 0; b < BLOCKS && tiles[i] > 0; ++b)
-                    tma_load(smem + S::kQ + i * S::kTile + b * kTcBlock, &maps.q, &bar.q_full,
-                             b * kTcCols, h0, (int)(t.q0 + t.row0) + i * pk.tokens);
-            bool going = true;
-            int j = 0;
-            for (; j < n && going; ++j) {
-                const int st = j & 1, round = j >> 1;
-                if (round > 0) going = tc_wait(&bar.k_empty[st], (round - 1) & 1, lost);
-                if (!going) break;
-                mbar_expect_tx(&bar.k_full[st], S::kTile);
-                for (int b = 0; b < BLOCKS; ++b)
-                    tma_load(smem + S::kK + st * S::kTile + b * kTcBlock, &maps.k, &bar.k_full[st],
-                             b * kTcCols, hk, (int)t.k0 + j * kTcRows);
-                if (round > 0) going = tc_wait(&bar.v_empty[st], (round - 1) & 1, lost);
-                if (!going) break;
-                mbar_expect_tx(&bar.v_full[st], S::kTile);
-                for (int b = 0; b < BLOCKS; ++b)
-                    tma_load(smem + S::kV + st * S::kTile + b * kTcBlock, &maps.v, &bar.v_full[st],
-                             b * kTcCols, hk, (int)t.k0 + j * kTcRows);
+        // ---- items and loads
+        const uint32_t q_bytes = (uint32_t)(pk.heads * pk.tokens) * 128 * BLOCKS;
+        Turn<S::kQs> qt;
+        Turn<S::kStages> kt;
+        bool going = true;
+        Item m{};
+        for (int64_t w = blockIdx.x; w < items && going; w += gridDim.x) {
+            // the tiles at the end of a sequence see the most keys and go first
+            const int tile = (int)(w / groups);
+            const Tile t = find_tile(a, pairs - 1 - tile, 2 * pk.tokens, false);
+            if (!t.any) continue;
+            m = {t.q0, t.k0, t.nq, t.nk, t.row0, (int)(w - (int64_t)tile * groups) * pk.heads, {0, 0}};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int row0 = t.row0 + i * pk.tokens;
+                const int end = row0 >= t.nq ? 0
+                                : !a.causal  ? t.nk
+                                             : max(0, min(t.nk, min(row0 + pk.tokens, t.nq) + t.nk - t.nq));
+                m.tiles[i] = (end + kTcRows - 1) / kTcRows;
             }
+            going = ring_put(bar.ring, turn, m, lost);
+            const int n = max(m.tiles[0], m.tiles[1]);
+            if (!going || n == 0) continue;
+            if (lane == 0) {
+                going = tc_wait(&bar.q_empty[qt.at], qt.parity ^ 1, lost);
+                const int hk = m.head / (a.Hq / a.Hk);
+                if (going) {
+                    mbar_expect_tx(&bar.q_full[qt.at], q_bytes * ((m.tiles[0] > 0) + (m.tiles[1] > 0)));
+                    for (int i = 0; i < 2; ++i)
+                        for (int b = 0; b < BLOCKS && m.tiles[i] > 0; ++b)
+                            tma_load(smem + S::kQ + (2 * qt.at + i) * S::kTile + b * kTcBlock, &maps.q,
+                                     &bar.q_full[qt.at], b * kTcCols, m.head,
+                                     (int)m.q0 + m.row0 + i * pk.tokens);
+                }
+                for (int j = 0; j < n && going; ++j) {
+                    going = tc_wait(&bar.k_empty[kt.at], kt.parity ^ 1, lost);
+                    if (!going) break;
+                    mbar_expect_tx(&bar.k_full[kt.at], S::kTile);
+                    for (int b = 0; b < BLOCKS; ++b)
+                        tma_load(smem + S::kK + kt.at * S::kTile + b * kTcBlock, &maps.k,
+                                 &bar.k_full[kt.at], b * kTcCols, hk, (int)m.k0 + j * kTcRows);
+                    going = tc_wait(&bar.v_empty[kt.at], kt.parity ^ 1, lost);
+                    if (!going) break;
+                    mbar_expect_tx(&bar.v_full[kt.at], S::kTile);
+                    for (int b = 0; b < BLOCKS; ++b)
+                        tma_load(smem + S::kV + kt.at * S::kTile + b * kTcBlock, &maps.v,
+                                 &bar.v_full[kt.at], b * kTcCols, hk, (int)m.k0 + j * kTcRows);
+                    kt.next();
+                }
+            }
+            qt.next();
+            going = __shfl_sync(0xffffffffu, (int)going, 0) != 0;
         }
+        m.tiles[0] = -1;
+        if (going) ring_put(bar.ring, turn, m, lost);
     } else if (warp == 9) {
         // ---- products
         const uint32_t s_desc = tc_idesc(kTcRows, false), o_desc = tc_idesc(width, true);
-        bool going = n > 0 && tc_wait_warp(&bar.q_full, 0, lost);
-        going = going && tc_wait_warp(&bar.k_full[0], 0, lost);
-        if (going) {
+        Turn<S::kQs> qt;
+        Turn<S::kStages> kt, vt;
+        uint32_t p_par[2] = {0, 0}, o_par[2] = {0, 0}, f_par[2] = {1, 1};
+        bool used[2] = {false, false}, going = true;
+        Item m;
+        // scores of tile i with the keys at kt, once its probabilities' place is free
+        const auto scores = [&](int i) {
+            if (S::kOver && used[i]) going = tc_wait_warp(&bar.o_done[i], o_par[i] ^ 1, lost);
+            if (!going) return;
             if (lane == 0) {
-                for (int i = 0; i < 2; ++i)
-                    if (tiles[i] > 0) {
-                        tc_dot(tmem + i * 128, smem + S::kQ + i * S::kTile, smem + S::kK, ksteps,
-                               s_desc);
-                        tc_commit(&bar.s_full[i]);
-                    }
-                tc_commit(&bar.k_empty[0]);
+                tc_dot(tmem + i * 128, smem + S::kQ + (2 * qt.at + i) * S::kTile,
+                       smem + S::kK + kt.at * S::kTile, ksteps, s_desc);
+                tc_commit(&bar.s_full[i]);
             }
             __syncwarp();
-        }
-        for (int j = 0; j < n && going; ++j) {
-            const int st = j & 1, par = (j >> 1) & 1, nst = st ^ 1, npar = ((j + 1) >> 1) & 1;
-            going = tc_wait_warp(&bar.v_full[st], par, lost);
+        };
+        while (going && ring_take(bar.ring, turn, m, lost)) {
+            const int n = max(m.tiles[0], m.tiles[1]);
+            if (n == 0) continue;
+            going = tc_wait_warp(&bar.q_full[qt.at], qt.parity, lost) &&
+                    tc_wait_warp(&bar.k_full[kt.at], kt.parity, lost);
             if (!going) break;
-            const char* v = smem + S::kV + st * S::kTile;
-            const int rows = t.nk - j * kTcRows;
-            if (rows < kTcRows) {
-                clear_rows(smem + S::kV + st * S::kTile, rows, BLOCKS);
-                fence_async_proxy();
-                __syncwarp();
-            }
-            if (j + 1 < n) going = tc_wait_warp(&bar.k_full[nst], npar, lost);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (!going || j >= tiles[i]) continue;
-                going = tc_wait_warp(&bar.p_full[i], j & 1, lost);
-                if (!going) continue;
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t p = tmem + i * 128;
-                    tc_rows(tmem + 256 + i * 128, [&](int k) { return p + 8 * k; }, v, o_desc, j > 0);
-                    tc_commit(&bar.o_done[i]);
-                }
-                __syncwarp();
-                if (j + 1 < tiles[i]) {
-                    // the next scores take the probabilities' place
-                    going = tc_wait_warp(&bar.o_done[i], j & 1, lost);
-                    if (!going) continue;
-                    if (lane == 0) {
-                        tc_dot(tmem + i * 128, smem + S::kQ + i * S::kTile,
-                               smem + S::kK + nst * S::kTile, ksteps, s_desc);
-                        tc_commit(&bar.s_full[i]);
-                    }
+            for (int i = 0; i < 2; ++i)
+                if (going && m.tiles[i] > 0) scores(i);
+            if (lane == 0 && going) {
+                tc_commit(&bar.k_empty[kt.at]);
+                if (n == 1) tc_commit(&bar.q_empty[qt.at]);
+            }
+            kt.next();
+            for (int j = 0; j < n && going; ++j) {
+                const bool more = j + 1 < n;
+                if (more) going = tc_wait_warp(&bar.k_full[kt.at], kt.parity, lost);
+                going = going && tc_wait_warp(&bar.v_full[vt.at], vt.parity, lost);
+                if (!going) break;
+                char* v = smem + S::kV + vt.at * S::kTile;
+                const int rows = m.nk - j * kTcRows;
+                if (rows < kTcRows) {
+                    clear_rows(v, rows, BLOCKS);
+                    fence_async_proxy();
                     __syncwarp();
                 }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (!going || j >= m.tiles[i]) continue;
+                    going = tc_wait_warp(&bar.p_full[i], p_par[i], lost);
+                    p_par[i] ^= 1;
+                    // the outputs of the item before have been read
+                    if (going && j == 0) {
+                        going = tc_wait_warp(&bar.o_free[i], f_par[i], lost);
+                        f_par[i] ^= 1;
+                    }
+                    if (!going) continue;
+                    tc_fence_after();
+                    if (!S::kOver && j + 1 < m.tiles[i]) scores(i);
+                    if (lane == 0) {
+                        const uint32_t p = fwd_p<BLOCKS>(tmem, i);
+                        tc_rows(tmem + 256 + i * 64 * BLOCKS, [&](int k) { return p + 8 * k; }, v,
+                                o_desc, j > 0);
+                        tc_commit(&bar.o_done[i]);
+                    }
+                    __syncwarp();
+                    o_par[i] ^= 1;
+                    used[i] = true;
+                    if (S::kOver && j + 1 < m.tiles[i]) scores(i);
+                }
+                if (lane == 0 && going) {
+                    tc_commit(&bar.v_empty[vt.at]);
+                    if (more) tc_commit(&bar.k_empty[kt.at]);
+                    if (j + 2 == n) tc_commit(&bar.q_empty[qt.at]);
+                }
+                if (more) kt.next();
+                vt.next();
             }
-            if (lane == 0 && going) {
-                tc_commit(&bar.v_empty[st]);
-                if (j + 1 < n) tc_commit(&bar.k_empty[nst]);
-            }
+            qt.next();
         }
     } else {
         // ---- softmax: warps 0-3 have tile 0, warps 4-7 tile 1
         const int i = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t s_at = tmem + i * 128 + lanes, o_at = tmem + 256 + i * 128 + lanes;
-        const int row = t.row0 + i * pk.tokens + r / pk.heads, head = h0 + r % pk.heads;
-        const bool live = t.any && r < pk.heads * pk.tokens && row < t.nq;
-        // rows that are not stored need no mask
-        const int seen = live && a.causal ? min(t.nk, row + t.nk - t.nq + 1) : t.nk;
-        const int my_tiles = i ? tiles[1] : tiles[0];
+        const uint32_t s_at = tmem + i * 128 + lanes, o_at = tmem + 256 + i * 64 * BLOCKS + lanes;
+        const uint32_t p_at = fwd_p<BLOCKS>(tmem, i) + lanes;
+        const int my_token = i * pk.tokens + r / pk.heads, my_head = r % pk.heads;
+        const bool stored = r < pk.heads * pk.tokens;
         const float c2 = a.scale * kLog2e;
-        float top = -INFINITY, shift = 0.0f;
-        F2 sum[2] = {0, 0};
+        const F2 cc = pack2(c2, c2);
+        uint32_t s_par = 0, o_par = 0;
         bool going = true;
-        for (int j = 0; j < my_tiles; ++j) {
-            going = tc_wait_warp(&bar.s_full[i], j & 1, lost);
-            if (!going) break;
-            tc_fence_after();
-            uint32_t s[128];
+        Item m;
+        while (going && ring_take(bar.ring, turn, m, lost)) {
+            const int tiles = i ? m.tiles[1] : m.tiles[0];
+            const int row = m.row0 + my_token, head = m.head + my_head;
+            const bool live = stored && row < m.nq;
+            // rows that are not stored need no mask
+            const int seen = live && a.causal ? min(m.nk, row + m.nk - m.nq + 1) : m.nk;
+            float top = -INFINITY, shift = 0.0f;
+            F2 sum = 0;
+            for (int j = 0; j < tiles && going; ++j) {
+                going = tc_wait_warp(&bar.s_full[i], s_par, lost);
+                s_par ^= 1;
+                if (!going) break;
+                tc_fence_after();
+                const int most = seen - j * kTcRows;     // columns below it are visible
+                const bool edge = __any_sync(0xffffffffu, most < kTcRows);
+                bool look = __any_sync(0xffffffffu, top == -INFINITY);
+                uint32_t p[64];
+                F2 part[2];
+                while (true) {
+                    if (look) {
+                        const float next = fmaxf(top, tile_max(s_at, most));
+                        const float want = next == -INFINITY ? 0.0f : next * c2;
+                        if (j > 0) {
+                            const float fade = top == -INFINITY ? 0.0f : ex2(shift - want);
+                            going = tc_wait_warp(&bar.o_done[i], o_par ^ 1, lost);
+                            if (!going) break;
+                            tc_fence_after();
+                            for (int c = 0; c < width; c += 32) {
+                                uint32_t o[32];
+                                tmem_load32(o_at + c, o);
+                                tmem_wait(o);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_load32(s_at + 32 * c, s + 32 * c);
-            tmem_wait(s);
-            const int most = seen - j * kTcRows;     // columns below it are visible
-            if (__any_sync(0xffffffffu, most < kTcRows)) {
+                                for (int e = 0; e < 32; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * fade);
+                                tmem_store32(o_at + c, o);
+                            }
+                            sum = mul2(sum, pack2(fade, fade));
+                        }
+                        top = next;
+                        shift = want;
+                    }
+                    const F2 mm = pack2(-shift, -shift);
+                    part[0] = part[1] = 0;
+                    uint32_t s[2][32];
+                    tmem_load32(s_at, s[0]);
 #pragma unroll
-                for (int c = 0; c < 128; ++c)
-                    if (c >= most) s[c] = 0xff800000u;
-            }
-            float m[4] = {top, top, top, top};
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_wait(s[c & 1]);
+                        if (c < 3) tmem_load32(s_at + 32 * (c + 1), s[(c + 1) & 1]);
+                        if (edge) {
 #pragma unroll
-            for (int c = 0; c < 128; c += 8)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    m[e] = fmaxf(m[e], fmaxf(__uint_as_float(s[c + e]), __uint_as_float(s[c + 4 + e])));
-            const float next = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-            // the shift follows the maximum only once it lags by a factor of 2^8,
-            // which bf16 probabilities and fp32 sums do not notice
-            const float want = next == -INFINITY ? 0.0f : next * c2;
-            const bool move = top == -INFINITY ? next > -INFINITY : want - shift > 8.0f;
-            if (__any_sync(0xffffffffu, move)) {
-                const float fade = top == -INFINITY ? 0.0f : ex2(shift - want);
-                if (j > 0) {
-                    going = tc_wait_warp(&bar.o_done[i], (j - 1) & 1, lost);
+                            for (int e = 0; e < 32; ++e)
+                                if (32 * c + e >= most) s[c & 1][e] = 0xff800000u;
+                        }
+                        exp32(s[c & 1], cc, mm, part, p + 16 * c);
+                    }
+                    part[0] = add2(part[0], part[1]);
+                    const float total = lo2(part[0]) + hi2(part[0]);
+                    if (look || !__any_sync(0xffffffffu, !(total <= 0x1p16f))) break;
+                    look = true;
+                }
+                if (!going) break;
+                sum = add2(sum, part[0]);
+                if (!S::kOver && j > 0) {     // the product before has read the last ones
+                    going = tc_wait_warp(&bar.o_done[i], o_par ^ 1, lost);
                     if (!going) break;
                     tc_fence_after();
-                    for (int c = 0; c < width; c += 32) {
-                        uint32_t o[32];
-                        tmem_load32(o_at + c, o);
-                        tmem_wait(o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            o[e] = __float_as_uint(__uint_as_float(o[e]) * fade);
-                        tmem_store32(o_at + c, o);
-                    }
-                    sum[0] = mul2(sum[0], pack2(fade, fade));
-                    sum[1] = mul2(sum[1], pack2(fade, fade));
                 }
-                top = next;
-                shift = want;
+                o_par ^= 1;
+                tmem_store32(p_at, p);
+                tmem_store32(p_at + 32, p + 32);
+                tmem_wait_stores();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.p_full[i]);
             }
-            const F2 cc = pack2(c2, c2), mm = pack2(-shift, -shift);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t p[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const int c = 64 * h + 2 * e;
-                    const F2 u = fma2((F2)s[c + 1] << 32 | s[c], cc, mm);
-                    const float x = ex2(lo2(u)), y = ex2(hi2(u));
-                    sum[e & 1] = add2(sum[e & 1], pack2(x, y));
-                    p[e] = pack_bf16x2(x, y);
-                }
-                tmem_store32(s_at + 32 * h, p);
+            if (going && tiles > 0) going = tc_wait_warp(&bar.o_done[i], o_par ^ 1, lost);
+            const float total = lo2(sum) + hi2(sum);
+            char* out = live ? row_of(a.out, m.q0 + row, head) : nullptr;
+            if (going && tiles > 0) {
+                tc_fence_after();
+                store_row(o_at, a.D, total == 0.0f ? 0.0f : 1.0f / total, out, live);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.o_free[i]);
+            } else if (going) {
+                zero_row(a.D, out, live);
             }
-            tmem_wait_stores();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.p_full[i]);
+            if (a.lse != nullptr && live)
+                a.lse[(int64_t)head * a.Tq + m.q0 + row] =
+                    !going ? __int_as_float(0x7fc00000)
+                    : total == 0.0f ? -INFINITY : (shift + log2f(total)) * kLn2;
         }
-        if (going && my_tiles > 0) going = tc_wait_warp(&bar.o_done[i], (my_tiles - 1) & 1, lost);
-        const F2 both = add2(sum[0], sum[1]);
-        const float total = lo2(both) + hi2(both);
-        char* out = live ? row_of(a.out, t.q0 + row, head) : nullptr;
-        if (going && my_tiles > 0) {
-            tc_fence_after();
-            store_row(o_at, a.D, total == 0.0f ? 0.0f : 1.0f / total, out, live);
-        } else if (going) {
-            zero_row(a.D, out, live);
-        }
-        if (a.lse != nullptr && live)
-            a.lse[(int64_t)head * a.Tq + t.q0 + row] =
-                !going ? __int_as_float(0x7fc00000)
-                : total == 0.0f ? -INFINITY : (shift + log2f(total)) * kLn2;
     }
-
     tc_finish(lost, tmem, warp == 9);
 }
 
@@ -455,7 +621,7 @@ k_attn_tc_dq(const __grid_constant__ Maps maps, AttnArgs a)
     volatile int* lost = &bar.lost;
     const uint32_t tmem = bar.tmem;
 
-    const Tile t = find_tile(a, gridDim.x - 1 - blockIdx.x, kTcRows, false);
+    const Tile t = find_tile(a, (int)(gridDim.x - 1 - blockIdx.x), kTcRows, false);
     const int h = blockIdx.y, hk = h / (a.Hq / a.Hk);
     const int ksteps = (a.D + 15) / 16, width = ksteps * 16;
     const int end = !t.any ? 0
@@ -642,7 +808,7 @@ k_attn_tc_dkv(const __grid_constant__ Maps maps, AttnArgs a)
     const uint32_t tmem = bar.tmem;
 
     // the first keys of a sequence are seen by the most queries: tiles in order
-    const Tile t = find_tile(a, blockIdx.x, kTcRows, true);
+    const Tile t = find_tile(a, (int)blockIdx.x, kTcRows, true);
     const int hk = blockIdx.y, G = a.Hq / a.Hk;
     const int ksteps = (a.D + 15) / 16, width = ksteps * 16;
     // the tiles of queries from the first that sees this tile's first key
@@ -942,11 +1108,15 @@ cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t s)
         !make_map(&m.v, a.v, a.Tk, a.Hk, a.D, 1, kTcRows))
         return launch_attn_any(a, s);
     m.dout = m.q;
+    int sms = 0;
+    const cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
     return by_blocks(a.D, [&](auto n) {
         static SmemRaisedOn raised;
-        return launch_tc(k_attn_tc<n>, raised, FwdShape<n>::kBytes,
-                         tiles_bound(a.cu_q, a.Tq, a.B, 2 * pk.tokens), a.Hq / pk.heads,
-                         kFwdThreads, s, m, a, pk);
+        const int64_t pairs = tiles_bound(a.cu_q, a.Tq, a.B, 2 * pk.tokens);
+        const int64_t items = pairs * (a.Hq / pk.heads);
+        return launch_tc(k_attn_tc<n>, raised, FwdShape<n>::kBytes, items < sms ? items : sms, 1,
+                         kFwdThreads, s, m, a, pk, (int)pairs, items);
     });
 }
 
