@@ -185,7 +185,9 @@ __device__ __forceinline__ bool ring_put(Ring& r, Turn<kRing>& turn, const Item&
 __device__ __forceinline__ bool ring_take(Ring& r, Turn<kRing>& turn, Item& item, volatile int* lost)
 {
     if (!tc_wait_warp(&r.full[turn.at], turn.parity, lost)) return false;
-    item = r.item[turn.at];
+    const Item& x = r.item[turn.at];
+    item = {x.q0, x.k0, uniform(x.nq), uniform(x.nk), uniform(x.row0), uniform(x.head),
+            {uniform(x.tiles[0]), uniform(x.tiles[1])}};
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&r.empty[turn.at]);
     turn.next();
@@ -275,7 +277,7 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
     extern __shared__ char smem_raw[];
     char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     FwdBars& bar = *reinterpret_cast<FwdBars*>(smem + S::kBars);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         ring_init(bar.ring, 9);
         for (int i = 0; i < 2; ++i) {
@@ -306,7 +308,7 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
     tc_fence_after();
     pdl_launch_dependents();
     volatile int* lost = &bar.lost;
-    const uint32_t tmem = bar.tmem;
+    const uint32_t tmem = (uint32_t)uniform((int)bar.tmem);
     const int groups = a.Hq / pk.heads;           // of heads that share a tile
     const int ksteps = (a.D + 15) / 16, width = ksteps * 16;
     Turn<kRing> turn;
@@ -379,8 +381,8 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
         const auto scores = [&](int i) {
             if (S::kOver && used[i]) going = tc_wait_warp(&bar.o_done[i], o_par[i] ^ 1, lost);
             if (!going) return;
-            if (lane == 0) {
-                tc_dot(tmem + i * 128, smem + S::kQ + (2 * qt.at + i) * S::kTile,
+            if (elect_one()) {
+                tc_dot<BLOCKS>(tmem + i * 128, smem + S::kQ + (2 * qt.at + i) * S::kTile,
                        smem + S::kK + kt.at * S::kTile, ksteps, s_desc);
                 tc_commit(&bar.s_full[i]);
             }
@@ -395,7 +397,7 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 if (going && m.tiles[i] > 0) scores(i);
-            if (lane == 0 && going) {
+            if (going && elect_one()) {
                 tc_commit(&bar.k_empty[kt.at]);
                 if (n == 1) tc_commit(&bar.q_empty[qt.at]);
             }
@@ -425,10 +427,9 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
                     if (!going) continue;
                     tc_fence_after();
                     if (!S::kOver && j + 1 < m.tiles[i]) scores(i);
-                    if (lane == 0) {
-                        const uint32_t p = fwd_p<BLOCKS>(tmem, i);
-                        tc_rows(tmem + 256 + i * 64 * BLOCKS, [&](int k) { return p + 8 * k; }, v,
-                                o_desc, j > 0);
+                    if (elect_one()) {
+                        tc_rows(tmem + 256 + i * 64 * BLOCKS, fwd_p<BLOCKS>(tmem, i), 0, v, o_desc,
+                                j > 0);
                         tc_commit(&bar.o_done[i]);
                     }
                     __syncwarp();
@@ -436,7 +437,7 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
                     used[i] = true;
                     if (S::kOver && j + 1 < m.tiles[i]) scores(i);
                 }
-                if (lane == 0 && going) {
+                if (going && elect_one()) {
                     tc_commit(&bar.v_empty[vt.at]);
                     if (more) tc_commit(&bar.k_empty[kt.at]);
                     if (j + 2 == n) tc_commit(&bar.q_empty[qt.at]);
@@ -610,7 +611,7 @@ k_attn_tc_dq(const __grid_constant__ Maps maps, AttnArgs a)
     char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     GradBars& bar = *reinterpret_cast<GradBars*>(smem + S::kBars);
     float* delta_s = reinterpret_cast<float*>(smem + S::kRows);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     pdl_wait_prior();
     if (warp == 9) tmem_alloc(&bar.tmem);
     else if (threadIdx.x == 0) grad_init(bar);
@@ -619,7 +620,7 @@ k_attn_tc_dq(const __grid_constant__ Maps maps, AttnArgs a)
     tc_fence_after();
     pdl_launch_dependents();
     volatile int* lost = &bar.lost;
-    const uint32_t tmem = bar.tmem;
+    const uint32_t tmem = (uint32_t)uniform((int)bar.tmem);
 
     const Tile t = find_tile(a, (int)(gridDim.x - 1 - blockIdx.x), kTcRows, false);
     const int h = blockIdx.y, hk = h / (a.Hq / a.Hk);
@@ -659,9 +660,9 @@ k_attn_tc_dq(const __grid_constant__ Maps maps, AttnArgs a)
             going = tc_wait_warp(&bar.d_full, j & 1, lost);
             if (!going) return;
             tc_fence_after();
-            if (lane == 0) {
-                tc_rows(tmem + 256, [&](int k) { return tmem + 384 + 8 * k; },
-                        smem + S::kIn + (j & 1) * 2 * S::kTile, o_desc, j > 0);
+            if (elect_one()) {
+                tc_rows(tmem + 256, tmem + 384, 0, smem + S::kIn + (j & 1) * 2 * S::kTile, o_desc,
+                        j > 0);
                 tc_commit(&bar.d_free);
                 tc_commit(&bar.in_empty[j & 1]);
             }
@@ -681,9 +682,9 @@ k_attn_tc_dq(const __grid_constant__ Maps maps, AttnArgs a)
             if (j > 0) going = tc_wait_warp(&bar.s_free, (j - 1) & 1, lost);
             if (!going) break;
             tc_fence_after();
-            if (lane == 0) {
-                tc_dot(tmem, smem + S::kA, in, ksteps, s_desc);
-                tc_dot(tmem + 128, smem + S::kB, in + S::kTile, ksteps, s_desc);
+            if (elect_one()) {
+                tc_dot<BLOCKS>(tmem, smem + S::kA, in, ksteps, s_desc);
+                tc_dot<BLOCKS>(tmem + 128, smem + S::kB, in + S::kTile, ksteps, s_desc);
                 tc_commit(&bar.s_full);
             }
             __syncwarp();
@@ -796,7 +797,7 @@ k_attn_tc_dkv(const __grid_constant__ Maps maps, AttnArgs a)
     char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     GradBars& bar = *reinterpret_cast<GradBars*>(smem + S::kBars);
     float* rows_s = reinterpret_cast<float*>(smem + S::kRows);   // [stage][-lse log2e, -delta][128]
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     pdl_wait_prior();
     if (warp == 9) tmem_alloc(&bar.tmem);
     else if (threadIdx.x == 0) grad_init(bar);
@@ -805,7 +806,7 @@ k_attn_tc_dkv(const __grid_constant__ Maps maps, AttnArgs a)
     tc_fence_after();
     pdl_launch_dependents();
     volatile int* lost = &bar.lost;
-    const uint32_t tmem = bar.tmem;
+    const uint32_t tmem = (uint32_t)uniform((int)bar.tmem);
 
     // the first keys of a sequence are seen by the most queries: tiles in order
     const Tile t = find_tile(a, (int)blockIdx.x, kTcRows, true);
@@ -865,9 +866,6 @@ k_attn_tc_dkv(const __grid_constant__ Maps maps, AttnArgs a)
         }
     } else if (warp == 9) {
         const uint32_t s_desc = tc_idesc(kTcRows, false), o_desc = tc_idesc(width, true);
-        const auto operand = [&](uint32_t at) {
-            return [=](int k) { return at + 8 * (k & 3) + 64 * (k >> 2); };
-        };
         bool going = n > 0 && tc_wait_warp(&bar.once_full, 0, lost);
         // waits for tile j, clears what lies beyond the sequence, issues its scores
         const auto scores = [&](int j) {
@@ -881,15 +879,15 @@ k_attn_tc_dkv(const __grid_constant__ Maps maps, AttnArgs a)
                 fence_async_proxy();
                 __syncwarp();
             }
-            if (lane == 0) {
-                tc_dot(tmem, smem + S::kA, in, ksteps, s_desc);
+            if (elect_one()) {
+                tc_dot<BLOCKS>(tmem, smem + S::kA, in, ksteps, s_desc);
                 tc_commit(&bar.s_full);
             }
             __syncwarp();
         };
         const auto grads = [&](int j) {
-            if (lane == 0) {
-                tc_dot(tmem + 128, smem + S::kB, smem + S::kIn + (j & 1) * 2 * S::kTile + S::kTile,
+            if (elect_one()) {
+                tc_dot<BLOCKS>(tmem + 128, smem + S::kB, smem + S::kIn + (j & 1) * 2 * S::kTile + S::kTile,
                        ksteps, s_desc);
                 tc_commit(&bar.g_full);
             }
@@ -902,8 +900,8 @@ k_attn_tc_dkv(const __grid_constant__ Maps maps, AttnArgs a)
             going = tc_wait_warp(&bar.p_full, j & 1, lost);
             if (!going) break;
             tc_fence_after();
-            if (lane == 0) {
-                tc_rows(tmem + kDv, operand(tmem), in + S::kTile, o_desc, j > 0);
+            if (elect_one()) {
+                tc_rows(tmem + kDv, tmem, 32, in + S::kTile, o_desc, j > 0);
                 tc_commit(&bar.d_free);
             }
             __syncwarp();
@@ -918,8 +916,8 @@ k_attn_tc_dkv(const __grid_constant__ Maps maps, AttnArgs a)
             going = tc_wait_warp(&bar.d_full, j & 1, lost);
             if (!going) break;
             tc_fence_after();
-            if (lane == 0) {
-                tc_rows(tmem + kDk, operand(tmem + 128), in, o_desc, j > 0);
+            if (elect_one()) {
+                tc_rows(tmem + kDk, tmem + 128, 32, in, o_desc, j > 0);
                 tc_commit(&bar.in_empty[j & 1]);
                 tc_commit(&bar.d_free);
             }
@@ -928,7 +926,7 @@ k_attn_tc_dkv(const __grid_constant__ Maps maps, AttnArgs a)
             if (going && j + 1 < n) grads(j + 1);
         }
         // the compute warps wait here for the last product
-        if (going && n > 0 && lane == 0) tc_commit(&bar.s_full);
+        if (going && n > 0 && elect_one()) tc_commit(&bar.s_full);
     } else {
         const int r = (warp & 3) * 32 + lane, half = warp >> 2;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;

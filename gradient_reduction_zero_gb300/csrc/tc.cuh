@@ -154,13 +154,33 @@ __device__ __forceinline__ void tc_fence_after()
 
 // ------------------------------------------------------------ products
 
+// What issues a product must be the same in the whole warp for the hardware's
+// uniform registers; values that come through shared memory are made so here.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// One thread of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+
 // Descriptor of an operand in blocks of 64 swizzled columns.  K-major: groups
 // of 8 rows are 1024 bytes apart.  MN-major: the same groups follow one another
-// along the sum, and blocks of 64 columns are `block` bytes apart.
-__device__ __forceinline__ uint64_t tc_desc(const void* p, uint32_t block)
+// along the sum, and blocks of 64 columns are kTcBlock bytes apart (which a K-major
+// operand ignores).  The low word holds the address in units of 16 bytes, so that
+// a step of the sum is an addition to it; the high word is the same for all.
+constexpr uint32_t kTcDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+
+__device__ __forceinline__ uint32_t tc_desc(const void* p)
 {
-    return (uint64_t)((smem_addr(p) & 0x3ffffu) >> 4) | (uint64_t)(block >> 4) << 16 |
-           (uint64_t)(1024u >> 4) << 32 | uint64_t(1) << 46 | uint64_t(2) << 61;
+    return (smem_addr(p) & 0x3ffffu) >> 4 | (uint32_t)(kTcBlock >> 4) << 16;
+}
+
+__device__ __forceinline__ uint64_t tc_whole(uint32_t low)
+{
+    return (uint64_t)kTcDescHigh << 32 | low;
 }
 
 // Instruction descriptor: bf16 x bf16 -> fp32, 128 rows, n columns; b_mn: the
@@ -172,23 +192,23 @@ __device__ __forceinline__ uint32_t tc_idesc(int n, bool b_mn)
 }
 
 // d (+)= a b, the sum over 16 elements; one thread issues it.
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add)
 {
     asm volatile(
         "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
         " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "l"(tc_whole(a)), "l"(tc_whole(b)), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
 
 // The same with the left operand in tensor memory.
-__device__ __forceinline__ void tc_mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void tc_mma_tmem(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                             bool add)
 {
     asm volatile(
         "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
         " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "r"(a), "l"(tc_whole(b)), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
 
@@ -201,24 +221,28 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar)
                  : "memory");
 }
 
-// d = a b^T over `steps` times 16 columns of two K-major operands.
+// d = a b^T over `steps` times 16 columns of two K-major operands of BLOCKS blocks.
+template <int BLOCKS>
 __device__ __forceinline__ void tc_dot(uint32_t d, const char* a, const char* b, int steps,
                                        uint32_t idesc)
 {
-    for (int k = 0; k < steps; ++k) {
-        const uint32_t at = (uint32_t)(k >> 2) * kTcBlock + (uint32_t)(k & 3) * 32;
-        tc_mma(d, tc_desc(a + at, 16), tc_desc(b + at, 16), idesc, k > 0);
+    const uint32_t x = tc_desc(a), y = tc_desc(b);
+#pragma unroll
+    for (int k = 0; k < 4 * BLOCKS; ++k) {
+        const uint32_t at = (uint32_t)((k >> 2) * kTcBlock + (k & 3) * 32) >> 4;
+        if (k < steps) tc_mma(d, x + at, y + at, idesc, k > 0);
     }
 }
 
 // d (+)= a b over the 128 rows of an MN-major operand b; a in tensor memory, its
-// k-th 16 elements at a + col(k).
-template <class F>
-__device__ __forceinline__ void tc_rows(uint32_t d, F&& col, const char* b, uint32_t idesc, bool add)
+// k-th 16 elements 8 k columns on, and `gap` more from the fifth.
+__device__ __forceinline__ void tc_rows(uint32_t d, uint32_t a, uint32_t gap, const char* b,
+                                        uint32_t idesc, bool add)
 {
+    const uint32_t y = tc_desc(b);
 #pragma unroll
     for (int k = 0; k < kTcRows / 16; ++k)
-        tc_mma_tmem(d, col(k), tc_desc(b + k * 2048, kTcBlock), idesc, add || k > 0);
+        tc_mma_tmem(d, a + 8 * k + (k >= 4 ? gap : 0), y + k * (2048 >> 4), idesc, add || k > 0);
 }
 
 // Zeros in rows [n, 128) of `blocks` blocks, by a warp.
