@@ -89,24 +89,56 @@ struct Packing {
     int heads, tokens;
 };
 
-// Columns [0, n) of the warp's rows, times k, as bf16 to rows of a tensor in memory.
-__device__ __forceinline__ void store_row(uint32_t tmem, int n, float k, char* row, bool live)
+// A 32-byte store whose line stays in L2 for the next kernel.
+__device__ __forceinline__ void st32_keep(void* p, const U8& v)
 {
-    for (int c = 0; c < n; c += 32) {
-        uint32_t r[32];
-        tmem_load32(tmem + c, r);
+    asm volatile("st.global.v8.u32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v.x[0]),
+                 "r"(v.x[1]), "r"(v.x[2]), "r"(v.x[3]), "r"(v.x[4]), "r"(v.x[5]), "r"(v.x[6]),
+                 "r"(v.x[7])
+                 : "memory");
+}
+
+// Whether every row of x begins on a boundary of 32 bytes.
+__device__ __forceinline__ bool wide_rows(const Heads& x)
+{
+    return ((reinterpret_cast<uintptr_t>(x.p) | (uintptr_t)(2 * x.ld) | (uintptr_t)(2 * x.hs)) & 31) == 0;
+}
+
+// Columns [0, n) of the warp's rows (n <= COLS, a multiple of 8) times k as bf16 to rows of
+// a tensor in memory.  The columns are in registers when read() is called, before the
+// stores.  wide: the rows are on boundaries of 32 bytes.
+template <int COLS, class F>
+__device__ __forceinline__ void store_row(uint32_t tmem, int n, float k, char* row, bool live,
+                                          bool wide, F&& read)
+{
+#pragma unroll
+    for (int c0 = 0; c0 < COLS; c0 += 64) {
+        constexpr int kPart = COLS < 64 ? COLS : 64;
+        uint32_t r[kPart];
+#pragma unroll
+        for (int c = 0; c < kPart; c += 32)
+            if (c0 + c < n) tmem_load32(tmem + c0 + c, r + c);
         tmem_wait(r);
+        if (c0 + 64 >= COLS) read();
+#pragma unroll
+        for (int c = 0; c < kPart / 2; ++c)
+            r[c] = pack_bf16x2(__uint_as_float(r[2 * c]) * k, __uint_as_float(r[2 * c + 1]) * k);
         if (!live) continue;
+        if (wide && n % 16 == 0) {
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            if (c + 8 * v >= n) break;
-            uint4 w;
-            uint32_t* u = &w.x;
+            for (int c = 0; c < kPart; c += 16)
+                if (c0 + c < n) {
+                    U8 w;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                u[i] = pack_bf16x2(__uint_as_float(r[8 * v + 2 * i]) * k,
-                                   __uint_as_float(r[8 * v + 2 * i + 1]) * k);
-            *reinterpret_cast<uint4*>(row + 2 * (c + 8 * v)) = w;
+                    for (int e = 0; e < 8; ++e) w.x[e] = r[c / 2 + e];
+                    st32_keep(row + 2 * (c0 + c), w);
+                }
+        } else {
+#pragma unroll
+            for (int c = 0; c < kPart; c += 8)
+                if (c0 + c < n)
+                    *reinterpret_cast<uint4*>(row + 2 * (c0 + c)) =
+                        make_uint4(r[c / 2], r[c / 2 + 1], r[c / 2 + 2], r[c / 2 + 3]);
         }
     }
 }
@@ -202,17 +234,21 @@ __device__ __forceinline__ bool ring_take(Ring& r, Turn<kRing>& turn, Item& item
 // (row = token * heads + head), where these divide 128 well enough, so that grouped
 // heads share keys and few queries fill a tile.
 //
-// The softmax keeps no running maximum.  The first tile's maximum is the row's
-// shift; a later tile is summed against it as it comes, and only if the tile's sum
-// passes 2^16 is the tile read again, its maximum taken and what the row has so far
-// scaled.  bf16 probabilities have fp32's range, so nothing is lost below that, and
-// the exponentials need not wait for a pass over the scores.
+// The softmax takes no maximum as long as none is needed: a row's scores are summed
+// against a shift of 0 as they come.  Only where a tile's sum passes 2^16, or the row's
+// sum stays below 2^-30, is the tile read again, its maximum made the shift and
+// what the row has so far scaled.  Between these bounds nothing is lost: fp32 sums and
+// bf16 probabilities are as exact there as near 1, and what falls below fp32's range is
+// below 2^-96 of the sum.
 //
 // Tensor memory, in columns of 32 bits: scores of the tiles at 0 and 128; outputs
 // at 256 and 256 + 64 BLOCKS; probabilities at 384 and 448, or, with 128 columns of
 // outputs, over the scores.
 
-constexpr int kFwdThreads = 320;    // 8 softmax warps, loads, products
+constexpr int kFwdThreads = 384;    // 8 softmax warps, loads, products, two idle
+// Registers of a thread, of the 168 that each is launched with: 2 x 128 x 208 + 128 x 88 =
+// 384 x 168.
+constexpr int kFwdSoftmaxRegs = 208, kFwdOtherRegs = 88;
 
 template <int BLOCKS>
 struct FwdShape {
@@ -256,6 +292,19 @@ __device__ __forceinline__ float tile_max(uint32_t at, int most)
     return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
+// Scales `width` columns of the warp's rows.
+__device__ __forceinline__ void scale_rows(uint32_t at, int width, float k)
+{
+    for (int c = 0; c < width; c += 32) {
+        uint32_t o[32];
+        tmem_load32(at + c, o);
+        tmem_wait(o);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * k);
+        tmem_store32(at + c, o);
+    }
+}
+
 // Probabilities of 32 columns, in pairs, and what they add to the sums.
 __device__ __forceinline__ void exp32(const uint32_t* s, F2 cc, F2 mm, F2 sum[2], uint32_t* p)
 {
@@ -265,6 +314,31 @@ __device__ __forceinline__ void exp32(const uint32_t* s, F2 cc, F2 mm, F2 sum[2]
         const float x = ex2(lo2(u)), y = ex2(hi2(u));
         sum[e & 1] = add2(sum[e & 1], pack2(x, y));
         p[e] = pack_bf16x2(x, y);
+    }
+}
+
+// The same of a tile's 128 columns; EDGE: of those below `most`, in the whole warp's or in
+// this row's view.
+template <bool EDGE>
+__device__ __forceinline__ void tile_exp(uint32_t at, int most, F2 cc, F2 mm, F2 sum[2], uint32_t* p)
+{
+    uint32_t s[2][32];
+    tmem_load32(at, s[0]);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        tmem_wait(s[c & 1]);
+        if (c < 3) tmem_load32(at + 32 * (c + 1), s[(c + 1) & 1]);
+        if (EDGE) {
+            if (!__any_sync(0xffffffffu, 32 * c < most)) {       // nothing to see
+#pragma unroll
+                for (int e = 0; e < 16; ++e) p[16 * c + e] = 0;
+                continue;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (32 * c + e >= most) s[c & 1][e] = 0xff800000u;
+        }
+        exp32(s[c & 1], cc, mm, sum, p + 16 * c);
     }
 }
 
@@ -315,6 +389,7 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
 
     if (warp == 8) {
         // ---- items and loads
+        set_registers_down<kFwdOtherRegs>();
         const uint32_t q_bytes = (uint32_t)(pk.heads * pk.tokens) * 128 * BLOCKS;
         Turn<S::kQs> qt;
         Turn<S::kStages> kt;
@@ -371,6 +446,7 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
         if (going) ring_put(bar.ring, turn, m, lost);
     } else if (warp == 9) {
         // ---- products
+        set_registers_down<kFwdOtherRegs>();
         const uint32_t s_desc = tc_idesc(kTcRows, false), o_desc = tc_idesc(width, true);
         Turn<S::kQs> qt;
         Turn<S::kStages> kt, vt;
@@ -447,14 +523,15 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
             }
             qt.next();
         }
-    } else {
+    } else if (warp < 8) {
         // ---- softmax: warps 0-3 have tile 0, warps 4-7 tile 1
+        set_registers_up<kFwdSoftmaxRegs>();
         const int i = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + i * 128 + lanes, o_at = tmem + 256 + i * 64 * BLOCKS + lanes;
         const uint32_t p_at = fwd_p<BLOCKS>(tmem, i) + lanes;
         const int my_token = i * pk.tokens + r / pk.heads, my_head = r % pk.heads;
-        const bool stored = r < pk.heads * pk.tokens;
+        const bool stored = r < pk.heads * pk.tokens, wide = wide_rows(a.out);
         const float c2 = a.scale * kLog2e;
         const F2 cc = pack2(c2, c2);
         uint32_t s_par = 0, o_par = 0;
@@ -466,7 +543,7 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
             const bool live = stored && row < m.nq;
             // rows that are not stored need no mask
             const int seen = live && a.causal ? min(m.nk, row + m.nk - m.nq + 1) : m.nk;
-            float top = -INFINITY, shift = 0.0f;
+            float shift = 0.0f;
             F2 sum = 0;
             for (int j = 0; j < tiles && going; ++j) {
                 going = tc_wait_warp(&bar.s_full[i], s_par, lost);
@@ -475,51 +552,32 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
                 tc_fence_after();
                 const int most = seen - j * kTcRows;     // columns below it are visible
                 const bool edge = __any_sync(0xffffffffu, most < kTcRows);
-                bool look = __any_sync(0xffffffffu, top == -INFINITY);
                 uint32_t p[64];
                 F2 part[2];
+                bool looked = false;
                 while (true) {
-                    if (look) {
-                        const float next = fmaxf(top, tile_max(s_at, most));
-                        const float want = next == -INFINITY ? 0.0f : next * c2;
-                        if (j > 0) {
-                            const float fade = top == -INFINITY ? 0.0f : ex2(shift - want);
-                            going = tc_wait_warp(&bar.o_done[i], o_par ^ 1, lost);
-                            if (!going) break;
-                            tc_fence_after();
-                            for (int c = 0; c < width; c += 32) {
-                                uint32_t o[32];
-                                tmem_load32(o_at + c, o);
-                                tmem_wait(o);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * fade);
-                                tmem_store32(o_at + c, o);
-                            }
-                            sum = mul2(sum, pack2(fade, fade));
-                        }
-                        top = next;
-                        shift = want;
-                    }
                     const F2 mm = pack2(-shift, -shift);
                     part[0] = part[1] = 0;
-                    uint32_t s[2][32];
-                    tmem_load32(s_at, s[0]);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        tmem_wait(s[c & 1]);
-                        if (c < 3) tmem_load32(s_at + 32 * (c + 1), s[(c + 1) & 1]);
-                        if (edge) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (32 * c + e >= most) s[c & 1][e] = 0xff800000u;
-                        }
-                        exp32(s[c & 1], cc, mm, part, p + 16 * c);
-                    }
+                    if (edge) tile_exp<true>(s_at, most, cc, mm, part, p);
+                    else tile_exp<false>(s_at, most, cc, mm, part, p);
                     part[0] = add2(part[0], part[1]);
-                    const float total = lo2(part[0]) + hi2(part[0]);
-                    if (look || !__any_sync(0xffffffffu, !(total <= 0x1p16f))) break;
-                    look = true;
+                    const float total = lo2(part[0]) + hi2(part[0]), before = lo2(sum) + hi2(sum);
+                    const bool fits = !live || (total <= 0x1p16f && total + before >= 0x1p-30f);
+                    if (looked || __all_sync(0xffffffffu, fits)) break;
+                    looked = true;
+                    const float next = tile_max(s_at, most) * c2;
+                    // a row's shift depends on that row alone, not on its neighbours
+                    const float want = fits || next == -INFINITY ? shift
+                                       : before > 0.0f ? fmaxf(shift, next) : next;
+                    if (j > 0) {
+                        const float fade = fits ? 1.0f : before > 0.0f ? ex2(shift - want) : 0.0f;
+                        going = tc_wait_warp(&bar.o_done[i], o_par ^ 1, lost);
+                        if (!going) break;
+                        tc_fence_after();
+                        scale_rows(o_at, width, fade);
+                        sum = mul2(sum, pack2(fade, fade));
+                    }
+                    shift = want;
                 }
                 if (!going) break;
                 sum = add2(sum, part[0]);
@@ -541,10 +599,12 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
             char* out = live ? row_of(a.out, m.q0 + row, head) : nullptr;
             if (going && tiles > 0) {
                 tc_fence_after();
-                store_row(o_at, a.D, total == 0.0f ? 0.0f : 1.0f / total, out, live);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.o_free[i]);
+                store_row<64 * BLOCKS>(o_at, a.D, total == 0.0f ? 0.0f : 1.0f / total, out, live, wide,
+                                       [&] {
+                                           tc_fence_before();
+                                           __syncwarp();
+                                           if (lane == 0) mbar_arrive(&bar.o_free[i]);
+                                       });
             } else if (going) {
                 zero_row(a.D, out, live);
             }
@@ -553,6 +613,8 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
                     !going ? __int_as_float(0x7fc00000)
                     : total == 0.0f ? -INFINITY : (shift + log2f(total)) * kLn2;
         }
+    } else {
+        set_registers_down<kFwdOtherRegs>();
     }
     tc_finish(lost, tmem, warp == 9);
 }
@@ -768,7 +830,9 @@ k_attn_tc_dq(const __grid_constant__ Maps maps, AttnArgs a)
             // a thread's half of its row, in whole 32 columns
             const int first = half * BLOCKS * 32, cols = min(a.D - first, BLOCKS * 32);
             char* out = live ? row_of(a.dq, t.q0 + row, h) + 2 * first : nullptr;
-            if (n > 0) store_row(tmem + lanes + 256 + first, cols, a.scale, out, live);
+            if (n > 0)
+                store_row<BLOCKS * 32>(tmem + lanes + 256 + first, cols, a.scale, out, live,
+                                       wide_rows(a.dq), [] {});
             else zero_row(cols, out, live);
         }
     }
@@ -1007,8 +1071,10 @@ k_attn_tc_dkv(const __grid_constant__ Maps maps, AttnArgs a)
             char* dv = live ? row_of(a.dv, t.k0 + row, hk) + 2 * begin : nullptr;
             char* dk = live ? row_of(a.dk, t.k0 + row, hk) + 2 * begin : nullptr;
             if (n > 0) {
-                store_row(tmem + lanes + kDv + begin, cols, 1.0f, dv, live);
-                store_row(tmem + lanes + kDk + begin, cols, a.scale, dk, live);
+                store_row<BLOCKS * 32>(tmem + lanes + kDv + begin, cols, 1.0f, dv, live,
+                                       wide_rows(a.dv), [] {});
+                store_row<BLOCKS * 32>(tmem + lanes + kDk + begin, cols, a.scale, dk, live,
+                                       wide_rows(a.dk), [] {});
             } else {
                 zero_row(cols, dv, live);
                 zero_row(cols, dk, live);

@@ -152,6 +152,22 @@ __device__ __forceinline__ void tc_fence_after()
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
+// ------------------------------------------------------------ registers
+//
+// A warpgroup's registers per thread from here on.  What some gain others must have
+// given: the sum over the block's warpgroups is at most what it was launched with.
+
+template <int N>
+__device__ __forceinline__ void set_registers_up()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_registers_down()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // ------------------------------------------------------------ products
 
 // What issues a product must be the same in the whole warp for the hardware's
