@@ -105,28 +105,27 @@ __device__ __forceinline__ bool wide_rows(const Heads& x)
 }
 
 // Columns [0, n) of the warp's rows (n <= COLS, a multiple of 8) times k as bf16 to rows of
-// a tensor in memory.  The columns are in registers when read() is called, before the
-// stores.  wide: the rows are on boundaries of 32 bytes.
-template <int COLS, class F>
+// a tensor in memory.  PART columns at a time; read() is called when the last are in
+// registers.  wide: the rows are on boundaries of 32 bytes.
+template <int COLS, int PART, class F>
 __device__ __forceinline__ void store_row(uint32_t tmem, int n, float k, char* row, bool live,
                                           bool wide, F&& read)
 {
 #pragma unroll
-    for (int c0 = 0; c0 < COLS; c0 += 64) {
-        constexpr int kPart = COLS < 64 ? COLS : 64;
-        uint32_t r[kPart];
+    for (int c0 = 0; c0 < COLS; c0 += PART) {
+        uint32_t r[PART];
 #pragma unroll
-        for (int c = 0; c < kPart; c += 32)
+        for (int c = 0; c < PART; c += 32)
             if (c0 + c < n) tmem_load32(tmem + c0 + c, r + c);
         tmem_wait(r);
-        if (c0 + 64 >= COLS) read();
+        if (c0 + PART >= COLS) read();
 #pragma unroll
-        for (int c = 0; c < kPart / 2; ++c)
+        for (int c = 0; c < PART / 2; ++c)
             r[c] = pack_bf16x2(__uint_as_float(r[2 * c]) * k, __uint_as_float(r[2 * c + 1]) * k);
         if (!live) continue;
         if (wide && n % 16 == 0) {
 #pragma unroll
-            for (int c = 0; c < kPart; c += 16)
+            for (int c = 0; c < PART; c += 16)
                 if (c0 + c < n) {
                     U8 w;
 #pragma unroll
@@ -135,7 +134,7 @@ __device__ __forceinline__ void store_row(uint32_t tmem, int n, float k, char* r
                 }
         } else {
 #pragma unroll
-            for (int c = 0; c < kPart; c += 8)
+            for (int c = 0; c < PART; c += 8)
                 if (c0 + c < n)
                     *reinterpret_cast<uint4*>(row + 2 * (c0 + c)) =
                         make_uint4(r[c / 2], r[c / 2 + 1], r[c / 2 + 2], r[c / 2 + 3]);
@@ -248,7 +247,7 @@ __device__ __forceinline__ bool ring_take(Ring& r, Turn<kRing>& turn, Item& item
 constexpr int kFwdThreads = 384;    // 8 softmax warps, loads, products, two idle
 // Registers of a thread, of the 168 that each is launched with: 2 x 128 x 208 + 128 x 88 =
 // 384 x 168.
-constexpr int kFwdSoftmaxRegs = 208, kFwdOtherRegs = 88;
+constexpr int kComputeRegs = 208, kOtherRegs = 88;
 
 template <int BLOCKS>
 struct FwdShape {
@@ -389,7 +388,7 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
 
     if (warp == 8) {
         // ---- items and loads
-        set_registers_down<kFwdOtherRegs>();
+        set_registers_down<kOtherRegs>();
         const uint32_t q_bytes = (uint32_t)(pk.heads * pk.tokens) * 128 * BLOCKS;
         Turn<S::kQs> qt;
         Turn<S::kStages> kt;
@@ -446,7 +445,7 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
         if (going) ring_put(bar.ring, turn, m, lost);
     } else if (warp == 9) {
         // ---- products
-        set_registers_down<kFwdOtherRegs>();
+        set_registers_down<kOtherRegs>();
         const uint32_t s_desc = tc_idesc(kTcRows, false), o_desc = tc_idesc(width, true);
         Turn<S::kQs> qt;
         Turn<S::kStages> kt, vt;
@@ -525,7 +524,7 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
         }
     } else if (warp < 8) {
         // ---- softmax: warps 0-3 have tile 0, warps 4-7 tile 1
-        set_registers_up<kFwdSoftmaxRegs>();
+        set_registers_up<kComputeRegs>();
         const int i = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + i * 128 + lanes, o_at = tmem + 256 + i * 64 * BLOCKS + lanes;
@@ -599,7 +598,7 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
             char* out = live ? row_of(a.out, m.q0 + row, head) : nullptr;
             if (going && tiles > 0) {
                 tc_fence_after();
-                store_row<64 * BLOCKS>(o_at, a.D, total == 0.0f ? 0.0f : 1.0f / total, out, live, wide,
+                store_row<64 * BLOCKS, 64>(o_at, a.D, total == 0.0f ? 0.0f : 1.0f / total, out, live, wide,
                                        [&] {
                                            tc_fence_before();
                                            __syncwarp();
@@ -614,7 +613,7 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
                     : total == 0.0f ? -INFINITY : (shift + log2f(total)) * kLn2;
         }
     } else {
-        set_registers_down<kFwdOtherRegs>();
+        set_registers_down<kOtherRegs>();
     }
     tc_finish(lost, tmem, warp == 9);
 }
@@ -625,216 +624,319 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
 //   scores and dout v^T (tensor memory, columns 0 and 128) -> ds in bf16 (384)
 //   -> dq += ds k (256).
 // The compute warps copy both products to registers before they work on them, so
-// the next tile's two run meanwhile, and dq's behind them.  Warps 0-3 have the
-// first 64 keys of a tile, 4-7 the others.
+// the next tile's two run meanwhile, and dq's behind them; the first two of the next
+// item are issued before the last dq of this one.  Warps 0-3 have the first 64 keys of a
+// tile, 4-7 the others.
 
-constexpr int kGradThreads = 320;
+constexpr int kGradThreads = 384;   // 8 compute warps, loads, products, two idle
 
 struct GradBars {
-    uint64_t once_full, in_full[2], in_empty[2], s_full, s_free, g_full, p_full, d_full, d_free;
+    Ring ring;
+    uint64_t once_full[2], once_empty[2], in_full[3], in_empty[3];
+    uint64_t s_full, s_free, g_full, p_full, d_full, d_free, o_full, o_free;
     uint32_t tmem;
     int lost;
 };
-static_assert(sizeof(GradBars) <= 256, "the barriers' place");
+static_assert(sizeof(GradBars) <= 1024, "the barriers' place");
 
 template <int BLOCKS>
 struct GradShape {
     static constexpr int kTile = BLOCKS * kTcBlock;
-    static constexpr int kA = 0, kB = kTile;                 // what stays: q, dout or k, v
-    static constexpr int kIn = 2 * kTile;                    // two stages of the others
-    static constexpr int kRows = kIn + 4 * kTile;            // 2 x 2 x 128 floats
-    static constexpr int kBars = kRows + 2048;
-    static constexpr int kBytes = kBars + 256 + 1024;
+    static constexpr int kOnces = BLOCKS == 1 ? 2 : 1;       // pairs of what stays: q, dout or k, v
+    static constexpr int kStages = BLOCKS == 1 ? 3 : 2;      // pairs of the others
+    static constexpr int kIn = kOnces * 2 * kTile;
+    static constexpr int kRows = kIn + kStages * 2 * kTile;  // floats of rows: kStages x 2 x 128
+    static constexpr int kBars = kRows + 3 * 1024;
+    static constexpr int kBytes = kBars + 1024 + 1024;
+    static_assert(kBytes <= 227 * 1024, "shared memory of a block");
 };
 
-__device__ __forceinline__ void grad_init(GradBars& bar)
+// The start of a block of either kernel: barriers, tensor memory.
+template <int BLOCKS>
+__device__ __forceinline__ uint32_t grad_start(GradBars& bar, const Maps& maps, int warp)
 {
-    mbar_init(&bar.once_full, 1);
-    for (int i = 0; i < 2; ++i) {
-        mbar_init(&bar.in_full[i], 1);
-        mbar_init(&bar.in_empty[i], 1);
+    using S = GradShape<BLOCKS>;
+    if (threadIdx.x == 0) {
+        ring_init(bar.ring, 9);
+        for (int i = 0; i < S::kOnces; ++i) {
+            mbar_init(&bar.once_full[i], 1);
+            mbar_init(&bar.once_empty[i], 1);
+        }
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&bar.in_full[i], 1);
+            mbar_init(&bar.in_empty[i], 1);
+        }
+        mbar_init(&bar.s_full, 1);
+        mbar_init(&bar.s_free, 8);
+        mbar_init(&bar.g_full, 1);
+        mbar_init(&bar.p_full, 8);
+        mbar_init(&bar.d_full, 8);
+        mbar_init(&bar.d_free, 1);
+        mbar_init(&bar.o_full, 1);
+        mbar_init(&bar.o_free, 8);
+        bar.lost = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        tma_prefetch(&maps.q);
+        tma_prefetch(&maps.k);
+        tma_prefetch(&maps.v);
+        tma_prefetch(&maps.dout);
     }
-    mbar_init(&bar.s_full, 1);
-    mbar_init(&bar.s_free, 8);
-    mbar_init(&bar.g_full, 1);
-    mbar_init(&bar.p_full, 8);
-    mbar_init(&bar.d_full, 8);
-    mbar_init(&bar.d_free, 1);
-    bar.lost = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    pdl_wait_prior();
+    if (warp == 9) tmem_alloc(&bar.tmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_launch_dependents();
+    return (uint32_t)uniform((int)bar.tmem);
+}
+
+// Two operands' tiles to a pair of places.
+template <int BLOCKS>
+__device__ __forceinline__ void load_pair(char* to, const CUtensorMap* x, const CUtensorMap* y,
+                                          uint64_t* full, int head, int row)
+{
+    constexpr int kTile = GradShape<BLOCKS>::kTile;
+    mbar_expect_tx(full, 2 * kTile);
+    for (int b = 0; b < BLOCKS; ++b) {
+        tma_load(to + b * kTcBlock, x, full, b * kTcCols, head, row);
+        tma_load(to + kTile + b * kTcBlock, y, full, b * kTcCols, head, row);
+    }
 }
 
 template <int BLOCKS>
 __global__ void __launch_bounds__(kGradThreads, 1)
-k_attn_tc_dq(const __grid_constant__ Maps maps, AttnArgs a)
+k_attn_tc_dq(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a, int tiles,
+             int64_t items)
 {
     using S = GradShape<BLOCKS>;
     extern __shared__ char smem_raw[];
     char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     GradBars& bar = *reinterpret_cast<GradBars*>(smem + S::kBars);
-    float* delta_s = reinterpret_cast<float*>(smem + S::kRows);
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    pdl_wait_prior();
-    if (warp == 9) tmem_alloc(&bar.tmem);
-    else if (threadIdx.x == 0) grad_init(bar);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    pdl_launch_dependents();
+    const uint32_t tmem = grad_start<BLOCKS>(bar, maps, warp);
     volatile int* lost = &bar.lost;
-    const uint32_t tmem = (uint32_t)uniform((int)bar.tmem);
-
-    const Tile t = find_tile(a, (int)(gridDim.x - 1 - blockIdx.x), kTcRows, false);
-    const int h = blockIdx.y, hk = h / (a.Hq / a.Hk);
     const int ksteps = (a.D + 15) / 16, width = ksteps * 16;
-    const int end = !t.any ? 0
-                    : !a.causal ? t.nk
-                                : max(0, min(t.nk, min(t.row0 + kTcRows, t.nq) + t.nk - t.nq));
-    const int n = (end + kTcRows - 1) / kTcRows;
+    Turn<kRing> turn;
 
     if (warp == 8) {
-        if (lane == 0 && n > 0) {
-            mbar_expect_tx(&bar.once_full, 2 * S::kTile);
-            for (int b = 0; b < BLOCKS; ++b) {
-                tma_load(smem + S::kA + b * kTcBlock, &maps.q, &bar.once_full, b * kTcCols, h,
-                         (int)t.q0 + t.row0);
-                tma_load(smem + S::kB + b * kTcBlock, &maps.dout, &bar.once_full, b * kTcCols, h,
-                         (int)t.q0 + t.row0);
-            }
-            for (int j = 0; j < n; ++j) {
-                const int st = j & 1, round = j >> 1;
-                if (round > 0 && !tc_wait(&bar.in_empty[st], (round - 1) & 1, lost)) break;
-                char* in = smem + S::kIn + st * 2 * S::kTile;
-                mbar_expect_tx(&bar.in_full[st], 2 * S::kTile);
-                for (int b = 0; b < BLOCKS; ++b) {
-                    tma_load(in + b * kTcBlock, &maps.k, &bar.in_full[st], b * kTcCols, hk,
-                             (int)t.k0 + j * kTcRows);
-                    tma_load(in + S::kTile + b * kTcBlock, &maps.v, &bar.in_full[st], b * kTcCols,
-                             hk, (int)t.k0 + j * kTcRows);
+        // ---- items and loads
+        set_registers_down<kOtherRegs>();
+        Turn<S::kOnces> qt;
+        Turn<S::kStages> kt;
+        bool going = true;
+        Item m{};
+        for (int64_t w = blockIdx.x; w < items && going; w += gridDim.x) {
+            // the tiles at the end of a sequence see the most keys and go first
+            const int tile = (int)(w / a.Hq);
+            const Tile t = find_tile(a, tiles - 1 - tile, kTcRows, false);
+            if (!t.any) continue;
+            const int end = !a.causal ? t.nk
+                                      : max(0, min(t.nk, min(t.row0 + kTcRows, t.nq) + t.nk - t.nq));
+            const int n = (end + kTcRows - 1) / kTcRows;
+            m = {t.q0, t.k0, t.nq, t.nk, t.row0, (int)(w - (int64_t)tile * a.Hq), {n, 0}};
+            going = ring_put(bar.ring, turn, m, lost);
+            if (!going || n == 0) continue;
+            if (lane == 0) {
+                going = tc_wait(&bar.once_empty[qt.at], qt.parity ^ 1, lost);
+                if (going)
+                    load_pair<BLOCKS>(smem + qt.at * 2 * S::kTile, &maps.q, &maps.dout,
+                                      &bar.once_full[qt.at], m.head, (int)t.q0 + t.row0);
+                for (int j = 0; j < n && going; ++j) {
+                    going = tc_wait(&bar.in_empty[kt.at], kt.parity ^ 1, lost);
+                    if (!going) break;
+                    load_pair<BLOCKS>(smem + S::kIn + kt.at * 2 * S::kTile, &maps.k, &maps.v,
+                                      &bar.in_full[kt.at], m.head / (a.Hq / a.Hk),
+                                      (int)t.k0 + j * kTcRows);
+                    kt.next();
                 }
             }
+            qt.next();
+            going = __shfl_sync(0xffffffffu, (int)going, 0) != 0;
         }
+        m.tiles[0] = -1;
+        if (going) ring_put(bar.ring, turn, m, lost);
     } else if (warp == 9) {
+        // ---- products
+        set_registers_down<kOtherRegs>();
         const uint32_t s_desc = tc_idesc(kTcRows, false), o_desc = tc_idesc(width, true);
-        bool going = n > 0 && tc_wait_warp(&bar.once_full, 0, lost);
-        // dq += ds k of tile j
-        const auto add_dq = [&](int j) {
-            going = tc_wait_warp(&bar.d_full, j & 1, lost);
+        Turn<S::kOnces> qt;
+        Turn<S::kStages> kt, dt;
+        uint32_t s_par = 1, d_par = 0, f_par = 1;
+        bool going = true, left = false, left_first = false;
+        // dq += ds k of the step before this one
+        const auto add_dq = [&] {
+            going = tc_wait_warp(&bar.d_full, d_par, lost);
+            d_par ^= 1;
+            if (going && left_first) {    // the result of the item before has been read
+                going = tc_wait_warp(&bar.o_free, f_par, lost);
+                f_par ^= 1;
+            }
             if (!going) return;
             tc_fence_after();
             if (elect_one()) {
-                tc_rows(tmem + 256, tmem + 384, 0, smem + S::kIn + (j & 1) * 2 * S::kTile, o_desc,
-                        j > 0);
+                tc_rows(tmem + 256, tmem + 384, 0, smem + S::kIn + dt.at * 2 * S::kTile, o_desc,
+                        !left_first);
                 tc_commit(&bar.d_free);
-                tc_commit(&bar.in_empty[j & 1]);
+                tc_commit(&bar.in_empty[dt.at]);
             }
             __syncwarp();
+            dt.next();
         };
-        for (int j = 0; j < n && going; ++j) {
-            const int st = j & 1;
-            going = tc_wait_warp(&bar.in_full[st], (j >> 1) & 1, lost);
-            if (!going) break;
-            char* in = smem + S::kIn + st * 2 * S::kTile;
-            const int rows = t.nk - j * kTcRows;
-            if (rows < kTcRows) {     // dq sums over the keys
-                clear_rows(in, rows, BLOCKS);
-                fence_async_proxy();
+        Item m;
+        while (going && ring_take(bar.ring, turn, m, lost)) {
+            const int n = m.tiles[0];
+            if (n == 0) {     // the compute warps come to it only after the item before
+                if (left) add_dq();
+                left = false;
+                continue;
+            }
+            going = tc_wait_warp(&bar.once_full[qt.at], qt.parity, lost);
+            const char* q = smem + qt.at * 2 * S::kTile;
+            for (int j = 0; j < n && going; ++j) {
+                going = tc_wait_warp(&bar.in_full[kt.at], kt.parity, lost);
+                if (!going) break;
+                char* in = smem + S::kIn + kt.at * 2 * S::kTile;
+                const int rows = m.nk - j * kTcRows;
+                if (rows < kTcRows) {     // dq sums over the keys
+                    clear_rows(in, rows, BLOCKS);
+                    fence_async_proxy();
+                    __syncwarp();
+                }
+                going = tc_wait_warp(&bar.s_free, s_par, lost);
+                s_par ^= 1;
+                if (!going) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    tc_dot<BLOCKS>(tmem, q, in, ksteps, s_desc);
+                    tc_dot<BLOCKS>(tmem + 128, q + S::kTile, in + S::kTile, ksteps, s_desc);
+                    tc_commit(&bar.s_full);
+                    if (j + 1 == n) tc_commit(&bar.once_empty[qt.at]);
+                }
                 __syncwarp();
+                kt.next();
+                if (left) add_dq();
+                left = true;
+                left_first = j == 0;
             }
-            if (j > 0) going = tc_wait_warp(&bar.s_free, (j - 1) & 1, lost);
-            if (!going) break;
-            tc_fence_after();
-            if (elect_one()) {
-                tc_dot<BLOCKS>(tmem, smem + S::kA, in, ksteps, s_desc);
-                tc_dot<BLOCKS>(tmem + 128, smem + S::kB, in + S::kTile, ksteps, s_desc);
-                tc_commit(&bar.s_full);
-            }
-            __syncwarp();
-            if (j > 0) add_dq(j - 1);
+            qt.next();
         }
-        if (going && n > 0) add_dq(n - 1);
-    } else {
+        if (going && left) add_dq();
+    } else if (warp < 8) {
+        // ---- scores' gradients
+        set_registers_up<kComputeRegs>();
+        float* delta_s = reinterpret_cast<float*>(smem + S::kRows);
         const int r = (warp & 3) * 32 + lane, half = warp >> 2;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const int row = t.row0 + r;
-        const bool live = t.any && row < t.nq;
-        // delta of 16 rows, two at a time
-        for (int q = 0; q < 16; q += 2) {
-            const int rr = warp * 16 + q + (lane >> 4), d = (lane & 15) * 8;
-            float y = 0.0f;
-            if (t.any && t.row0 + rr < t.nq && d < a.D) {
-                const int64_t at = t.q0 + t.row0 + rr;
-                const uint4 u = *reinterpret_cast<const uint4*>(row_of(a.dout, at, h) + 2 * d);
-                const uint4 w = *reinterpret_cast<const uint4*>(row_of(a.out, at, h) + 2 * d);
-                const uint32_t us[4] = {u.x, u.y, u.z, u.w}, ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    y = fmaf(bf16_hi(us[e]), bf16_hi(ws[e]), fmaf(bf16_lo(us[e]), bf16_lo(ws[e]), y));
-            }
-#pragma unroll
-            for (int o = 1; o < 16; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-            if ((lane & 15) == 0) {
-                delta_s[rr] = y;
-                if (t.any && t.row0 + rr < t.nq) a.delta[(int64_t)h * a.Tq + t.q0 + t.row0 + rr] = y;
-            }
-        }
-        asm volatile("bar.sync 1, 256;" ::: "memory");    // the compute warps
-        const float delta = delta_s[r];
-        const float lse = live ? a.lse[(int64_t)h * a.Tq + t.q0 + row] : -INFINITY;
-        const bool none = lse == -INFINITY;
-        const int seen = none ? 0 : a.causal ? min(t.nk, row + t.nk - t.nq + 1) : t.nk;
         const float c2 = a.scale * kLog2e;
-        const F2 cc = pack2(c2, c2), nl = pack2(-lse * kLog2e, -lse * kLog2e);
-        const F2 nd = pack2(-delta, -delta);
+        const F2 cc = pack2(c2, c2);
+        const bool wide = wide_rows(a.dq);
+        uint32_t s_par = 0, d_par = 0;
         bool going = true;
-        for (int j = 0; j < n; ++j) {
-            going = tc_wait_warp(&bar.s_full, j & 1, lost);
-            if (!going) break;
-            tc_fence_after();
-            uint32_t x[128];      // 64 scores, 64 of dout v^T
-            tmem_load32(tmem + lanes + 64 * half, x);
-            tmem_load32(tmem + lanes + 64 * half + 32, x + 32);
-            tmem_load32(tmem + lanes + 128 + 64 * half, x + 64);
-            tmem_load32(tmem + lanes + 128 + 64 * half + 32, x + 96);
-            tmem_wait(x);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.s_free);
-            uint32_t ds[32];
-            const int most = seen - j * kTcRows - 64 * half;
-            const bool mask = __any_sync(0xffffffffu, most < 64);
+        Item m;
+        while (going && ring_take(bar.ring, turn, m, lost)) {
+            const int row = m.row0 + r, n = m.tiles[0];
+            const bool live = row < m.nq;
+            const float lse = live ? a.lse[(int64_t)m.head * a.Tq + m.q0 + row] : -INFINITY;
+            // delta of 16 rows, two at a time, all loads first
+            float part[8];
+            {
+                uint4 u[8], w[8];
+                const int d = (lane & 15) * 8;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                const F2 u = fma2((F2)x[2 * e + 1] << 32 | x[2 * e], cc, nl);
-                const F2 p = pack2(ex2(lo2(u)), ex2(hi2(u)));
-                const F2 d = mul2(p, add2((F2)x[64 + 2 * e + 1] << 32 | x[64 + 2 * e], nd));
-                ds[e] = pack_bf16x2(lo2(d), hi2(d));
-            }
-            if (mask) {
+                for (int q = 0; q < 8; ++q) {
+                    const int rr = m.row0 + warp * 16 + 2 * q + (lane >> 4);
+                    u[q] = w[q] = make_uint4(0, 0, 0, 0);
+                    if (rr < m.nq && d < a.D) {
+                        u[q] = *reinterpret_cast<const uint4*>(row_of(a.dout, m.q0 + rr, m.head) + 2 * d);
+                        w[q] = *reinterpret_cast<const uint4*>(row_of(a.out, m.q0 + rr, m.head) + 2 * d);
+                    }
+                }
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    ds[e] = 2 * e + 1 < most ? ds[e] : 2 * e < most ? ds[e] & 0xffffu : 0u;
+                for (int q = 0; q < 8; ++q) {
+                    const uint32_t us[4] = {u[q].x, u[q].y, u[q].z, u[q].w};
+                    const uint32_t ws[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+                    part[q] = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        part[q] = fmaf(bf16_hi(us[e]), bf16_hi(ws[e]),
+                                       fmaf(bf16_lo(us[e]), bf16_lo(ws[e]), part[q]));
+                }
             }
-            if (j > 0) going = tc_wait_warp(&bar.d_free, (j - 1) & 1, lost);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) part[q] += __shfl_xor_sync(0xffffffffu, part[q], o);
+                if ((lane & 15) == 0) {
+                    const int rr = warp * 16 + 2 * q + (lane >> 4);
+                    delta_s[rr] = part[q];
+                    if (m.row0 + rr < m.nq)
+                        a.delta[(int64_t)m.head * a.Tq + m.q0 + m.row0 + rr] = part[q];
+                }
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");    // the compute warps
+            const float delta = delta_s[r];
+            delta_s = reinterpret_cast<float*>(smem + S::kRows) +
+                      (delta_s == reinterpret_cast<float*>(smem + S::kRows) ? 128 : 0);
+            const bool none = lse == -INFINITY;
+            const int seen = none ? 0 : a.causal ? min(m.nk, row + m.nk - m.nq + 1) : m.nk;
+            const F2 nl = pack2(-lse * kLog2e, -lse * kLog2e), nd = pack2(-delta, -delta);
+            for (int j = 0; j < n; ++j) {
+                going = tc_wait_warp(&bar.s_full, s_par, lost);
+                s_par ^= 1;
+                if (!going) break;
+                tc_fence_after();
+                uint32_t x[128];      // 64 scores, 64 of dout v^T
+                tmem_load32(tmem + lanes + 64 * half, x);
+                tmem_load32(tmem + lanes + 64 * half + 32, x + 32);
+                tmem_load32(tmem + lanes + 128 + 64 * half, x + 64);
+                tmem_load32(tmem + lanes + 128 + 64 * half + 32, x + 96);
+                tmem_wait(x);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.s_free);
+                uint32_t ds[32];
+                const int most = seen - j * kTcRows - 64 * half;
+                const bool mask = __any_sync(0xffffffffu, most < 64);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const F2 u = fma2((F2)x[2 * e + 1] << 32 | x[2 * e], cc, nl);
+                    const F2 p = pack2(ex2(lo2(u)), ex2(hi2(u)));
+                    const F2 d = mul2(p, add2((F2)x[64 + 2 * e + 1] << 32 | x[64 + 2 * e], nd));
+                    ds[e] = pack_bf16x2(lo2(d), hi2(d));
+                }
+                if (mask) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        ds[e] = 2 * e + 1 < most ? ds[e] : 2 * e < most ? ds[e] & 0xffffu : 0u;
+                }
+                if (j > 0) {      // the product before has read the last ones
+                    going = tc_wait_warp(&bar.d_free, d_par ^ 1, lost);
+                    if (!going) break;
+                    tc_fence_after();
+                }
+                d_par ^= 1;
+                tmem_store32(tmem + lanes + 384 + 32 * half, ds);
+                tmem_wait_stores();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.d_full);
+            }
+            if (going && n > 0) going = tc_wait_warp(&bar.d_free, d_par ^ 1, lost);
             if (!going) break;
-            tc_fence_after();
-            tmem_store32(tmem + lanes + 384 + 32 * half, ds);
-            tmem_wait_stores();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.d_full);
-        }
-        if (going && n > 0) going = tc_wait_warp(&bar.d_free, (n - 1) & 1, lost);
-        if (going) {
             tc_fence_after();
             // a thread's half of its row, in whole 32 columns
             const int first = half * BLOCKS * 32, cols = min(a.D - first, BLOCKS * 32);
-            char* out = live ? row_of(a.dq, t.q0 + row, h) + 2 * first : nullptr;
+            char* out = live ? row_of(a.dq, m.q0 + row, m.head) + 2 * first : nullptr;
             if (n > 0)
-                store_row<BLOCKS * 32>(tmem + lanes + 256 + first, cols, a.scale, out, live,
-                                       wide_rows(a.dq), [] {});
+                store_row<BLOCKS * 32, 32>(tmem + lanes + 256 + first, cols, a.scale, out, live, wide, [&] {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.o_free);
+                });
             else zero_row(cols, out, live);
         }
+    } else {
+        set_registers_down<kOtherRegs>();
     }
     tc_finish(lost, tmem, warp == 9);
 }
@@ -849,11 +951,18 @@ k_attn_tc_dq(const __grid_constant__ Maps maps, AttnArgs a)
 // p^T and ds^T take the places of what they were made from, each warp writing
 // over columns that only it has read.  The products alternate with the
 // compute warps' two halves: dv and the next scores run while ds is computed, dk
-// and the next dp while p is.
+// and the next dp while p is; the next item's first two run behind this one's stores.
+
+// The queries' tiles that an item of keys walks over, for each head.
+__device__ __forceinline__ int first_query(const AttnArgs& a, const Item& m)
+{
+    return a.causal ? max(0, m.row0 - (m.nk - m.nq)) / kTcRows * kTcRows : 0;
+}
 
 template <int BLOCKS>
 __global__ void __launch_bounds__(kGradThreads, 1)
-k_attn_tc_dkv(const __grid_constant__ Maps maps, AttnArgs a)
+k_attn_tc_dkv(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a, int tiles,
+              int64_t items)
 {
     using S = GradShape<BLOCKS>;
     constexpr uint32_t kDv = 256, kDk = BLOCKS == 2 ? 384 : 320;
@@ -862,39 +971,37 @@ k_attn_tc_dkv(const __grid_constant__ Maps maps, AttnArgs a)
     GradBars& bar = *reinterpret_cast<GradBars*>(smem + S::kBars);
     float* rows_s = reinterpret_cast<float*>(smem + S::kRows);   // [stage][-lse log2e, -delta][128]
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    pdl_wait_prior();
-    if (warp == 9) tmem_alloc(&bar.tmem);
-    else if (threadIdx.x == 0) grad_init(bar);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    pdl_launch_dependents();
+    const uint32_t tmem = grad_start<BLOCKS>(bar, maps, warp);
     volatile int* lost = &bar.lost;
-    const uint32_t tmem = (uint32_t)uniform((int)bar.tmem);
-
-    // the first keys of a sequence are seen by the most queries: tiles in order
-    const Tile t = find_tile(a, (int)blockIdx.x, kTcRows, true);
-    const int hk = blockIdx.y, G = a.Hq / a.Hk;
+    const int G = a.Hq / a.Hk;
     const int ksteps = (a.D + 15) / 16, width = ksteps * 16;
-    // the tiles of queries from the first that sees this tile's first key
-    const int first = a.causal ? max(0, t.row0 - (t.nk - t.nq)) / kTcRows * kTcRows : 0;
-    const int per = t.any && first < t.nq ? (t.nq - first + kTcRows - 1) / kTcRows : 0;
-    const int n = per * G;
+    Turn<kRing> turn;
 
     if (warp == 8) {
-        if (n > 0) {
-            if (lane == 0) {
-                mbar_expect_tx(&bar.once_full, 2 * S::kTile);
-                for (int b = 0; b < BLOCKS; ++b) {
-                    tma_load(smem + S::kA + b * kTcBlock, &maps.k, &bar.once_full, b * kTcCols, hk,
-                             (int)t.k0 + t.row0);
-                    tma_load(smem + S::kB + b * kTcBlock, &maps.v, &bar.once_full, b * kTcCols, hk,
-                             (int)t.k0 + t.row0);
-                }
-            }
-            int h = hk * G, i0 = first;
-            for (int j = 0; j < n; ++j) {
-                const int st = j & 1, round = j >> 1;
+        // ---- items and loads
+        set_registers_down<kOtherRegs>();
+        Turn<S::kOnces> qt;
+        Turn<S::kStages> kt;
+        bool going = true;
+        Item m{};
+        for (int64_t w = blockIdx.x; w < items && going; w += gridDim.x) {
+            // the first keys of a sequence are seen by the most queries: tiles in order
+            const int tile = (int)(w / a.Hk);
+            const Tile t = find_tile(a, tile, kTcRows, true);
+            if (!t.any) continue;
+            m = {t.q0, t.k0, t.nq, t.nk, t.row0, (int)(w - (int64_t)tile * a.Hk), {0, 0}};
+            const int first = first_query(a, m);
+            const int n = first < t.nq ? (t.nq - first + kTcRows - 1) / kTcRows * G : 0;
+            m.tiles[0] = n;
+            going = ring_put(bar.ring, turn, m, lost);
+            if (!going || n == 0) continue;
+            going = tc_wait_warp(&bar.once_empty[qt.at], qt.parity ^ 1, lost);
+            if (going && lane == 0)
+                load_pair<BLOCKS>(smem + qt.at * 2 * S::kTile, &maps.k, &maps.v,
+                                  &bar.once_full[qt.at], m.head, (int)t.k0 + t.row0);
+            qt.next();
+            int h = m.head * G, i0 = first;
+            for (int j = 0; j < n && going; ++j) {
                 float nl[4], nd[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -904,23 +1011,18 @@ k_attn_tc_dkv(const __grid_constant__ Maps maps, AttnArgs a)
                     nl[e] = l == -INFINITY ? -INFINITY : -l * kLog2e;
                     nd[e] = row < t.nq ? -a.delta[at] : 0.0f;
                 }
-                if (round > 0 && !tc_wait_warp(&bar.in_empty[st], (round - 1) & 1, lost)) break;
+                going = tc_wait_warp(&bar.in_empty[kt.at], kt.parity ^ 1, lost);
+                if (!going) break;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    rows_s[st * 256 + 32 * e + lane] = nl[e];
-                    rows_s[st * 256 + 128 + 32 * e + lane] = nd[e];
+                    rows_s[kt.at * 256 + 32 * e + lane] = nl[e];
+                    rows_s[kt.at * 256 + 128 + 32 * e + lane] = nd[e];
                 }
                 __syncwarp();
-                if (lane == 0) {
-                    char* in = smem + S::kIn + st * 2 * S::kTile;
-                    mbar_expect_tx(&bar.in_full[st], 2 * S::kTile);
-                    for (int b = 0; b < BLOCKS; ++b) {
-                        tma_load(in + b * kTcBlock, &maps.q, &bar.in_full[st], b * kTcCols, h,
-                                 (int)t.q0 + i0);
-                        tma_load(in + S::kTile + b * kTcBlock, &maps.dout, &bar.in_full[st],
-                                 b * kTcCols, h, (int)t.q0 + i0);
-                    }
-                }
+                if (lane == 0)
+                    load_pair<BLOCKS>(smem + S::kIn + kt.at * 2 * S::kTile, &maps.q, &maps.dout,
+                                      &bar.in_full[kt.at], h, (int)t.q0 + i0);
+                kt.next();
                 i0 += kTcRows;
                 if (i0 >= t.nq) {
                     i0 = first;
@@ -928,158 +1030,201 @@ k_attn_tc_dkv(const __grid_constant__ Maps maps, AttnArgs a)
                 }
             }
         }
+        m.tiles[0] = -1;
+        if (going) ring_put(bar.ring, turn, m, lost);
     } else if (warp == 9) {
+        // ---- products
+        set_registers_down<kOtherRegs>();
         const uint32_t s_desc = tc_idesc(kTcRows, false), o_desc = tc_idesc(width, true);
-        bool going = n > 0 && tc_wait_warp(&bar.once_full, 0, lost);
-        // waits for tile j, clears what lies beyond the sequence, issues its scores
-        const auto scores = [&](int j) {
-            const int st = j & 1, rows = t.nq - (first + j % per * kTcRows);
-            going = tc_wait_warp(&bar.in_full[st], (j >> 1) & 1, lost);
-            if (!going) return;
-            char* in = smem + S::kIn + st * 2 * S::kTile;
-            if (rows < kTcRows) {     // dk and dv sum over the queries
-                clear_rows(in, rows, BLOCKS);
-                clear_rows(in + S::kTile, rows, BLOCKS);
-                fence_async_proxy();
+        Turn<S::kOnces> qt;
+        Turn<S::kStages> kt, dt;      // of the next scores, of the step under way
+        uint32_t p_par = 0, f_par = 1;
+        bool going = true;
+        Item m;
+        while (going && ring_take(bar.ring, turn, m, lost)) {
+            const int n = m.tiles[0];
+            if (n == 0) continue;
+            const int first = first_query(a, m);
+            int i0 = first;               // of the next scores
+            const char* k = smem + qt.at * 2 * S::kTile;
+            going = tc_wait_warp(&bar.once_full[qt.at], qt.parity, lost);
+            // waits for a tile, clears what lies beyond the sequence, issues its scores
+            const auto scores = [&] {
+                going = tc_wait_warp(&bar.in_full[kt.at], kt.parity, lost);
+                if (!going) return;
+                char* in = smem + S::kIn + kt.at * 2 * S::kTile;
+                if (m.nq - i0 < kTcRows) {     // dk and dv sum over the queries
+                    clear_rows(in, m.nq - i0, BLOCKS);
+                    clear_rows(in + S::kTile, m.nq - i0, BLOCKS);
+                    fence_async_proxy();
+                    __syncwarp();
+                }
+                if (elect_one()) {
+                    tc_dot<BLOCKS>(tmem, k, in, ksteps, s_desc);
+                    tc_commit(&bar.s_full);
+                }
                 __syncwarp();
-            }
-            if (elect_one()) {
-                tc_dot<BLOCKS>(tmem, smem + S::kA, in, ksteps, s_desc);
-                tc_commit(&bar.s_full);
-            }
-            __syncwarp();
-        };
-        const auto grads = [&](int j) {
-            if (elect_one()) {
-                tc_dot<BLOCKS>(tmem + 128, smem + S::kB, smem + S::kIn + (j & 1) * 2 * S::kTile + S::kTile,
-                       ksteps, s_desc);
-                tc_commit(&bar.g_full);
-            }
-            __syncwarp();
-        };
-        if (going) scores(0);
-        if (going) grads(0);
-        for (int j = 0; j < n && going; ++j) {
-            const char* in = smem + S::kIn + (j & 1) * 2 * S::kTile;
-            going = tc_wait_warp(&bar.p_full, j & 1, lost);
-            if (!going) break;
-            tc_fence_after();
-            if (elect_one()) {
-                tc_rows(tmem + kDv, tmem, 32, in + S::kTile, o_desc, j > 0);
-                tc_commit(&bar.d_free);
-            }
-            __syncwarp();
-            if (j + 1 < n) {
+                i0 += kTcRows;
+                if (i0 >= m.nq) i0 = first;
+                kt.next();
+            };
+            const auto grads = [&](int at) {
+                if (elect_one()) {
+                    tc_dot<BLOCKS>(tmem + 128, k + S::kTile,
+                                   smem + S::kIn + at * 2 * S::kTile + S::kTile, ksteps, s_desc);
+                    tc_commit(&bar.g_full);
+                }
+                __syncwarp();
+            };
+            if (going) scores();
+            if (going) grads(dt.at);
+            for (int j = 0; j < n && going; ++j) {
+                const char* in = smem + S::kIn + dt.at * 2 * S::kTile;
+                going = tc_wait_warp(&bar.p_full, p_par, lost);
+                if (going && j == 0) {         // the results of the item before have been read
+                    going = tc_wait_warp(&bar.o_free, f_par, lost);
+                    f_par ^= 1;
+                }
+                if (!going) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    tc_rows(tmem + kDv, tmem, 32, in + S::kTile, o_desc, j > 0);
+                    tc_commit(&bar.d_free);
+                }
+                __syncwarp();
                 // the next scores take the probabilities' place
                 going = tc_wait_warp(&bar.d_free, 0, lost);
-                if (going) scores(j + 1);
-            } else {
-                going = tc_wait_warp(&bar.d_free, 0, lost);
+                if (going && j + 1 < n) scores();
+                if (!going) break;
+                going = tc_wait_warp(&bar.d_full, p_par, lost);
+                p_par ^= 1;
+                if (!going) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    tc_rows(tmem + kDk, tmem + 128, 32, in, o_desc, j > 0);
+                    tc_commit(&bar.in_empty[dt.at]);
+                    tc_commit(&bar.d_free);
+                    if (j + 1 == n) {
+                        tc_commit(&bar.once_empty[qt.at]);
+                        tc_commit(&bar.o_full);
+                    }
+                }
+                __syncwarp();
+                dt.next();
+                going = tc_wait_warp(&bar.d_free, 1, lost);
+                if (going && j + 1 < n) grads(dt.at);
             }
-            if (!going) break;
-            going = tc_wait_warp(&bar.d_full, j & 1, lost);
-            if (!going) break;
-            tc_fence_after();
-            if (elect_one()) {
-                tc_rows(tmem + kDk, tmem + 128, 32, in, o_desc, j > 0);
-                tc_commit(&bar.in_empty[j & 1]);
-                tc_commit(&bar.d_free);
-            }
-            __syncwarp();
-            going = tc_wait_warp(&bar.d_free, 1, lost);
-            if (going && j + 1 < n) grads(j + 1);
+            qt.next();
         }
-        // the compute warps wait here for the last product
-        if (going && n > 0 && elect_one()) tc_commit(&bar.s_full);
-    } else {
+    } else if (warp < 8) {
+        // ---- probabilities and scores' gradients
+        set_registers_up<kComputeRegs>();
         const int r = (warp & 3) * 32 + lane, half = warp >> 2;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const int row = t.row0 + r;
-        const bool live = t.any && row < t.nk;
         const float c2 = a.scale * kLog2e;
         const F2 cc = pack2(c2, c2);
+        const bool wide_k = wide_rows(a.dk), wide_v = wide_rows(a.dv);
+        Turn<S::kStages> kt;
+        uint32_t s_par = 0, o_par = 0;
         bool going = true;
-        for (int j = 0; j < n; ++j) {
-            const int st = j & 1, i0 = first + j % per * kTcRows;
-            const float* nl = rows_s + st * 256 + 64 * half;
-            const float* nd = nl + 128;
-            going = tc_wait_warp(&bar.in_full[st], (j >> 1) & 1, lost) &&
-                    tc_wait_warp(&bar.s_full, j & 1, lost);
-            if (!going) break;
-            tc_fence_after();
-            uint32_t s[64];
-            tmem_load32(tmem + lanes + 64 * half, s);
-            tmem_load32(tmem + lanes + 64 * half + 32, s + 32);
-            tmem_wait(s);
-            // columns from `from` on see this row's key
-            const int from = a.causal ? row - (t.nk - t.nq) - i0 - 64 * half : 0;
-            const bool mask = __any_sync(0xffffffffu, from > 0);
-            uint32_t p[32];
+        Item m;
+        while (going && ring_take(bar.ring, turn, m, lost)) {
+            const int n = m.tiles[0], first = first_query(a, m), row = m.row0 + r;
+            const bool live = row < m.nk;
+            int i0 = first;
+            for (int j = 0; j < n; ++j) {
+                const float* nl = rows_s + kt.at * 256 + 64 * half;
+                const float* nd = nl + 128;
+                going = tc_wait_warp(&bar.in_full[kt.at], kt.parity, lost) &&
+                        tc_wait_warp(&bar.s_full, s_par, lost);
+                if (!going) break;
+                kt.next();
+                tc_fence_after();
+                uint32_t s[64];
+                tmem_load32(tmem + lanes + 64 * half, s);
+                tmem_load32(tmem + lanes + 64 * half + 32, s + 32);
+                tmem_wait(s);
+                // columns from `from` on see this row's key
+                const int from = a.causal ? row - (m.nk - m.nq) - i0 - 64 * half : 0;
+                const bool mask = __any_sync(0xffffffffu, from > 0);
+                uint32_t p[32];
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-                const float4 l = *reinterpret_cast<const float4*>(nl + 2 * e);
-                const F2 u = fma2((F2)s[2 * e + 1] << 32 | s[2 * e], cc, pack2(l.x, l.y));
-                const F2 v = fma2((F2)s[2 * e + 3] << 32 | s[2 * e + 2], cc, pack2(l.z, l.w));
-                float y[4] = {ex2(lo2(u)), ex2(hi2(u)), ex2(lo2(v)), ex2(hi2(v))};
+                for (int e = 0; e < 32; e += 2) {
+                    const float4 l = *reinterpret_cast<const float4*>(nl + 2 * e);
+                    const F2 u = fma2((F2)s[2 * e + 1] << 32 | s[2 * e], cc, pack2(l.x, l.y));
+                    const F2 v = fma2((F2)s[2 * e + 3] << 32 | s[2 * e + 2], cc, pack2(l.z, l.w));
+                    s[2 * e] = __float_as_uint(ex2(lo2(u)));
+                    s[2 * e + 1] = __float_as_uint(ex2(hi2(u)));
+                    s[2 * e + 2] = __float_as_uint(ex2(lo2(v)));
+                    s[2 * e + 3] = __float_as_uint(ex2(hi2(v)));
+                }
                 if (mask) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (2 * e + k < from) y[k] = 0.0f;
+                    for (int e = 0; e < 64; ++e)
+                        if (e < from) s[e] = 0;
                 }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) s[2 * e + k] = __float_as_uint(y[k]);
-                p[e] = pack_bf16x2(y[0], y[1]);
-                p[e + 1] = pack_bf16x2(y[2], y[3]);
+                for (int e = 0; e < 32; ++e)
+                    p[e] = pack_bf16x2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+                tmem_store32(tmem + lanes + 64 * half, p);
+                tmem_wait_stores();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.p_full);
+                going = tc_wait_warp(&bar.g_full, s_par, lost);
+                s_par ^= 1;
+                if (!going) break;
+                tc_fence_after();
+                uint32_t g[64];
+                tmem_load32(tmem + lanes + 128 + 64 * half, g);
+                tmem_load32(tmem + lanes + 128 + 64 * half + 32, g + 32);
+                tmem_wait(g);
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const float4 l = *reinterpret_cast<const float4*>(nd + 2 * e);
+                    const F2 u = mul2((F2)s[2 * e + 1] << 32 | s[2 * e],
+                                      add2((F2)g[2 * e + 1] << 32 | g[2 * e], pack2(l.x, l.y)));
+                    const F2 v = mul2((F2)s[2 * e + 3] << 32 | s[2 * e + 2],
+                                      add2((F2)g[2 * e + 3] << 32 | g[2 * e + 2], pack2(l.z, l.w)));
+                    p[e] = pack_bf16x2(lo2(u), hi2(u));
+                    p[e + 1] = pack_bf16x2(lo2(v), hi2(v));
+                }
+                if (mask) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        p[e] = 2 * e >= from ? p[e] : 2 * e + 1 >= from ? p[e] & 0xffff0000u : 0u;
+                }
+                tmem_store32(tmem + lanes + 128 + 64 * half, p);
+                tmem_wait_stores();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.d_full);
+                i0 += kTcRows;
+                if (i0 >= m.nq) i0 = first;
             }
-            tmem_store32(tmem + lanes + 64 * half, p);
-            tmem_wait_stores();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.p_full);
-            going = tc_wait_warp(&bar.g_full, j & 1, lost);
+            if (going && n > 0) {
+                going = tc_wait_warp(&bar.o_full, o_par, lost);
+                o_par ^= 1;
+            }
             if (!going) break;
             tc_fence_after();
-            uint32_t g[64];
-            tmem_load32(tmem + lanes + 128 + 64 * half, g);
-            tmem_load32(tmem + lanes + 128 + 64 * half + 32, g + 32);
-            tmem_wait(g);
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-                const float4 l = *reinterpret_cast<const float4*>(nd + 2 * e);
-                F2 u = mul2((F2)s[2 * e + 1] << 32 | s[2 * e],
-                            add2((F2)g[2 * e + 1] << 32 | g[2 * e], pack2(l.x, l.y)));
-                F2 v = mul2((F2)s[2 * e + 3] << 32 | s[2 * e + 2],
-                            add2((F2)g[2 * e + 3] << 32 | g[2 * e + 2], pack2(l.z, l.w)));
-                p[e] = pack_bf16x2(lo2(u), hi2(u));
-                p[e + 1] = pack_bf16x2(lo2(v), hi2(v));
-            }
-            if (mask) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    p[e] = 2 * e >= from ? p[e] : 2 * e + 1 >= from ? p[e] & 0xffff0000u : 0u;
-            }
-            tmem_store32(tmem + lanes + 128 + 64 * half, p);
-            tmem_wait_stores();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.d_full);
-        }
-        if (going && n > 0) going = tc_wait_warp(&bar.s_full, n & 1, lost);
-        if (going) {
-            tc_fence_after();
             const int begin = half * BLOCKS * 32, cols = min(a.D - begin, BLOCKS * 32);
-            char* dv = live ? row_of(a.dv, t.k0 + row, hk) + 2 * begin : nullptr;
-            char* dk = live ? row_of(a.dk, t.k0 + row, hk) + 2 * begin : nullptr;
+            char* dv = live ? row_of(a.dv, m.k0 + row, m.head) + 2 * begin : nullptr;
+            char* dk = live ? row_of(a.dk, m.k0 + row, m.head) + 2 * begin : nullptr;
             if (n > 0) {
-                store_row<BLOCKS * 32>(tmem + lanes + kDv + begin, cols, 1.0f, dv, live,
-                                       wide_rows(a.dv), [] {});
-                store_row<BLOCKS * 32>(tmem + lanes + kDk + begin, cols, a.scale, dk, live,
-                                       wide_rows(a.dk), [] {});
+                store_row<BLOCKS * 32, 32>(tmem + lanes + kDv + begin, cols, 1.0f, dv, live, wide_v, [] {});
+                store_row<BLOCKS * 32, 32>(tmem + lanes + kDk + begin, cols, a.scale, dk, live, wide_k, [&] {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.o_free);
+                });
             } else {
                 zero_row(cols, dv, live);
                 zero_row(cols, dk, live);
             }
         }
+    } else {
+        set_registers_down<kOtherRegs>();
     }
     tc_finish(lost, tmem, warp == 9);
 }
@@ -1201,10 +1346,15 @@ cudaError_t launch_attn_tc_dq(const AttnArgs& a, cudaStream_t s)
     set_last_kernel_name("attn_grad_dq");
     Maps m;
     if (!grad_maps(&m, a)) return launch_attn_any_dq(a, s);
+    int sms = 0;
+    const cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
     return by_blocks(a.D, [&](auto n) {
         static SmemRaisedOn raised;
-        return launch_tc(k_attn_tc_dq<n>, raised, GradShape<n>::kBytes,
-                         tiles_bound(a.cu_q, a.Tq, a.B, kTcRows), a.Hq, kGradThreads, s, m, a);
+        const int64_t tiles = tiles_bound(a.cu_q, a.Tq, a.B, kTcRows);
+        const int64_t items = tiles * a.Hq;
+        return launch_tc(k_attn_tc_dq<n>, raised, GradShape<n>::kBytes, items < sms ? items : sms, 1,
+                         kGradThreads, s, m, a, (int)tiles, items);
     });
 }
 
@@ -1213,10 +1363,15 @@ cudaError_t launch_attn_tc_dkv(const AttnArgs& a, cudaStream_t s)
     set_last_kernel_name("attn_grad_dkv");
     Maps m;
     if (!grad_maps(&m, a)) return launch_attn_any_dkv(a, s);
+    int sms = 0;
+    const cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
     return by_blocks(a.D, [&](auto n) {
         static SmemRaisedOn raised;
-        return launch_tc(k_attn_tc_dkv<n>, raised, GradShape<n>::kBytes,
-                         tiles_bound(a.cu_k, a.Tk, a.B, kTcRows), a.Hk, kGradThreads, s, m, a);
+        const int64_t tiles = tiles_bound(a.cu_k, a.Tk, a.B, kTcRows);
+        const int64_t items = tiles * a.Hk;
+        return launch_tc(k_attn_tc_dkv<n>, raised, GradShape<n>::kBytes, items < sms ? items : sms, 1,
+                         kGradThreads, s, m, a, (int)tiles, items);
     });
 }
 
