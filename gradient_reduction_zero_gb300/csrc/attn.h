@@ -44,7 +44,7 @@ constexpr int kRopeParts = 1024;    // most partial sums of the weights' gradien
 DPZ_HD inline int64_t rope_part_tokens(int64_t T)
 {
     const int64_t n = (T + kRopeParts - 1) / kRopeParts;
-    return n < 1 ? 1 : n;
+    return n < 2 ? 2 : n;
 }
 DPZ_HD inline int64_t rope_parts(int64_t T)
 {

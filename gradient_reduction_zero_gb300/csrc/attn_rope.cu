@@ -12,10 +12,9 @@
 // head.  A group of lanes takes one token and several of its heads, and
 // computes the token's sines and cosines once for all of them.
 //
-// Angles: a position times a frequency is taken as a fraction of a turn in 64-bit
-// fixed point, whose product with an integer position wraps exactly: far
-// positions lose nothing, where a product in fp32 is off by whole radians at
-// 10^7.  The top 32 bits go to sincospi.
+// Angles: a frequency is taken as a fraction of a turn in 128-bit fixed point, whose
+// product with a 64-bit position wraps exactly: far positions lose nothing, where a
+// product in fp32 is off by whole radians at 10^7.  The top 32 bits go to sincospi.
 #include <cmath>
 #include <type_traits>
 
@@ -29,74 +28,68 @@ namespace dpz {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kHeadsPerItem = 8;    // heads that share a token's sines and cosines
 
-// A vector of V elements of type DT as fp32.
+// A vector of V elements of type DT: as it lies in memory, and as fp32.
 template <int DT, int V>
 struct Vec;
 
 template <>
 struct Vec<DPZ_F32, 1> {
-    static __device__ __forceinline__ void load(const char* p, float x[1])
-    {
-        x[0] = *reinterpret_cast<const float*>(p);
-    }
-    static __device__ __forceinline__ void store(char* p, const float x[1])
-    {
-        *reinterpret_cast<float*>(p) = x[0];
-    }
+    using Raw = float;
+    static __device__ __forceinline__ void unpack(const Raw& r, float x[1]) { x[0] = r; }
+    static __device__ __forceinline__ Raw pack(const float x[1]) { return x[0]; }
 };
 template <>
 struct Vec<DPZ_F32, 4> {
-    static __device__ __forceinline__ void load(const char* p, float x[4])
+    using Raw = float4;
+    static __device__ __forceinline__ void unpack(const Raw& r, float x[4])
     {
-        const float4 v = *reinterpret_cast<const float4*>(p);
-        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+        x[0] = r.x; x[1] = r.y; x[2] = r.z; x[3] = r.w;
     }
-    static __device__ __forceinline__ void store(char* p, const float x[4])
+    static __device__ __forceinline__ Raw pack(const float x[4])
     {
-        *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+        return make_float4(x[0], x[1], x[2], x[3]);
     }
 };
 template <>
 struct Vec<DPZ_BF16, 1> {
-    static __device__ __forceinline__ void load(const char* p, float x[1])
+    using Raw = uint16_t;
+    static __device__ __forceinline__ void unpack(const Raw& r, float x[1])
     {
-        x[0] = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(p) << 16);
+        x[0] = __uint_as_float((uint32_t)r << 16);
     }
-    static __device__ __forceinline__ void store(char* p, const float x[1])
+    static __device__ __forceinline__ Raw pack(const float x[1])
     {
-        *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(x[0]);
+        return (uint16_t)pack_bf16x2(x[0], 0.0f);
     }
 };
 template <>
 struct Vec<DPZ_BF16, 4> {
-    static __device__ __forceinline__ void load(const char* p, float x[4])
+    using Raw = uint2;
+    static __device__ __forceinline__ void unpack(const Raw& r, float x[4])
     {
-        const uint2 v = *reinterpret_cast<const uint2*>(p);
-        x[0] = bf16_lo(v.x); x[1] = bf16_hi(v.x);
-        x[2] = bf16_lo(v.y); x[3] = bf16_hi(v.y);
+        x[0] = bf16_lo(r.x); x[1] = bf16_hi(r.x);
+        x[2] = bf16_lo(r.y); x[3] = bf16_hi(r.y);
     }
-    static __device__ __forceinline__ void store(char* p, const float x[4])
+    static __device__ __forceinline__ Raw pack(const float x[4])
     {
-        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+        return make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
     }
 };
 template <>
 struct Vec<DPZ_BF16, 8> {
-    static __device__ __forceinline__ void load(const char* p, float x[8])
+    using Raw = uint4;
+    static __device__ __forceinline__ void unpack(const Raw& r, float x[8])
     {
-        const uint4 v = *reinterpret_cast<const uint4*>(p);
-        x[0] = bf16_lo(v.x); x[1] = bf16_hi(v.x);
-        x[2] = bf16_lo(v.y); x[3] = bf16_hi(v.y);
-        x[4] = bf16_lo(v.z); x[5] = bf16_hi(v.z);
-        x[6] = bf16_lo(v.w); x[7] = bf16_hi(v.w);
+        x[0] = bf16_lo(r.x); x[1] = bf16_hi(r.x);
+        x[2] = bf16_lo(r.y); x[3] = bf16_hi(r.y);
+        x[4] = bf16_lo(r.z); x[5] = bf16_hi(r.z);
+        x[6] = bf16_lo(r.w); x[7] = bf16_hi(r.w);
     }
-    static __device__ __forceinline__ void store(char* p, const float x[8])
+    static __device__ __forceinline__ Raw pack(const float x[8])
     {
-        *reinterpret_cast<uint4*>(p) =
-            make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                       pack_bf16x2(x[6], x[7]));
+        return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                          pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
     }
 };
 
@@ -140,30 +133,41 @@ __device__ __forceinline__ void slot_elems(const Cut& c, int slot, int D, bool i
     }
 }
 
-// inv_freq / (2 pi) modulo 1, in units of 2^-64 (rounded down): the mantissa
-// times 1 / (2 pi) in 128 bits, shifted by the exponent.
-__device__ __forceinline__ uint64_t turn_fraction(float f)
+// A fraction of a turn in units of 2^-128.
+struct Fraction {
+    uint64_t hi, lo;
+};
+
+// 64 bits of the number p from bit b on, 0 <= b.
+__device__ __forceinline__ uint64_t bits_from(const uint64_t p[4], int b)
 {
-    // floor(2^128 / (2 pi)), high and low words
-    const uint64_t hi = 0x28be60db9391054aull, lo = 0x7f09d5f47d4d3770ull;
+    const int i = b >> 6, r = b & 63;
+    const uint64_t x = i == 0 ? p[0] : i == 1 ? p[1] : i == 2 ? p[2] : i == 3 ? p[3] : 0;
+    const uint64_t y = i == 0 ? p[1] : i == 1 ? p[2] : i == 2 ? p[3] : 0;
+    return r == 0 ? x : x >> r | y << (64 - r);
+}
+
+// f / (2 pi) modulo 1, rounded towards 0: the mantissa times 1 / (2 pi) in 192 bits, shifted
+// by the exponent.
+__device__ __forceinline__ Fraction turn_fraction(float f)
+{
+    // floor(2^192 / (2 pi)), high word first
+    const uint64_t c2 = 0x28be60db9391054aull, c1 = 0x7f09d5f47d4d3770ull, c0 = 0x36d8a5664f10e410ull;
     const uint32_t b = __float_as_uint(f);
     const int ex = (int)(b >> 23 & 255);
     const uint64_t m = ex ? (b & 0x7fffff) | 0x800000 : b & 0x7fffff;
     const int e = (ex ? ex : 1) - 150;              // |f| = m 2^e
-    // p = m * (hi, lo): 152 bits in (p2, p1, p0)
-    const uint64_t p0 = m * lo;
-    const uint64_t c0 = __umul64hi(m, lo);
-    const uint64_t p1 = m * hi + c0;
-    const uint64_t p2 = __umul64hi(m, hi) + (p1 < c0);
-    // bits 64 - e and up of p, modulo 2^64
-    const int sh = 64 - e;                           // 64 - e >= 0 up to e = 64
-    uint64_t r = 0;
-    if (sh >= 128) r = sh < 192 ? p2 >> (sh - 128) : 0;
-    else if (sh > 64) r = p1 >> (sh - 64) | p2 << (128 - sh);
-    else if (sh == 64) r = p1;
-    else if (sh > 0) r = p0 >> sh | p1 << (64 - sh);
-    else if (sh > -64) r = p0 << -sh;
-    return b >> 31 ? 0 - r : r;
+    uint64_t p[4];
+    p[0] = m * c0;
+    const uint64_t h0 = __umul64hi(m, c0);
+    p[1] = m * c1 + h0;
+    const uint64_t h1 = __umul64hi(m, c1) + (p[1] < h0);
+    p[2] = m * c2 + h1;
+    p[3] = __umul64hi(m, c2) + (p[2] < h1);
+    const int sh = max(64 - e, 0);                  // |f| < 2^88 is exact
+    const uint64_t hi = bits_from(p, sh + 64), lo = bits_from(p, sh);
+    if (b >> 31) return {~hi + (lo == 0), 0 - lo};
+    return {hi, lo};
 }
 
 __device__ __forceinline__ int64_t position_of(const RopeArgs& a, int64_t t)
@@ -172,10 +176,11 @@ __device__ __forceinline__ int64_t position_of(const RopeArgs& a, int64_t t)
                               : (int64_t) static_cast<const int*>(a.positions)[t];
 }
 
-// Sine and cosine of position * frequency.
-__device__ __forceinline__ void turn_by(int64_t pos, uint64_t frac, float* s, float* c)
+// Sine and cosine of position * frequency: the product's top 64 bits of the turn's fraction.
+__device__ __forceinline__ void turn_by(int64_t pos, const Fraction& f, float* s, float* c)
 {
-    const uint64_t u = (uint64_t)pos * frac;
+    const uint64_t u = (uint64_t)pos * f.hi + __umul64hi((uint64_t)pos, f.lo) -
+                       (pos < 0 ? f.lo : 0);
     const float half_turns = (float)(int32_t)(u >> 32) * 0x1p-31f;   // in [-1, 1]
     sincospif(half_turns, s, c);
 }
@@ -203,7 +208,7 @@ __device__ __forceinline__ Part<V, NS> my_part(const Cut& c, int lane, const Rop
 // Neighbours: V / 2 in each vector, the identity past the rotated elements.
 template <int V, int NS>
 __device__ __forceinline__ void slot_turns(const Part<V, NS>& p, const RopeArgs& a,
-                                           const uint64_t* frac, int64_t t, float sn[NS][V],
+                                           const Fraction* frac, int64_t t, float sn[NS][V],
                                            float cs[NS][V])
 {
     const int64_t pos = a.positions ? position_of(a, t) : 0;
@@ -250,19 +255,32 @@ __device__ __forceinline__ void rotate(float x[2][V], const float sn[V], const f
     }
 }
 
+// A lane's part of a row as it lies in memory; zeros where it has none or `on` is false.
 template <int DT, int V, int NS>
-__device__ __forceinline__ void load_slots(const Part<V, NS>& p, const char* row, float x[NS][2][V])
-{
-    constexpr int ES = DT == DPZ_BF16 ? 2 : 4;
+struct RawSlots {
+    typename Vec<DT, V>::Raw r[NS][2];
+
+    __device__ __forceinline__ void load(const Part<V, NS>& p, const char* row, bool on)
+    {
+        constexpr int ES = DT == DPZ_BF16 ? 2 : 4;
 #pragma unroll
-    for (int s = 0; s < NS; ++s)
+        for (int s = 0; s < NS; ++s)
 #pragma unroll
-        for (int v = 0; v < 2; ++v)
-            if (p.e[s][v] >= 0) Vec<DT, V>::load(row + (int64_t)p.e[s][v] * ES, x[s][v]);
-            else
+            for (int v = 0; v < 2; ++v) {
+                r[s][v] = {};
+                if (on && p.e[s][v] >= 0)
+                    r[s][v] = *reinterpret_cast<const typename Vec<DT, V>::Raw*>(
+                        row + (int64_t)p.e[s][v] * ES);
+            }
+    }
+    __device__ __forceinline__ void unpack(float x[NS][2][V]) const
+    {
 #pragma unroll
-                for (int i = 0; i < V; ++i) x[s][v][i] = 0.0f;
-}
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+            for (int v = 0; v < 2; ++v) Vec<DT, V>::unpack(r[s][v], x[s][v]);
+    }
+};
 
 template <int DT, int V, int NS>
 __device__ __forceinline__ void store_slots(const Part<V, NS>& p, char* row, const float x[NS][2][V])
@@ -272,7 +290,9 @@ __device__ __forceinline__ void store_slots(const Part<V, NS>& p, char* row, con
     for (int s = 0; s < NS; ++s)
 #pragma unroll
         for (int v = 0; v < 2; ++v)
-            if (p.e[s][v] >= 0) Vec<DT, V>::store(row + (int64_t)p.e[s][v] * ES, x[s][v]);
+            if (p.e[s][v] >= 0)
+                *reinterpret_cast<typename Vec<DT, V>::Raw*>(row + (int64_t)p.e[s][v] * ES) =
+                    Vec<DT, V>::pack(x[s][v]);
 }
 
 template <int V, int NS>
@@ -307,176 +327,140 @@ __device__ __forceinline__ float dot(const float a[NS][2][V], const float b[NS][
     return s;
 }
 
-// Row of head h (queries' heads first, then keys') of token t.
-__device__ __forceinline__ char* head_row(const Heads* x, const RopeArgs& a, int64_t t, int h, int es)
+// Row of head h of token t.
+__device__ __forceinline__ char* head_row(const Heads& x, int64_t t, int h, int es)
 {
-    const int k = h >= a.H[0];
-    const Heads& m = x[k];
-    return m.p + (t * m.ld + (int64_t)(h - (k ? a.H[0] : 0)) * m.hs) * es;
+    return x.p + (t * x.ld + (int64_t)h * x.hs) * es;
 }
 
-__device__ __forceinline__ void fill_fractions(const RopeArgs& a, uint64_t* frac)
+__device__ __forceinline__ void fill_fractions(const RopeArgs& a, Fraction* frac)
 {
     for (int i = threadIdx.x; i < (a.positions ? a.R / 2 : 0); i += kRopeThreads)
         frac[i] = turn_fraction(a.inv_freq[i]);
     __syncthreads();
 }
 
-// An item is a token and kHeadsPerItem of the queries' or of the keys' heads.
-struct Items {
-    int per[2];     // items of a token among the queries' and the keys' heads
-    int64_t n;
-};
-
-__device__ __forceinline__ Items items_of(const RopeArgs& a, int64_t tokens)
-{
-    Items m;
-    m.per[0] = (a.H[0] + kHeadsPerItem - 1) / kHeadsPerItem;
-    m.per[1] = (a.H[1] + kHeadsPerItem - 1) / kHeadsPerItem;
-    m.n = tokens * (m.per[0] + m.per[1]);
-    return m;
-}
+// An item is a token and `per` of the queries' (blockIdx.y = 0) or of the keys' heads, which
+// share the token's sines and cosines; the next head's row is loaded while one is at work.
 
 template <int DT, int V, int NS>
-__global__ void __launch_bounds__(kRopeThreads) k_rope(RopeArgs a)
+__global__ void __launch_bounds__(kRopeThreads, 3) k_rope(const __grid_constant__ RopeArgs a, int per)
 {
     pdl_enter();
     constexpr int ES = DT == DPZ_BF16 ? 2 : 4;
-    __shared__ uint64_t frac[kRopeMaxD / 2];
+    __shared__ Fraction frac[kRopeMaxD / 2];
     fill_fractions(a, frac);
+    const int k = blockIdx.y, H = a.H[k];
     const Cut c = make_cut<V>(a.D, a.R, a.interleaved);
     const int lane = threadIdx.x & (c.lanes - 1);
     const Part<V, NS> p = my_part<V, NS>(c, lane, a);
-    const Items m = items_of(a, a.T);
+    const unsigned each = (unsigned)(H + per - 1) / (unsigned)per;
     const int64_t item = ((int64_t)blockIdx.x * kRopeThreads + threadIdx.x) / c.lanes;
-    const bool live = item < m.n;     // every lane takes part in the exchanges
-    const int each = m.per[0] + m.per[1];
+    const bool live = item < a.T * each;     // every lane takes part in the exchanges
     const int64_t t = live ? item / each : 0;
-    const int g = live ? (int)(item % each) : 0, k = g >= m.per[0];
-    const int h0 = (k ? g - m.per[0] : g) * kHeadsPerItem + (k ? a.H[0] : 0);
-    const int h1 = min(h0 + kHeadsPerItem, k ? a.H[0] + a.H[1] : a.H[0]);
+    const int h0 = live ? (int)(item - t * each) * per : 0;
+    const int n = live ? min(per, H - h0) : 0;
+    RawSlots<DT, V, NS> raw;
+    raw.load(p, head_row(a.in[k], t, h0, ES), n > 0);
     float sn[NS][V], cs[NS][V], w[NS][2][V];
-    slot_turns<V, NS>(p, a, frac, t, sn, cs);
     load_weights<V, NS>(p, a.w[k], a.wdt, w);
+    slot_turns<V, NS>(p, a, frac, t, sn, cs);
     const float inv = 1.0f / (float)a.D;
-    constexpr int kAtOnce = NS * V >= 8 ? 2 : 4;
-    for (int b = 0; b < kHeadsPerItem; b += kAtOnce) {
-        float x[kAtOnce][NS][2][V];
+    for (int b = 0; b < per; ++b) {
+        float x[NS][2][V];
+        raw.unpack(x);
+        raw.load(p, head_row(a.in[k], t, h0 + b + 1, ES), b + 1 < n);
+        const float r = rsqrtf(fmaf(dot<V, NS>(x, x, c.lanes), inv, a.eps));
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j)
-            if (live && h0 + b + j < h1)
-                load_slots<DT, V, NS>(p, head_row(a.in, a, t, h0 + b + j, ES), x[j]);
-            else
+        for (int s = 0; s < NS; ++s) {
 #pragma unroll
-                for (int i = 0; i < NS * 2 * V; ++i) (&x[j][0][0][0])[i] = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-            const float r = rsqrtf(fmaf(dot<V, NS>(x[j], x[j], c.lanes), inv, a.eps));
-#pragma unroll
-            for (int s = 0; s < NS; ++s) {
-#pragma unroll
-                for (int i = 0; i < 2 * V; ++i) (&x[j][s][0][0])[i] *= r * (&w[s][0][0])[i];
-                rotate<V>(x[j][s], sn[s], cs[s], a.interleaved, 1.0f);
-            }
-            if (live && h0 + b + j < h1)
-                store_slots<DT, V, NS>(p, head_row(a.out, a, t, h0 + b + j, ES), x[j]);
+            for (int i = 0; i < 2 * V; ++i) (&x[s][0][0])[i] *= r * (&w[s][0][0])[i];
+            rotate<V>(x[s], sn[s], cs[s], a.interleaved, 1.0f);
         }
+        if (b < n) store_slots<DT, V, NS>(p, head_row(a.out[k], t, h0 + b, ES), x);
     }
 }
 
-// One block per part of the tokens; each group of lanes walks the part's items
-// and keeps the weights' gradients of its slot, which are joined in the
-// order of the groups at the end.
+// One block per part of the tokens, for the queries and for the keys; each group of lanes
+// walks the part's items and keeps the weights' gradient of its slot, which are
+// joined in the order of the groups at the end.
 template <int DT, int V, int NS>
-__global__ void __launch_bounds__(kRopeThreads) k_rope_grad(RopeArgs a)
+__global__ void __launch_bounds__(kRopeThreads, 2)
+k_rope_grad(const __grid_constant__ RopeArgs a, int per)
 {
     pdl_enter();
     constexpr int ES = DT == DPZ_BF16 ? 2 : 4;
-    __shared__ uint64_t frac[kRopeMaxD / 2];
-    __shared__ float joined[kRopeThreads / 32][2][kRopeMaxD];
+    __shared__ Fraction frac[kRopeMaxD / 2];
+    __shared__ float joined[kRopeThreads / 32][kRopeMaxD];
     fill_fractions(a, frac);
+    const int k = blockIdx.y, H = a.H[k];
     const Cut c = make_cut<V>(a.D, a.R, a.interleaved);
-    const int lane = threadIdx.x & (c.lanes - 1);
+    const int lane = threadIdx.x & (c.lanes - 1), groups = kRopeThreads / c.lanes;
     const Part<V, NS> p = my_part<V, NS>(c, lane, a);
-    const int64_t per = rope_part_tokens(a.T), t0 = blockIdx.x * per;
-    const Items m = items_of(a, min(per, a.T - t0));
-    const int each = m.per[0] + m.per[1], groups = kRopeThreads / c.lanes;
+    const int64_t tokens = rope_part_tokens(a.T), t0 = blockIdx.x * tokens;
+    const unsigned each = (unsigned)(H + per - 1) / (unsigned)per;
+    const int items = (int)min(tokens, a.T - t0) * (int)each;
     const float inv = 1.0f / (float)a.D;
-    float dw[2][NS][2][V] = {};
+    float w[NS][2][V], dw[NS][2][V] = {};
+    load_weights<V, NS>(p, a.w[k], a.wdt, w);
     // whole warps go round the loop together
-    for (int64_t base = 0; base < m.n; base += groups) {
-        const int64_t item = base + threadIdx.x / c.lanes;
-        const bool live = item < m.n;
-        const int64_t t = t0 + (live ? item / each : 0);
-        const int g = live ? (int)(item % each) : 0, k = g >= m.per[0];
-        const int h0 = (k ? g - m.per[0] : g) * kHeadsPerItem + (k ? a.H[0] : 0);
-        const int h1 = min(h0 + kHeadsPerItem, k ? a.H[0] + a.H[1] : a.H[0]);
-        float sn[NS][V], cs[NS][V], w[NS][2][V];
+    for (int base = 0; base < items; base += groups) {
+        const int item = base + (int)threadIdx.x / c.lanes;
+        const bool live = item < items;
+        const int64_t t = t0 + (live ? (int)((unsigned)item / each) : 0);
+        const int h0 = live ? (int)((unsigned)item % each) * per : 0;
+        const int n = live ? min(per, H - h0) : 0;
+        RawSlots<DT, V, NS> rx, rd;
+        rx.load(p, head_row(a.in[k], t, h0, ES), n > 0);
+        rd.load(p, head_row(a.dout[k], t, h0, ES), n > 0);
+        float sn[NS][V], cs[NS][V];
         slot_turns<V, NS>(p, a, frac, t, sn, cs);
-        load_weights<V, NS>(p, a.w[k], a.wdt, w);
-        constexpr int kAtOnce = 2;
-        for (int b = 0; b < kHeadsPerItem; b += kAtOnce) {
-            float x[kAtOnce][NS][2][V], d[kAtOnce][NS][2][V];
+        for (int b = 0; b < per; ++b) {
+            float x[NS][2][V], d[NS][2][V];
+            rx.unpack(x);
+            rd.unpack(d);
+            rx.load(p, head_row(a.in[k], t, h0 + b + 1, ES), b + 1 < n);
+            rd.load(p, head_row(a.dout[k], t, h0 + b + 1, ES), b + 1 < n);
+            const float r = rsqrtf(fmaf(dot<V, NS>(x, x, c.lanes), inv, a.eps));
 #pragma unroll
-            for (int j = 0; j < kAtOnce; ++j)
-                if (live && h0 + b + j < h1) {
-                    load_slots<DT, V, NS>(p, head_row(a.in, a, t, h0 + b + j, ES), x[j]);
-                    load_slots<DT, V, NS>(p, head_row(a.dout, a, t, h0 + b + j, ES), d[j]);
-                } else {
+            for (int s = 0; s < NS; ++s) {
+                rotate<V>(d[s], sn[s], cs[s], a.interleaved, -1.0f);
 #pragma unroll
-                    for (int i = 0; i < NS * 2 * V; ++i)
-                        (&x[j][0][0][0])[i] = (&d[j][0][0][0])[i] = 0.0f;
+                for (int i = 0; i < 2 * V; ++i) {
+                    const float y = (&x[s][0][0])[i] *= r;
+                    float& g = (&d[s][0][0])[i];
+                    (&dw[s][0][0])[i] = fmaf(g, y, (&dw[s][0][0])[i]);
+                    g *= (&w[s][0][0])[i];
                 }
-#pragma unroll
-            for (int j = 0; j < kAtOnce; ++j) {
-                const float r = rsqrtf(fmaf(dot<V, NS>(x[j], x[j], c.lanes), inv, a.eps));
-#pragma unroll
-                for (int s = 0; s < NS; ++s) {
-                    rotate<V>(d[j][s], sn[s], cs[s], a.interleaved, -1.0f);
-#pragma unroll
-                    for (int i = 0; i < 2 * V; ++i) {
-                        const float n = (&x[j][s][0][0])[i] *= r;
-                        float& g1 = (&d[j][s][0][0])[i];
-                        float& sum0 = (&dw[0][s][0][0])[i];
-                        float& sum1 = (&dw[1][s][0][0])[i];
-                        sum0 = fmaf(k ? 0.0f : g1, n, sum0);
-                        sum1 = fmaf(k ? g1 : 0.0f, n, sum1);
-                        g1 *= (&w[s][0][0])[i];
-                    }
-                }
-                const float mean = dot<V, NS>(x[j], d[j], c.lanes) * inv;
-#pragma unroll
-                for (int s = 0; s < NS; ++s)
-#pragma unroll
-                    for (int i = 0; i < 2 * V; ++i)
-                        (&d[j][s][0][0])[i] = r * fmaf(-mean, (&x[j][s][0][0])[i], (&d[j][s][0][0])[i]);
-                if (live && h0 + b + j < h1)
-                    store_slots<DT, V, NS>(p, head_row(a.out, a, t, h0 + b + j, ES), d[j]);
             }
+            const float mean = dot<V, NS>(x, d, c.lanes) * inv;
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+#pragma unroll
+                for (int i = 0; i < 2 * V; ++i)
+                    (&d[s][0][0])[i] = r * fmaf(-mean, (&x[s][0][0])[i], (&d[s][0][0])[i]);
+            if (b < n) store_slots<DT, V, NS>(p, head_row(a.out[k], t, h0 + b, ES), d);
         }
     }
     if (a.dw[0] == nullptr && a.dw[1] == nullptr) return;
     // the groups of a warp, then the warps, in a fixed order
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int s = 0; s < NS; ++s)
 #pragma unroll
-        for (int s = 0; s < NS; ++s)
+        for (int v = 0; v < 2; ++v)
 #pragma unroll
-            for (int v = 0; v < 2; ++v)
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    float y = dw[k][s][v][i];
-                    for (int o = c.lanes; o < 32; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-                    if ((threadIdx.x & 31) < c.lanes && p.e[s][v] >= 0)
-                        joined[threadIdx.x >> 5][k][p.e[s][v] + i] = y;
-                }
+            for (int i = 0; i < V; ++i) {
+                float y = dw[s][v][i];
+                for (int o = c.lanes; o < 32; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+                if ((threadIdx.x & 31) < c.lanes && p.e[s][v] >= 0)
+                    joined[threadIdx.x >> 5][p.e[s][v] + i] = y;
+            }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * a.D; i += kRopeThreads) {
-        const int k = i >= a.D, d = k ? i - a.D : i;
+    for (int i = threadIdx.x; i < a.D; i += kRopeThreads) {
         float y = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kRopeThreads / 32; ++w) y += joined[w][k][d];
-        a.partial[(int64_t)blockIdx.x * 2 * a.D + i] = y;
+        for (int w = 0; w < kRopeThreads / 32; ++w) y += joined[w][i];
+        a.partial[((int64_t)blockIdx.x * 2 + k) * a.D + i] = y;
     }
 }
 
@@ -552,16 +536,26 @@ cudaError_t by_vector(const RopeArgs& a, bool grad, F&& f)
 
 }  // namespace
 
+// Heads of an item, by sizes alone (the sums' order follows it): up to 16, fewer while
+// the items would leave most of the GPU without work.
+int heads_of_item(int64_t tokens, int H, int lanes, int64_t threads)
+{
+    int per = 16;
+    while (per > 1 && tokens * ((H + per - 1) / per) * lanes < threads) per /= 2;
+    return per;
+}
+
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s)
 {
     set_last_kernel_name("attn_qk_norm_rope");
     return by_vector(a, false, [&](auto dt, auto v, auto ns) {
         const Cut c = make_cut<v>(a.D, a.R, a.interleaved);
-        const int64_t each = (a.H[0] + kHeadsPerItem - 1) / kHeadsPerItem +
-                             (a.H[1] + kHeadsPerItem - 1) / kHeadsPerItem;
-        const int64_t threads = a.T * each * c.lanes;
+        const int H = a.H[0] > a.H[1] ? a.H[0] : a.H[1];
+        const int per = heads_of_item(a.T, H, c.lanes, 152 * 768);
+        const int64_t threads = a.T * ((H + per - 1) / per) * c.lanes;
         const unsigned blocks = (unsigned)((threads + kRopeThreads - 1) / kRopeThreads);
-        return launch_kernel(k_rope<dt, v, ns>, dim3(blocks), dim3(kRopeThreads), 0, s, true, 0u, a);
+        return launch_kernel(k_rope<dt, v, ns>, dim3(blocks, a.H[1] > 0 ? 2 : 1), dim3(kRopeThreads),
+                             0, s, true, 0u, a, per);
     });
 }
 
@@ -569,8 +563,11 @@ cudaError_t launch_rope_grad(const RopeArgs& a, cudaStream_t s)
 {
     set_last_kernel_name("attn_qk_norm_rope_grad");
     return by_vector(a, true, [&](auto dt, auto v, auto ns) {
-        return launch_kernel(k_rope_grad<dt, v, ns>, dim3((unsigned)rope_parts(a.T)),
-                             dim3(kRopeThreads), 0, s, true, 0u, a);
+        const Cut c = make_cut<v>(a.D, a.R, a.interleaved);
+        const int H = a.H[0] > a.H[1] ? a.H[0] : a.H[1];
+        const int per = heads_of_item(rope_part_tokens(a.T), H, c.lanes, kRopeThreads);
+        return launch_kernel(k_rope_grad<dt, v, ns>, dim3((unsigned)rope_parts(a.T), 2),
+                             dim3(kRopeThreads), 0, s, true, 0u, a, per);
     });
 }
 
