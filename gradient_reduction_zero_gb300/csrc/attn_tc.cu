@@ -165,6 +165,7 @@ struct Item {
     int64_t q0, k0;
     int nq, nk, row0, head;
     int tiles[2];      // of the other axis, for each tile of the block; [0] < 0: no more items
+    int first;         // the first of them (forward)
 };
 
 constexpr int kRing = 4;
@@ -218,7 +219,7 @@ __device__ __forceinline__ bool ring_take(Ring& r, Turn<kRing>& turn, Item& item
     if (!tc_wait_warp(&r.full[turn.at], turn.parity, lost)) return false;
     const Item& x = r.item[turn.at];
     item = {x.q0, x.k0, uniform(x.nq), uniform(x.nk), uniform(x.row0), uniform(x.head),
-            {uniform(x.tiles[0]), uniform(x.tiles[1])}};
+            {uniform(x.tiles[0]), uniform(x.tiles[1])}, uniform(x.first)};
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&r.empty[turn.at]);
     turn.next();
@@ -263,7 +264,7 @@ struct FwdShape {
 struct FwdBars {
     Ring ring;
     uint64_t q_full[2], q_empty[2], k_full[3], k_empty[3], v_full[3], v_empty[3];
-    uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
+    uint64_t s_full[2], p_full[2], o_done[2], o_free[2], parts_done;
     uint32_t tmem;
     int lost;
 };
@@ -341,10 +342,109 @@ __device__ __forceinline__ void tile_exp(uint32_t at, int most, F2 cc, F2 mm, F2
     }
 }
 
+// Few queries against many keys: the blocks of a cluster have parts of the keys, and leave
+// each row's unscaled output, shift and sum in their shared memory (where the operands
+// were); then each block joins its share of the rows.  Rows are 4 floats apart from
+// multiples of the banks.
 template <int BLOCKS>
+struct SplitShape {
+    static constexpr int kStride = 64 * BLOCKS + 4;
+    static constexpr int kStats = 256 * kStride * 4;    // bytes before 256 shifts and 256 sums
+    static_assert(kStats + 2048 <= FwdShape<BLOCKS>::kBars, "within the operands' place");
+};
+
+template <int BLOCKS>
+__device__ __forceinline__ void split_put(char* smem, int row, uint32_t o_at, int tiles, float shift,
+                                          float sum, uint64_t* done, volatile int* lost)
+{
+    using P = SplitShape<BLOCKS>;
+    // both tiles' products have read the operands (each warp has waited for its tile's)
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(done);
+    if (!tc_wait_warp(done, 0, lost)) tiles = -1;
+    float* o = reinterpret_cast<float*>(smem) + row * P::kStride;
+    float* stats = reinterpret_cast<float*>(smem + P::kStats);
+    stats[row] = shift;
+    stats[256 + row] = tiles < 0 ? __int_as_float(0x7fc00000) : tiles > 0 ? sum : 0.0f;
+    if (tiles <= 0) return;
+    tc_fence_after();
+#pragma unroll
+    for (int c = 0; c < 64 * BLOCKS; c += 32) {
+        uint32_t r[32];
+        tmem_load32(o_at + c, r);
+        tmem_wait(r);
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<uint4*>(o + c + e) = make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
+    }
+}
+
+// A float of another block of the cluster, by its address in this one.
+__device__ __forceinline__ float of_block(const float* p, int block)
+{
+    uint32_t at;
+    float x;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(block));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+    return x;
+}
+
+template <int BLOCKS>
+__device__ __forceinline__ void split_join(char* smem, const Ring& ring, const AttnArgs& a,
+                                           const Packing& pk, int parts)
+{
+    using P = SplitShape<BLOCKS>;
+    cluster_arrive_release();
+    cluster_wait();
+    const Item& m = ring.item[0];
+    const int lane = threadIdx.x & 31, rank = (int)blockIdx.x % parts;
+    const float* o = reinterpret_cast<const float*>(smem);
+    const float* stats = reinterpret_cast<const float*>(smem + P::kStats);
+    for (int at = rank * (kFwdThreads / 32) + (int)(threadIdx.x >> 5); m.tiles[0] >= 0 && at < 256;
+         at += parts * (kFwdThreads / 32)) {
+        const int i = at >> 7, r = at & 127, row = m.row0 + i * pk.tokens + r / pk.heads;
+        if (r >= pk.heads * pk.tokens || row >= m.nq) continue;
+        // lane c has part c's shift and sum (a NaN sum takes part)
+        float shift = -INFINITY, sum = 0.0f;
+        if (lane < parts) {
+            sum = of_block(stats + 256 + at, lane);
+            if (sum != 0.0f) shift = of_block(stats + at, lane);
+        }
+        float top = shift;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+        const float weight = sum != 0.0f ? ex2(shift - top) : 0.0f;
+        float total = sum * weight;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) total += __shfl_xor_sync(0xffffffffu, total, k);
+        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+        float y[2 * BLOCKS] = {};
+        for (int c = 0; c < parts; ++c) {
+            const float k = __shfl_sync(0xffffffffu, weight, c);
+            if (k == 0.0f) continue;
+#pragma unroll
+            for (int e = 0; e < 2 * BLOCKS; ++e)
+                if (lane + 32 * e < a.D)
+                    y[e] = fmaf(of_block(o + at * P::kStride + lane + 32 * e, c), k, y[e]);
+        }
+        const int head = m.head + r % pk.heads;
+        __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(row_of(a.out, m.q0 + row, head));
+#pragma unroll
+        for (int e = 0; e < 2 * BLOCKS; ++e)
+            if (lane + 32 * e < a.D) out[lane + 32 * e] = __float2bfloat16_rn(y[e] * inv);
+        if (a.lse != nullptr && lane == 0)
+            a.lse[(int64_t)head * a.Tq + m.q0 + row] =
+                total == 0.0f ? -INFINITY : (top + log2f(total)) * kLn2;
+    }
+    // no block leaves while another may read from it
+    cluster_arrive_release();
+    cluster_wait();
+}
+
+template <int BLOCKS, bool SPLIT>
 __global__ void __launch_bounds__(kFwdThreads, 1)
 k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a, Packing pk,
-          int pairs, int64_t items)
+          int pairs, int64_t items, int parts)
 {
     using S = FwdShape<BLOCKS>;
     extern __shared__ char smem_raw[];
@@ -353,6 +453,8 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         ring_init(bar.ring, 9);
+        bar.ring.item[0].tiles[0] = -1;
+        mbar_init(&bar.parts_done, 8);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.q_full[i], 1);
             mbar_init(&bar.q_empty[i], 1);
@@ -394,12 +496,14 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
         Turn<S::kStages> kt;
         bool going = true;
         Item m{};
-        for (int64_t w = blockIdx.x; w < items && going; w += gridDim.x) {
+        // in parts: one item for the blocks of a cluster
+        for (int64_t w = SPLIT ? blockIdx.x / parts : blockIdx.x; w < items && going;
+             w += gridDim.x) {
             // the tiles at the end of a sequence see the most keys and go first
             const int tile = (int)(w / groups);
             const Tile t = find_tile(a, pairs - 1 - tile, 2 * pk.tokens, false);
             if (!t.any) continue;
-            m = {t.q0, t.k0, t.nq, t.nk, t.row0, (int)(w - (int64_t)tile * groups) * pk.heads, {0, 0}};
+            m = {t.q0, t.k0, t.nq, t.nk, t.row0, (int)(w - (int64_t)tile * groups) * pk.heads, {0, 0}, 0};
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int row0 = t.row0 + i * pk.tokens;
@@ -407,6 +511,13 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
                                 : !a.causal  ? t.nk
                                              : max(0, min(t.nk, min(row0 + pk.tokens, t.nq) + t.nk - t.nq));
                 m.tiles[i] = (end + kTcRows - 1) / kTcRows;
+            }
+            if (SPLIT) {
+                const int all = max(m.tiles[0], m.tiles[1]), each = (all + parts - 1) / parts;
+                m.first = min(all, (int)(blockIdx.x % parts) * each);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    m.tiles[i] = max(0, min(m.tiles[i], m.first + each) - m.first);
             }
             going = ring_put(bar.ring, turn, m, lost);
             const int n = max(m.tiles[0], m.tiles[1]);
@@ -428,13 +539,13 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
                     mbar_expect_tx(&bar.k_full[kt.at], S::kTile);
                     for (int b = 0; b < BLOCKS; ++b)
                         tma_load(smem + S::kK + kt.at * S::kTile + b * kTcBlock, &maps.k,
-                                 &bar.k_full[kt.at], b * kTcCols, hk, (int)m.k0 + j * kTcRows);
+                                 &bar.k_full[kt.at], b * kTcCols, hk, (int)m.k0 + (m.first + j) * kTcRows);
                     going = tc_wait(&bar.v_empty[kt.at], kt.parity ^ 1, lost);
                     if (!going) break;
                     mbar_expect_tx(&bar.v_full[kt.at], S::kTile);
                     for (int b = 0; b < BLOCKS; ++b)
                         tma_load(smem + S::kV + kt.at * S::kTile + b * kTcBlock, &maps.v,
-                                 &bar.v_full[kt.at], b * kTcCols, hk, (int)m.k0 + j * kTcRows);
+                                 &bar.v_full[kt.at], b * kTcCols, hk, (int)m.k0 + (m.first + j) * kTcRows);
                     kt.next();
                 }
             }
@@ -483,7 +594,7 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
                 going = going && tc_wait_warp(&bar.v_full[vt.at], vt.parity, lost);
                 if (!going) break;
                 char* v = smem + S::kV + vt.at * S::kTile;
-                const int rows = m.nk - j * kTcRows;
+                const int rows = m.nk - (m.first + j) * kTcRows;
                 if (rows < kTcRows) {
                     clear_rows(v, rows, BLOCKS);
                     fence_async_proxy();
@@ -549,7 +660,7 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
                 s_par ^= 1;
                 if (!going) break;
                 tc_fence_after();
-                const int most = seen - j * kTcRows;     // columns below it are visible
+                const int most = seen - (m.first + j) * kTcRows;     // columns below it are visible
                 const bool edge = __any_sync(0xffffffffu, most < kTcRows);
                 uint32_t p[64];
                 F2 part[2];
@@ -595,6 +706,11 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
             }
             if (going && tiles > 0) going = tc_wait_warp(&bar.o_done[i], o_par ^ 1, lost);
             const float total = lo2(sum) + hi2(sum);
+            if (SPLIT) {
+                split_put<BLOCKS>(smem, i * 128 + r, o_at, going ? tiles : -1, shift, total,
+                                  &bar.parts_done, lost);
+                continue;
+            }
             char* out = live ? row_of(a.out, m.q0 + row, head) : nullptr;
             if (going && tiles > 0) {
                 tc_fence_after();
@@ -615,6 +731,7 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
     } else {
         set_registers_down<kOtherRegs>();
     }
+    if (SPLIT) split_join<BLOCKS>(smem, bar.ring, a, pk, parts);
     tc_finish(lost, tmem, warp == 9);
 }
 
@@ -633,7 +750,8 @@ constexpr int kGradThreads = 384;   // 8 compute warps, loads, products, two idl
 struct GradBars {
     Ring ring;
     uint64_t once_full[2], once_empty[2], in_full[3], in_empty[3];
-    uint64_t s_full, s_free, g_full, p_full, d_full, d_free, o_full, o_free;
+    uint64_t s_full, s_free, g_full, p_full, d_full, d_free, o_full, o_free,
+        rows_full;
     uint32_t tmem;
     int lost;
 };
@@ -674,6 +792,7 @@ __device__ __forceinline__ uint32_t grad_start(GradBars& bar, const Maps& maps, 
         mbar_init(&bar.d_free, 1);
         mbar_init(&bar.o_full, 1);
         mbar_init(&bar.o_free, 8);
+        mbar_init(&bar.rows_full, 8);
         bar.lost = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         tma_prefetch(&maps.q);
@@ -830,7 +949,7 @@ k_attn_tc_dq(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs
         const float c2 = a.scale * kLog2e;
         const F2 cc = pack2(c2, c2);
         const bool wide = wide_rows(a.dq);
-        uint32_t s_par = 0, d_par = 0;
+        uint32_t s_par = 0, d_par = 0, r_par = 0;
         bool going = true;
         Item m;
         while (going && ring_take(bar.ring, turn, m, lost)) {
@@ -873,7 +992,11 @@ k_attn_tc_dq(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs
                         a.delta[(int64_t)m.head * a.Tq + m.q0 + m.row0 + rr] = part[q];
                 }
             }
-            asm volatile("bar.sync 1, 256;" ::: "memory");    // the compute warps
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.rows_full);
+            going = tc_wait_warp(&bar.rows_full, r_par, lost);    // of all compute warps
+            r_par ^= 1;
+            if (!going) break;
             const float delta = delta_s[r];
             delta_s = reinterpret_cast<float*>(smem + S::kRows) +
                       (delta_s == reinterpret_cast<float*>(smem + S::kRows) ? 128 : 0);
@@ -1284,12 +1407,12 @@ Packing packing_of(const AttnArgs& a)
 
 template <class Kernel, class... Args>
 cudaError_t launch_tc(Kernel fn, SmemRaisedOn& raised, size_t smem, int64_t blocks, int heads,
-                      int threads, cudaStream_t s, Args... args)
+                      int threads, cudaStream_t s, unsigned cluster, Args... args)
 {
     const cudaError_t e = raise_smem(raised, reinterpret_cast<const void*>(fn), smem);
     if (e != cudaSuccess) return e;
     return launch_kernel(fn, dim3((unsigned)blocks, (unsigned)heads), dim3(threads), smem, s, true,
-                         0u, args...);
+                         cluster, args...);
 }
 
 template <class F>
@@ -1324,8 +1447,17 @@ cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t s)
         static SmemRaisedOn raised;
         const int64_t pairs = tiles_bound(a.cu_q, a.Tq, a.B, 2 * pk.tokens);
         const int64_t items = pairs * (a.Hq / pk.heads);
-        return launch_tc(k_attn_tc<n>, raised, FwdShape<n>::kBytes, items < sms ? items : sms, 1,
-                         kFwdThreads, s, m, a, pk, (int)pairs, items);
+        // few items with many keys each: up to eight blocks share one (16 queries
+        // of 32 + 8 heads of 128 against 8,191 keys: 20 us, 87 with one block)
+        int parts = 1;
+        while (parts < 8 && items * parts * 2 <= sms && a.len_k >= parts * 4 * kTcRows) parts *= 2;
+        if (parts > 1) {
+            static SmemRaisedOn split_raised;
+            return launch_tc(k_attn_tc<n, true>, split_raised, FwdShape<n>::kBytes, items * parts, 1,
+                             kFwdThreads, s, (unsigned)parts, m, a, pk, (int)pairs, items, parts);
+        }
+        return launch_tc(k_attn_tc<n, false>, raised, FwdShape<n>::kBytes, items < sms ? items : sms, 1,
+                         kFwdThreads, s, 0u, m, a, pk, (int)pairs, items, 1);
     });
 }
 
@@ -1354,7 +1486,7 @@ cudaError_t launch_attn_tc_dq(const AttnArgs& a, cudaStream_t s)
         const int64_t tiles = tiles_bound(a.cu_q, a.Tq, a.B, kTcRows);
         const int64_t items = tiles * a.Hq;
         return launch_tc(k_attn_tc_dq<n>, raised, GradShape<n>::kBytes, items < sms ? items : sms, 1,
-                         kGradThreads, s, m, a, (int)tiles, items);
+                         kGradThreads, s, 0u, m, a, (int)tiles, items);
     });
 }
 
@@ -1371,7 +1503,7 @@ cudaError_t launch_attn_tc_dkv(const AttnArgs& a, cudaStream_t s)
         const int64_t tiles = tiles_bound(a.cu_k, a.Tk, a.B, kTcRows);
         const int64_t items = tiles * a.Hk;
         return launch_tc(k_attn_tc_dkv<n>, raised, GradShape<n>::kBytes, items < sms ? items : sms, 1,
-                         kGradThreads, s, m, a, (int)tiles, items);
+                         kGradThreads, s, 0u, m, a, (int)tiles, items);
     });
 }
 

@@ -334,3 +334,23 @@ def test_without_tokens(dpz):
         run(dpz, x, True)
         x = make(0, 0, 2, 1, 64, dt, 1)
         run(dpz, x, False)
+
+
+@pytest.mark.parametrize("nq,nk,Hq,Hk,D", [(1, 5000, 1, 1, 64), (16, 8191, 8, 2, 128), (1, 2049, 7, 1, 80),
+                                           (300, 4100, 2, 2, 64), (129, 3000, 4, 4, 128), (1, 20000, 32, 1, 128)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_few_queries_and_many_keys(dpz, nq, nk, Hq, Hk, D, causal):
+    """Keys in parts for the blocks of a cluster."""
+    x = make(nq, nk, Hq, Hk, D, "bf16", nk)
+    run(dpz, x, causal, backward=False)
+
+
+def test_few_queries_of_packed_sequences(dpz):
+    """Lengths whose parts are empty for some blocks, or all; a sharp row in a late part."""
+    k = [0, 4000, 4000, 4001, 4130, 9000]
+    q = [0, 1, 3, 5, 6, 9]
+    x = make(q[-1], k[-1], 4, 2, 64, "bf16", 3)
+    x["k"].t[8000] *= 60
+    cu = tuple(torch.tensor(c, dtype=torch.int32, device="cuda") for c in (q, k))
+    run(dpz, x, True, cu=cu, backward=False)
+    run(dpz, x, False, cu=cu, backward=False)
