@@ -25,7 +25,8 @@ SOURCES = ["api.cpp", "reduce.cu", "adamw.cu", "staged.cu", "norm_static.cu", "l
            "attn_any.cu", "attn_tc.cu", "tensors_api.cpp", "tensors.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("internal.h", "api_util.h", "api_check.h", "lm.h",
                                           "lm_shape.h", "lm_rows.cuh", "device.cuh", "bulk.cuh",
-                                          "attn.h", "tc.cuh", "tensors.h")] + \
+                                          "attn.h", "pairs.cuh", "tc.cuh",
+                                          "tensors.h")] + \
     [os.path.join(INCLUDE, "dpz.h")]
 
 NVCC_FLAGS = [

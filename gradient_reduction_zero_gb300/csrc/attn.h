@@ -38,7 +38,7 @@ struct RopeArgs {
 };
 
 constexpr int kRopeMaxD = 256;
-constexpr int kRopeParts = 1024;    // most partial sums of the weights' gradients
+constexpr int kRopeParts = 304;     // most partial sums of the weights' gradients
 
 // Tokens of one partial sum of the weights' gradients, and how many there are.
 DPZ_HD inline int64_t rope_part_tokens(int64_t T)

@@ -17,6 +17,7 @@
 #include "bulk.cuh"
 #include "device.cuh"
 #include "lm_shape.h"
+#include "pairs.cuh"
 #include "tc.cuh"
 
 namespace dpz {
@@ -33,35 +34,6 @@ __device__ __forceinline__ float ex2(float u)
     float e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(u));
     return e;
-}
-
-// Paired fp32 operations, one instruction for two.
-using F2 = uint64_t;
-__device__ __forceinline__ F2 pack2(float lo, float hi)
-{
-    F2 d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-    return d;
-}
-__device__ __forceinline__ float lo2(F2 a) { return __uint_as_float((uint32_t)a); }
-__device__ __forceinline__ float hi2(F2 a) { return __uint_as_float((uint32_t)(a >> 32)); }
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
-{
-    F2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b)
-{
-    F2 d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b)
-{
-    F2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
 }
 
 // The end of a block: after a wait that ran out, time for what is in flight.

@@ -139,22 +139,26 @@ k_tensors_sumsq(const __grid_constant__ List<CAP> l, double* __restrict__ partia
     if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
-constexpr int kListFinalThreads = 512;
+constexpr int kListFinalThreads = 1024;
+constexpr int kListChains = 16;
 
-// sqrt of the sum of n partials, thread t taking t, t + 512, ... in turn.
+// sqrt of the sum of n partials, thread t taking t, t + 1024, ... in 16 chains.
 __global__ void __launch_bounds__(kListFinalThreads)
 k_tensors_norm(const double* __restrict__ partial, int64_t n, float* norm_out)
 {
     pdl_enter();
-    double s[8] = {};
-    for (int64_t i = threadIdx.x; i < n; i += 8 * kListFinalThreads)
+    double s[kListChains] = {};
+    for (int64_t i = threadIdx.x; i < n; i += kListChains * kListFinalThreads)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < kListChains; ++k) {
             const int64_t at = i + k * kListFinalThreads;
             if (at < n) s[k] += partial[at];
         }
-    const double sum =
-        block_sum(((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7])));
+#pragma unroll
+    for (int o = kListChains / 2; o > 0; o /= 2)
+#pragma unroll
+        for (int k = 0; k < o; ++k) s[k] += s[k + o];
+    const double sum = block_sum(s[0]);
     if (threadIdx.x == 0) *norm_out = (float)sqrt(sum);
 }
 
@@ -262,7 +266,9 @@ cudaError_t clip_list(const dpz_tensor* in, const dpz_tensor* out, int n, const 
 cudaError_t launch_tensors_sumsq(const dpz_tensor* in, int n, double* partial, cudaStream_t s)
 {
     set_last_kernel_name("tensors_sumsq");
-    return n <= kListSmall ? sumsq<kListSmall>(in, n, partial, s) : sumsq<kListMost>(in, n, partial, s);
+    return n <= kListSmall  ? sumsq<kListSmall>(in, n, partial, s)
+           : n <= kListMid  ? sumsq<kListMid>(in, n, partial, s)
+                            : sumsq<kListMost>(in, n, partial, s);
 }
 
 cudaError_t launch_tensors_norm(const double* partial, int64_t n, float* norm_out, cudaStream_t s)
@@ -277,6 +283,7 @@ cudaError_t launch_tensors_clip(const dpz_tensor* in, const dpz_tensor* out, int
 {
     set_last_kernel_name("tensors_clip");
     return n <= kListSmall ? clip_list<kListSmall>(in, out, n, norm, clip, s)
+           : n <= kListMid ? clip_list<kListMid>(in, out, n, norm, clip, s)
                            : clip_list<kListMost>(in, out, n, norm, clip, s);
 }
 

@@ -13,7 +13,8 @@ namespace dpz {
 
 constexpr int kListChunk = 65536;   // bytes of a block's part of a tensor
 constexpr int kListMost = 1024;     // tensors of one launch: their addresses are its parameters
-constexpr int kListSmall = 64;      // a smaller block of parameters for short lists
+constexpr int kListSmall = 64;      // smaller blocks of parameters for shorter lists
+constexpr int kListMid = 256;
 
 // Blocks of one tensor.
 inline int64_t list_chunks(const dpz_tensor& t)

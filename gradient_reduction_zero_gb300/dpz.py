@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+from array import array
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libdpz.so")
@@ -557,57 +558,65 @@ def lm_distill_step(logits, teacher_ids, teacher_logits, dloss, loss, dlogits, l
 
 # ------------------------------------------------------------ the attention block
 
-def _heads(words: list, t, what: str, dev: int, tokens: int, heads: int, D: int, code: int) -> None:
-    """Appends the dpz_heads of a tensor [tokens, heads, D] of unit element stride to
-    `words`."""
-    shape, strides = t.shape, t.stride()
-    if _CODES.get(t.dtype) != code or len(shape) != 3 or t.get_device() != dev \
-            or shape[0] != tokens or shape[1] != heads or shape[2] != D \
-            or (strides[2] != 1 and D > 1):
-        if t.dtype not in _dtypes():
-            raise TypeError(f"{what}: unsupported dtype {t.dtype}")
-        if _CODES[t.dtype] != code:
-            raise TypeError(f"{what} must have the dtype of q, not {t.dtype}")
-        raise ValueError(f"{what} must be [{tokens}, {heads}, {D}] of unit element stride on "
-                         f"cuda:{dev}, not {list(shape)} with strides {list(strides)} on {t.device}")
-    words += (t.data_ptr(), strides[0], strides[1])
+def _heads(words: list, t, what: str, dev: int, want: tuple, dtype) -> None:
+    """Appends the dpz_heads of a tensor of shape `want`, [tokens, heads, D], and unit element
+    stride to `words`."""
+    if t.shape != want or t.dtype is not dtype or t.get_device() != dev:
+        _bad_heads(t, what, dev, want, dtype)
+    ld, hs, step = t.stride()
+    if step != 1 and want[2] > 1:
+        _bad_heads(t, what, dev, want, dtype)
+    words += (t.data_ptr(), ld, hs)
+
+
+def _bad_heads(t, what, dev, want, dtype):
+    if t.dtype not in _dtypes():
+        raise TypeError(f"{what}: unsupported dtype {t.dtype}")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype} as q is, not {t.dtype}")
+    raise ValueError(f"{what} must be {list(want)} of unit element stride on cuda:{dev}, not "
+                     f"{list(t.shape)} with strides {list(t.stride())} on {t.device}")
 
 
 def _q_of(q) -> tuple:
-    """(GPU, dtype code, tokens, heads, D) of the queries."""
-    dev = q.get_device()
+    """(GPU, dtype, dtype code, tokens, heads, D) of the queries."""
+    dev, dtype, shape = q.get_device(), q.dtype, q.shape
     if dev != _current_device():     # the other tensors are compared with it
         _bad_device(q, "q")
-    code = _dtypes().get(q.dtype)
+    code = _CODES.get(dtype) if _ID_CODES else _dtypes().get(dtype)
     if code is None:
-        raise TypeError(f"q: unsupported dtype {q.dtype}")
-    if len(q.shape) != 3:
-        raise ValueError(f"q must be [tokens, heads, D], not {list(q.shape)}")
-    return (dev, code, *q.shape)
+        raise TypeError(f"q: unsupported dtype {dtype}")
+    if len(shape) != 3:
+        raise ValueError(f"q must be [tokens, heads, D], not {list(shape)}")
+    T, H, D = shape
+    return dev, dtype, code, T, H, D
 
 
 def _keys_of(k) -> tuple:
     """(tokens, heads) of the keys."""
-    if len(k.shape) != 3:
-        raise ValueError(f"k must be [tokens, heads, D], not {list(k.shape)}")
-    return k.shape[0], k.shape[1]
+    shape = k.shape
+    if len(shape) != 3:
+        raise ValueError(f"k must be [tokens, heads, D], not {list(shape)}")
+    return shape[0], shape[1]
 
 
 def _structs(words: list) -> tuple:
-    """A host array of the structs, and the address of each (three words)."""
-    a = (ctypes.c_int64 * len(words))(*words)
-    at = ctypes.addressof(a)
-    return a, [at + 8 * i for i in range(0, len(words), 3)]
+    """The words as dpz_heads structs on the host, three words each, and their address."""
+    a = array("q", words)
+    return a, a.buffer_info()[0]
+
+
+_HEADS_BYTES = 24
 
 
 def _rope_args(q, k, wq, wk, eps, positions, inv_freq, interleaved) -> tuple:
     """The GPU, the words of q and k and the arguments that the call and its gradient have in
     common."""
-    dev, code, T, Hq, D = _q_of(q)
+    dev, dtype, code, T, Hq, D = _q_of(q)
     Hk = _keys_of(k)[1]
     words: list = []
-    _heads(words, q, "q", dev, T, Hq, D, code)
-    _heads(words, k, "k", dev, T, Hk, D, code)
+    _heads(words, q, "q", dev, (T, Hq, D), dtype)
+    _heads(words, k, "k", dev, (T, Hk, D), dtype)
     wc, pw = F32, []
     for w, what in ((wq, "wq"), (wk, "wk")):
         if w is not None:
@@ -635,11 +644,13 @@ def attn_qk_norm_rope(q, k, q_out, k_out, wq=None, wk=None, positions=None, inv_
     times inv_freq (fp32), in pairs half of them apart, or of neighbours if
     `interleaved`.  q_out and k_out may be q and k."""
     dev, words, args = _rope_args(q, k, wq, wk, eps, positions, inv_freq, interleaved)
-    T, Hq, Hk, D, code = args[:5]
-    _heads(words, q_out, "q_out", dev, T, Hq, D, code)
-    _heads(words, k_out, "k_out", dev, T, Hk, D, code)
+    T, Hq, Hk, D = args[:4]
+    _heads(words, q_out, "q_out", dev, (T, Hq, D), q.dtype)
+    _heads(words, k_out, "k_out", dev, (T, Hk, D), q.dtype)
     keep, at = _structs(words)
-    _check(_C.attn_qk_norm_rope(at[0], at[1], *args, at[2], at[3], _current_stream(dev, stream)))
+    n = _HEADS_BYTES
+    _check(_C.attn_qk_norm_rope(at, at + n, *args, at + 2 * n, at + 3 * n,
+                                _current_stream(dev, stream)))
 
 
 def attn_qk_norm_rope_workspace(T: int, Hq: int, Hk: int, D: int, device=None):
@@ -665,10 +676,10 @@ def attn_qk_norm_rope_grad(q, k, dq_out, dk_out, dq, dk, ws=None, wq=None, wk=No
     dwq, dwk [D] of the weights' dtype.  ws: attn_qk_norm_rope_workspace(T, Hq,
     Hk, D), needed with dwq or dwk."""
     dev, words, args = _rope_args(q, k, wq, wk, eps, positions, inv_freq, interleaved)
-    T, Hq, Hk, D, code = args[:5]
+    T, Hq, Hk, D = args[:4]
     for t, what, h in ((dq_out, "dq_out", Hq), (dk_out, "dk_out", Hk), (dq, "dq", Hq),
                        (dk, "dk", Hk)):
-        _heads(words, t, what, dev, T, h, D, code)
+        _heads(words, t, what, dev, (T, h, D), q.dtype)
     pd, pws = [], None
     for d, w, what in ((dwq, wq, "dwq"), (dwk, wk, "dwk")):
         if d is not None and w is None:
@@ -680,19 +691,20 @@ def attn_qk_norm_rope_grad(q, k, dq_out, dk_out, dq, dk, ws=None, wq=None, wk=No
             raise ValueError("dwq and dwk need ws")
         pws = _workspace_of(ws, need, dev)
     keep, at = _structs(words)
-    _check(_C.attn_qk_norm_rope_grad(at[0], at[1], at[2], at[3], *args, at[4], at[5], pd[0], pd[1],
-                                     pws, _current_stream(dev, stream)))
+    n = _HEADS_BYTES
+    _check(_C.attn_qk_norm_rope_grad(at, at + n, at + 2 * n, at + 3 * n, *args, at + 4 * n, at + 5 * n,
+                                     pd[0], pd[1], pws, _current_stream(dev, stream)))
 
 
 def _attn_args(q, k, v, scale, causal, batch, cu_q, cu_k) -> tuple:
     """The GPU, the words of q, k and v and the arguments that attention and its
     gradient have in common."""
-    dev, code, Tq, Hq, D = _q_of(q)
+    dev, dtype, code, Tq, Hq, D = _q_of(q)
     Tk, Hk = _keys_of(k)
     words: list = []
-    _heads(words, q, "q", dev, Tq, Hq, D, code)
-    _heads(words, k, "k", dev, Tk, Hk, D, code)
-    _heads(words, v, "v", dev, Tk, Hk, D, code)
+    _heads(words, q, "q", dev, (Tq, Hq, D), dtype)
+    _heads(words, k, "k", dev, (Tk, Hk, D), dtype)
+    _heads(words, v, "v", dev, (Tk, Hk, D), dtype)
     pq = pk = None
     it = I32
     if (cu_q is None) != (cu_k is None):
@@ -720,11 +732,12 @@ def attn_forward(q, k, v, out, lse=None, scale=None, causal: bool = False, batch
     D ** -0.5.  causal: the last query of a sequence sees all of its keys, the one
     before it one less."""
     dev, words, args = _attn_args(q, k, v, scale, causal, batch, cu_q, cu_k)
-    Tq, _, Hq, _, D, code = args[:6]
-    _heads(words, out, "out", dev, Tq, Hq, D, code)
+    Tq, _, Hq, _, D = args[:5]
+    _heads(words, out, "out", dev, (Tq, Hq, D), q.dtype)
     keep, at = _structs(words)
-    _check(_C.attn_forward(at[0], at[1], at[2], *args, at[3], _rows_of_heads(lse, "lse", dev, Hq, Tq),
-                           _current_stream(dev, stream)))
+    n = _HEADS_BYTES
+    _check(_C.attn_forward(at, at + n, at + 2 * n, *args, at + 3 * n,
+                           _rows_of_heads(lse, "lse", dev, Hq, Tq), _current_stream(dev, stream)))
 
 
 def _rows_of_heads(t, what: str, dev: int, H: int, T: int):
@@ -748,14 +761,17 @@ def attn_grad(q, k, v, out, lse, dout, dq, dk, dv, ws, scale=None, causal: bool 
     lse and dout [Tq, Hq, D].  ws: attn_grad_workspace(Tq, Tk, batch, Hq, Hk, D)
     or larger."""
     dev, words, args = _attn_args(q, k, v, scale, causal, batch, cu_q, cu_k)
-    Tq, Tk, Hq, Hk, D, code, B = args[:7]
-    for t, what, n, h in ((out, "out", Tq, Hq), (dout, "dout", Tq, Hq), (dq, "dq", Tq, Hq),
-                          (dk, "dk", Tk, Hk), (dv, "dv", Tk, Hk)):
-        _heads(words, t, what, dev, n, h, D, code)
+    Tq, Tk, Hq, Hk, D, _, B = args[:7]
+    rows, keys = (Tq, Hq, D), (Tk, Hk, D)
+    for t, what, want in ((out, "out", rows), (dout, "dout", rows), (dq, "dq", rows),
+                          (dk, "dk", keys), (dv, "dv", keys)):
+        _heads(words, t, what, dev, want, q.dtype)
     pws = _workspace_of(ws, lib.attn_grad_workspace_bytes(Tq, Tk, B, Hq, Hk, D), dev)
     keep, at = _structs(words)
-    _check(_C.attn_grad(at[0], at[1], at[2], at[3], _rows_of_heads(lse, "lse", dev, Hq, Tq), at[4],
-                        *args, at[5], at[6], at[7], pws, _current_stream(dev, stream)))
+    n = _HEADS_BYTES
+    _check(_C.attn_grad(at, at + n, at + 2 * n, at + 3 * n, _rows_of_heads(lse, "lse", dev, Hq, Tq),
+                        at + 4 * n, *args, at + 5 * n, at + 6 * n, at + 7 * n, pws,
+                        _current_stream(dev, stream)))
 
 
 # ------------------------------------------------------------ lists of tensors
