@@ -116,9 +116,10 @@ __device__ __forceinline__ void seq_bounds(const void* cu, int itype, int64_t b,
 }
 
 // Tile number `tile` of all sequences' tiles of `per` rows, over the queries
-// (of_keys false) or the keys.  Called by whole warps with equal arguments: with
-// offsets, 32 sequences' numbers of tiles are summed at a time.  The number
-// of tiles is at most tiles_bound(), below 2^31.
+// (of_keys false) or the keys: by position in sequences of equal length, else by
+// sequence.  Called by whole warps with equal arguments: with offsets, 32
+// sequences' numbers of tiles are summed at a time.  The number of tiles is at
+// most tiles_bound(), below 2^31.
 __device__ __forceinline__ Tile find_tile(const AttnArgs& a, int tile, int per, bool of_keys)
 {
     const void* cu = of_keys ? a.cu_k : a.cu_q;
@@ -127,13 +128,11 @@ __device__ __forceinline__ Tile find_tile(const AttnArgs& a, int tile, int per, 
     Tile t{};
     int b = -1;
     if (cu == nullptr) {
-        const unsigned each = (unsigned)(len + per - 1) / (unsigned)per;
-        if (each > 0) {
-            const unsigned q = (unsigned)tile / each;
-            if (q < a.B) {
-                b = (int)q;
-                t.row0 = (int)((unsigned)tile - q * each) * per;
-            }
+        // the same tile of every sequence, then the next: equal amounts of work side by side
+        const unsigned n = (unsigned)a.B, at = (unsigned)tile / n;
+        if ((int64_t)at * per < len) {
+            b = (int)((unsigned)tile - at * n);
+            t.row0 = (int)at * per;
         }
     } else {
         const int lane = threadIdx.x & 31;

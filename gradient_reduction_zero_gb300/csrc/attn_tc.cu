@@ -140,6 +140,14 @@ struct Item {
     int first;         // the first of them (forward)
 };
 
+// The item of block b in a round: there and back, so that the block with the longest item of
+// one round has the shortest of the next.
+__device__ __forceinline__ int64_t item_of_round(int64_t round)
+{
+    const unsigned b = round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+    return round * gridDim.x + b;
+}
+
 constexpr int kRing = 4;
 
 struct Ring {
@@ -469,8 +477,9 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
         bool going = true;
         Item m{};
         // in parts: one item for the blocks of a cluster
-        for (int64_t w = SPLIT ? blockIdx.x / parts : blockIdx.x; w < items && going;
-             w += gridDim.x) {
+        for (int64_t round = 0; round * (SPLIT ? 1 << 30 : gridDim.x) < items && going; ++round) {
+            const int64_t w = SPLIT ? blockIdx.x / parts : item_of_round(round);
+            if (w >= items) continue;
             // the tiles at the end of a sequence see the most keys and go first
             const int tile = (int)(w / groups);
             const Tile t = find_tile(a, pairs - 1 - tile, 2 * pk.tokens, false);
@@ -816,7 +825,9 @@ k_attn_tc_dq(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs
         Turn<S::kStages> kt;
         bool going = true;
         Item m{};
-        for (int64_t w = blockIdx.x; w < items && going; w += gridDim.x) {
+        for (int64_t round = 0; round * gridDim.x < items && going; ++round) {
+            const int64_t w = item_of_round(round);
+            if (w >= items) continue;
             // the tiles at the end of a sequence see the most keys and go first
             const int tile = (int)(w / a.Hq);
             const Tile t = find_tile(a, tiles - 1 - tile, kTcRows, false);
@@ -1079,7 +1090,9 @@ k_attn_tc_dkv(const __grid_constant__ Maps maps, const __grid_constant__ AttnArg
         Turn<S::kStages> kt;
         bool going = true;
         Item m{};
-        for (int64_t w = blockIdx.x; w < items && going; w += gridDim.x) {
+        for (int64_t round = 0; round * gridDim.x < items && going; ++round) {
+            const int64_t w = item_of_round(round);
+            if (w >= items) continue;
             // the first keys of a sequence are seen by the most queries: tiles in order
             const int tile = (int)(w / a.Hk);
             const Tile t = find_tile(a, tile, kTcRows, true);
