@@ -1,8 +1,10 @@
 """GB300-native data-parallel / ZeRO-1 step: ring reduce-scatter + average,
 global-norm clip, sharded AdamW, bf16 cast and all-gather for N simulated
-ranks resident in one GPU's HBM, and the vocabulary-sized ends of a replica's step
-(embedding, token log probabilities, distillation, with their gradients), as
-hand-written sm_103a CUDA behind a C-ABI (include/dpz.h).
+ranks resident in one GPU's HBM, the vocabulary-sized ends of a replica's step
+(embedding, token log probabilities, distillation, with their gradients), its attention
+block (head norm with rotation, attention, their gradients), and the global norm and
+clip of a list of tensors, as hand-written sm_103a CUDA behind a C-ABI
+(include/dpz.h).
 
 ``dpz`` is the ctypes binding; importing it (or any of its names from this
 package) loads libdpz.so and raises ImportError if it is not built: there is

@@ -42,28 +42,80 @@ __device__ __forceinline__ void put(char* p, float x)
     else *reinterpret_cast<float*>(p) = x;
 }
 
-// 64 rows of DP floats, rows DP + 4 apart: rows [row, row + 64) of head h among
-// rows [first, first + n) of x, zeros beyond n and beyond D.
+// Whether groups of four elements of every row lie on boundaries of their size.
+template <int DT>
+__device__ __forceinline__ bool quads(const Heads& x, int D)
+{
+    constexpr int ES = DT == DPZ_BF16 ? 2 : 4;
+    return ((reinterpret_cast<uintptr_t>(x.p) / ES | (uintptr_t)x.ld | (uintptr_t)x.hs | (uintptr_t)D) & 3) == 0 &&
+           reinterpret_cast<uintptr_t>(x.p) % ES == 0;
+}
+
+// A thread's part of a tile: 64 rows of DP floats, rows [row, row + 64) of head h among rows
+// [first, first + n) of x, zeros beyond n and beyond D.  All of its loads are under way
+// before the first is used.
+template <int DT, int DP>
+struct TileLoad {
+    static constexpr int kQuads = kAnyTile * DP / 4 / kAnyThreads;
+    float4 v[kQuads];
+
+    __device__ __forceinline__ void load(const Heads& x, int64_t first, int row, int n, int h, int D)
+    {
+        constexpr int ES = DT == DPZ_BF16 ? 2 : 4;
+        const char* base = x.p + ((first + row) * x.ld + (int64_t)h * x.hs) * ES;
+        const int rows = min(kAnyTile, n - row);
+        const bool whole = quads<DT>(x, D);
+#pragma unroll
+        for (int k = 0; k < kQuads; ++k) {
+            const int i = threadIdx.x + k * kAnyThreads, r = i / (DP / 4), d = i % (DP / 4) * 4;
+            v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (r >= rows || d >= D) continue;
+            const char* p = base + ((int64_t)r * x.ld + d) * ES;
+            if (whole) {
+                if constexpr (DT == DPZ_BF16) {
+                    const uint2 w = *reinterpret_cast<const uint2*>(p);
+                    v[k] = make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+                } else {
+                    v[k] = *reinterpret_cast<const float4*>(p);
+                }
+            } else {
+                v[k].x = elem<DT>(p);
+                if (d + 1 < D) v[k].y = elem<DT>(p + ES);
+                if (d + 2 < D) v[k].z = elem<DT>(p + 2 * ES);
+                if (d + 3 < D) v[k].w = elem<DT>(p + 3 * ES);
+            }
+        }
+    }
+    // rows DP + 4 floats apart
+    __device__ __forceinline__ void store(float* s) const
+    {
+#pragma unroll
+        for (int k = 0; k < kQuads; ++k) {
+            const int i = threadIdx.x + k * kAnyThreads, r = i / (DP / 4), d = i % (DP / 4) * 4;
+            *reinterpret_cast<float4*>(s + r * (DP + 4) + d) = v[k];
+        }
+    }
+};
+
 template <int DT, int DP>
 __device__ __forceinline__ void load_tile(float* s, const Heads& x, int64_t first, int row, int n,
                                           int h, int D)
 {
-    constexpr int ES = DT == DPZ_BF16 ? 2 : 4, DS = DP + 4;
-    const char* base = x.p + ((first + row) * x.ld + (int64_t)h * x.hs) * ES;
-    const int rows = min(kAnyTile, n - row);
-    // four elements of a thread, 16 rows of a pass in the case of 64 elements
-    for (int i = threadIdx.x; i < kAnyTile * DP / 4; i += kAnyThreads) {
-        const int r = i / (DP / 4), d = i % (DP / 4) * 4;
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (r < rows) {
-            const char* p = base + ((int64_t)r * x.ld + d) * ES;
-            if (d < D) v.x = elem<DT>(p);
-            if (d + 1 < D) v.y = elem<DT>(p + ES);
-            if (d + 2 < D) v.z = elem<DT>(p + 2 * ES);
-            if (d + 3 < D) v.w = elem<DT>(p + 3 * ES);
-        }
-        *reinterpret_cast<float4*>(s + r * DS + d) = v;
-    }
+    TileLoad<DT, DP> t;
+    t.load(x, first, row, n, h, D);
+    t.store(s);
+}
+
+// Two tiles at once.
+template <int DT, int DP>
+__device__ __forceinline__ void load_tiles(float* s0, const Heads& x0, float* s1, const Heads& x1,
+                                           int64_t first, int row, int n, int h, int D)
+{
+    TileLoad<DT, DP> t, u;
+    t.load(x0, first, row, n, h, D);
+    u.load(x1, first, row, n, h, D);
+    t.store(s0);
+    u.store(s1);
 }
 
 // acc[i][j] = a[row 4 ty + i] . b[row tx + 16 j]
@@ -214,8 +266,7 @@ __global__ void __launch_bounds__(kAnyThreads) k_attn_any(AttnArgs a)
     const int end = keys_end(a, t, kAnyTile);
     for (int j0 = 0; j0 < end; j0 += kAnyTile) {
         __syncthreads();
-        load_tile<DT, DP>(k, a.k, t.k0, j0, t.nk, hk, a.D);
-        load_tile<DT, DP>(v, a.v, t.k0, j0, t.nk, hk, a.D);
+        load_tiles<DT, DP>(k, a.k, v, a.v, t.k0, j0, t.nk, hk, a.D);
         __syncthreads();
         float s[4][4];
         dot_tile<DP>(q, k, s);
@@ -297,8 +348,7 @@ __global__ void __launch_bounds__(kAnyThreads) k_attn_any_dq(AttnArgs a)
     if (!t.any) return;
     const int h = blockIdx.y, hk = h / (a.Hq / a.Hk);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    load_tile<DT, DP>(q, a.q, t.q0, t.row0, t.nq, h, a.D);
-    load_tile<DT, DP>(dout, a.dout, t.q0, t.row0, t.nq, h, a.D);
+    load_tiles<DT, DP>(q, a.q, dout, a.dout, t.q0, t.row0, t.nq, h, a.D);
     load_tile<DT, DP>(k, a.out, t.q0, t.row0, t.nq, h, a.D);
     __syncthreads();
     float lse[4], delta[4];
@@ -316,8 +366,7 @@ __global__ void __launch_bounds__(kAnyThreads) k_attn_any_dq(AttnArgs a)
     const int end = keys_end(a, t, kAnyTile);
     for (int j0 = 0; j0 < end; j0 += kAnyTile) {
         __syncthreads();
-        load_tile<DT, DP>(k, a.k, t.k0, j0, t.nk, hk, a.D);
-        load_tile<DT, DP>(v, a.v, t.k0, j0, t.nk, hk, a.D);
+        load_tiles<DT, DP>(k, a.k, v, a.v, t.k0, j0, t.nk, hk, a.D);
         __syncthreads();
         float s[4][4], ds[4][4];
         score_grad<DP>(a, t, t.row0, j0, q, k, dout, v, lse, delta, s, ds);
@@ -346,16 +395,14 @@ __global__ void __launch_bounds__(kAnyThreads) k_attn_any_dkv(AttnArgs a)
     if (!t.any) return;
     const int hk = blockIdx.y, G = a.Hq / a.Hk;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    load_tile<DT, DP>(k, a.k, t.k0, t.row0, t.nk, hk, a.D);
-    load_tile<DT, DP>(v, a.v, t.k0, t.row0, t.nk, hk, a.D);
+    load_tiles<DT, DP>(k, a.k, v, a.v, t.k0, t.row0, t.nk, hk, a.D);
     float dk[4][DP / 64][4] = {}, dv[4][DP / 64][4] = {};
     // the first query that sees this tile's first key
     const int first = a.causal ? max(0, t.row0 - (t.nk - t.nq)) / kAnyTile * kAnyTile : 0;
     for (int h = hk * G; h < (hk + 1) * G; ++h)
         for (int i0 = first; i0 < t.nq; i0 += kAnyTile) {
             __syncthreads();
-            load_tile<DT, DP>(q, a.q, t.q0, i0, t.nq, h, a.D);
-            load_tile<DT, DP>(dout, a.dout, t.q0, i0, t.nq, h, a.D);
+            load_tiles<DT, DP>(q, a.q, dout, a.dout, t.q0, i0, t.nq, h, a.D);
             float lse[4], delta[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
