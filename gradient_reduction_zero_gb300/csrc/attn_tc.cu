@@ -729,13 +729,13 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
 // item are issued before the last dq of this one.  Warps 0-3 have the first 64 keys of a
 // tile, 4-7 the others.
 
-constexpr int kGradThreads = 384;   // 8 compute warps, loads, products, two idle
+constexpr int kGradThreads = 384;   // 8 compute warps, loads, products, two for delta or idle
 
 struct GradBars {
     Ring ring;
-    uint64_t once_full[2], once_empty[2], in_full[3], in_empty[3];
-    uint64_t s_full, s_free, g_full, p_full, d_full, d_free, o_full, o_free,
-        rows_full;
+    uint64_t once_full[2], once_empty[2], in_full[3], in_empty[3], v_full[3], v_empty[3];
+    uint64_t s_full, s_free, g_full, p_full, d_full, d_free, o_full, o_free;
+    uint64_t rows_full[2], rows_empty[2];
     uint32_t tmem;
     int lost;
 };
@@ -753,20 +753,40 @@ struct GradShape {
     static_assert(kBytes <= 227 * 1024, "shared memory of a block");
 };
 
+// The queries' kernel keeps keys until dq has them and values only until dp has: places of
+// their own, three for keys.  (With two pairs of places the next keys began to load only
+// when dq was done: 3,080 clocks a tile of 128 columns.)
+constexpr int kDqComputeRegs = 192, kDqOtherRegs = 120;    // 2 x 128 x 192 + 128 x 120 = 384 x 168
+
+template <int BLOCKS>
+struct DqShape {
+    static constexpr int kTile = BLOCKS * kTcBlock;
+    static constexpr int kOnces = GradShape<BLOCKS>::kOnces;
+    static constexpr int kKs = 3, kVs = BLOCKS == 1 ? 3 : 2;
+    static constexpr int kK = kOnces * 2 * kTile, kV = kK + kKs * kTile;
+    static constexpr int kRows = kV + kVs * kTile;       // 2 x 128 floats
+    static constexpr int kBars = kRows + 1024;
+    static constexpr int kBytes = kBars + 1024 + 1008;   // the base is rounded up from 16 to 1024
+    static_assert(kBytes <= 227 * 1024, "shared memory of a block");
+};
+
 // The start of a block of either kernel: barriers, tensor memory.
 template <int BLOCKS>
-__device__ __forceinline__ uint32_t grad_start(GradBars& bar, const Maps& maps, int warp)
+__device__ __forceinline__ uint32_t grad_start(GradBars& bar, const Maps& maps, int warp,
+                                               uint32_t readers)
 {
     using S = GradShape<BLOCKS>;
     if (threadIdx.x == 0) {
-        ring_init(bar.ring, 9);
+        ring_init(bar.ring, readers);
         for (int i = 0; i < S::kOnces; ++i) {
             mbar_init(&bar.once_full[i], 1);
             mbar_init(&bar.once_empty[i], 1);
         }
-        for (int i = 0; i < S::kStages; ++i) {
+        for (int i = 0; i < 3; ++i) {
             mbar_init(&bar.in_full[i], 1);
             mbar_init(&bar.in_empty[i], 1);
+            mbar_init(&bar.v_full[i], 1);
+            mbar_init(&bar.v_empty[i], 1);
         }
         mbar_init(&bar.s_full, 1);
         mbar_init(&bar.s_free, 8);
@@ -776,7 +796,10 @@ __device__ __forceinline__ uint32_t grad_start(GradBars& bar, const Maps& maps, 
         mbar_init(&bar.d_free, 1);
         mbar_init(&bar.o_full, 1);
         mbar_init(&bar.o_free, 8);
-        mbar_init(&bar.rows_full, 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.rows_full[i], 2);
+            mbar_init(&bar.rows_empty[i], 8);
+        }
         bar.lost = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         tma_prefetch(&maps.q);
@@ -791,6 +814,16 @@ __device__ __forceinline__ uint32_t grad_start(GradBars& bar, const Maps& maps, 
     tc_fence_after();
     pdl_launch_dependents();
     return (uint32_t)uniform((int)bar.tmem);
+}
+
+// An operand's tile to its place.
+template <int BLOCKS>
+__device__ __forceinline__ void load_one(char* to, const CUtensorMap* x, uint64_t* full, int head,
+                                         int row)
+{
+    mbar_expect_tx(full, GradShape<BLOCKS>::kTile);
+    for (int b = 0; b < BLOCKS; ++b)
+        tma_load(to + b * kTcBlock, x, full, b * kTcCols, head, row);
 }
 
 // Two operands' tiles to a pair of places.
@@ -811,21 +844,22 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 k_attn_tc_dq(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a, int tiles,
              int64_t items)
 {
-    using S = GradShape<BLOCKS>;
+    using S = DqShape<BLOCKS>;
     extern __shared__ char smem_raw[];
     char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     GradBars& bar = *reinterpret_cast<GradBars*>(smem + S::kBars);
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const uint32_t tmem = grad_start<BLOCKS>(bar, maps, warp);
+    const uint32_t tmem = grad_start<BLOCKS>(bar, maps, warp, 11);
     volatile int* lost = &bar.lost;
     const int ksteps = (a.D + 15) / 16, width = ksteps * 16;
     Turn<kRing> turn;
 
     if (warp == 8) {
         // ---- items and loads
-        set_registers_down<kOtherRegs>();
+        set_registers_down<kDqOtherRegs>();
         Turn<S::kOnces> qt;
-        Turn<S::kStages> kt;
+        Turn<S::kKs> kt;
+        Turn<S::kVs> vt;
         bool going = true;
         Item m{};
         for (int64_t round = 0; round * gridDim.x < items && going; ++round) {
@@ -846,13 +880,18 @@ k_attn_tc_dq(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs
                 if (going)
                     load_pair<BLOCKS>(smem + qt.at * 2 * S::kTile, &maps.q, &maps.dout,
                                       &bar.once_full[qt.at], m.head, (int)t.q0 + t.row0);
+                const int hk = m.head / (a.Hq / a.Hk);
                 for (int j = 0; j < n && going; ++j) {
                     going = tc_wait(&bar.in_empty[kt.at], kt.parity ^ 1, lost);
                     if (!going) break;
-                    load_pair<BLOCKS>(smem + S::kIn + kt.at * 2 * S::kTile, &maps.k, &maps.v,
-                                      &bar.in_full[kt.at], m.head / (a.Hq / a.Hk),
-                                      (int)t.k0 + j * kTcRows);
+                    load_one<BLOCKS>(smem + S::kK + kt.at * S::kTile, &maps.k, &bar.in_full[kt.at], hk,
+                                     (int)t.k0 + j * kTcRows);
                     kt.next();
+                    going = tc_wait(&bar.v_empty[vt.at], vt.parity ^ 1, lost);
+                    if (!going) break;
+                    load_one<BLOCKS>(smem + S::kV + vt.at * S::kTile, &maps.v, &bar.v_full[vt.at], hk,
+                                     (int)t.k0 + j * kTcRows);
+                    vt.next();
                 }
             }
             qt.next();
@@ -862,10 +901,11 @@ k_attn_tc_dq(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs
         if (going) ring_put(bar.ring, turn, m, lost);
     } else if (warp == 9) {
         // ---- products
-        set_registers_down<kOtherRegs>();
+        set_registers_down<kDqOtherRegs>();
         const uint32_t s_desc = tc_idesc(kTcRows, false), o_desc = tc_idesc(width, true);
         Turn<S::kOnces> qt;
-        Turn<S::kStages> kt, dt;
+        Turn<S::kKs> kt, dt;
+        Turn<S::kVs> vt;
         uint32_t s_par = 1, d_par = 0, f_par = 1;
         bool going = true, left = false, left_first = false;
         // dq += ds k of the step before this one
@@ -879,7 +919,7 @@ k_attn_tc_dq(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs
             if (!going) return;
             tc_fence_after();
             if (elect_one()) {
-                tc_rows(tmem + 256, tmem + 384, 0, smem + S::kIn + dt.at * 2 * S::kTile, o_desc,
+                tc_rows(tmem + 256, tmem + 384, 0, smem + S::kK + dt.at * S::kTile, o_desc,
                         !left_first);
                 tc_commit(&bar.d_free);
                 tc_commit(&bar.in_empty[dt.at]);
@@ -898,9 +938,10 @@ k_attn_tc_dq(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs
             going = tc_wait_warp(&bar.once_full[qt.at], qt.parity, lost);
             const char* q = smem + qt.at * 2 * S::kTile;
             for (int j = 0; j < n && going; ++j) {
-                going = tc_wait_warp(&bar.in_full[kt.at], kt.parity, lost);
+                going = tc_wait_warp(&bar.in_full[kt.at], kt.parity, lost) &&
+                        tc_wait_warp(&bar.v_full[vt.at], vt.parity, lost);
                 if (!going) break;
-                char* in = smem + S::kIn + kt.at * 2 * S::kTile;
+                char* in = smem + S::kK + kt.at * S::kTile;
                 const int rows = m.nk - j * kTcRows;
                 if (rows < kTcRows) {     // dq sums over the keys
                     clear_rows(in, rows, BLOCKS);
@@ -913,12 +954,15 @@ k_attn_tc_dq(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs
                 tc_fence_after();
                 if (elect_one()) {
                     tc_dot<BLOCKS>(tmem, q, in, ksteps, s_desc);
-                    tc_dot<BLOCKS>(tmem + 128, q + S::kTile, in + S::kTile, ksteps, s_desc);
+                    tc_dot<BLOCKS>(tmem + 128, q + S::kTile, smem + S::kV + vt.at * S::kTile, ksteps,
+                                   s_desc);
                     tc_commit(&bar.s_full);
+                    tc_commit(&bar.v_empty[vt.at]);
                     if (j + 1 == n) tc_commit(&bar.once_empty[qt.at]);
                 }
                 __syncwarp();
                 kt.next();
+                vt.next();
                 if (left) add_dq();
                 left = true;
                 left_first = j == 0;
@@ -928,64 +972,27 @@ k_attn_tc_dq(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs
         if (going && left) add_dq();
     } else if (warp < 8) {
         // ---- scores' gradients
-        set_registers_up<kComputeRegs>();
-        float* delta_s = reinterpret_cast<float*>(smem + S::kRows);
+        set_registers_up<kDqComputeRegs>();
+        const float* rows_s = reinterpret_cast<const float*>(smem + S::kRows);
+        Turn<2> rt;
         const int r = (warp & 3) * 32 + lane, half = warp >> 2;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const float c2 = a.scale * kLog2e;
         const F2 cc = pack2(c2, c2);
         const bool wide = wide_rows(a.dq);
-        uint32_t s_par = 0, d_par = 0, r_par = 0;
+        uint32_t s_par = 0, d_par = 0;
         bool going = true;
         Item m;
         while (going && ring_take(bar.ring, turn, m, lost)) {
             const int row = m.row0 + r, n = m.tiles[0];
             const bool live = row < m.nq;
             const float lse = live ? a.lse[(int64_t)m.head * a.Tq + m.q0 + row] : -INFINITY;
-            // delta of 16 rows, two at a time, all loads first
-            float part[8];
-            {
-                uint4 u[8], w[8];
-                const int d = (lane & 15) * 8;
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const int rr = m.row0 + warp * 16 + 2 * q + (lane >> 4);
-                    u[q] = w[q] = make_uint4(0, 0, 0, 0);
-                    if (rr < m.nq && d < a.D) {
-                        u[q] = *reinterpret_cast<const uint4*>(row_of(a.dout, m.q0 + rr, m.head) + 2 * d);
-                        w[q] = *reinterpret_cast<const uint4*>(row_of(a.out, m.q0 + rr, m.head) + 2 * d);
-                    }
-                }
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const uint32_t us[4] = {u[q].x, u[q].y, u[q].z, u[q].w};
-                    const uint32_t ws[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
-                    part[q] = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        part[q] = fmaf(bf16_hi(us[e]), bf16_hi(ws[e]),
-                                       fmaf(bf16_lo(us[e]), bf16_lo(ws[e]), part[q]));
-                }
-            }
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-#pragma unroll
-                for (int o = 1; o < 16; o <<= 1) part[q] += __shfl_xor_sync(0xffffffffu, part[q], o);
-                if ((lane & 15) == 0) {
-                    const int rr = warp * 16 + 2 * q + (lane >> 4);
-                    delta_s[rr] = part[q];
-                    if (m.row0 + rr < m.nq)
-                        a.delta[(int64_t)m.head * a.Tq + m.q0 + m.row0 + rr] = part[q];
-                }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.rows_full);
-            going = tc_wait_warp(&bar.rows_full, r_par, lost);    // of all compute warps
-            r_par ^= 1;
+            going = tc_wait_warp(&bar.rows_full[rt.at], rt.parity, lost);
             if (!going) break;
-            const float delta = delta_s[r];
-            delta_s = reinterpret_cast<float*>(smem + S::kRows) +
-                      (delta_s == reinterpret_cast<float*>(smem + S::kRows) ? 128 : 0);
+            const float delta = rows_s[rt.at * 128 + r];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.rows_empty[rt.at]);
+            rt.next();
             const bool none = lse == -INFINITY;
             const int seen = none ? 0 : a.causal ? min(m.nk, row + m.nk - m.nq + 1) : m.nk;
             const F2 nl = pack2(-lse * kLog2e, -lse * kLog2e), nd = pack2(-delta, -delta);
@@ -1045,7 +1052,53 @@ k_attn_tc_dq(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs
             else zero_row(cols, out, live);
         }
     } else {
-        set_registers_down<kOtherRegs>();
+        // ---- delta, 64 rows of an item each, ahead of the compute warps
+        set_registers_down<kDqOtherRegs>();
+        float* rows_s = reinterpret_cast<float*>(smem + S::kRows);
+        Turn<2> rt;
+        // lanes of a row, rows of a load, loads under way: what a pass waits for is latency
+        constexpr int kLanes = 8 * BLOCKS, kAtOnce = 32 / kLanes, kLoads = 8;
+        const int d = (lane & (kLanes - 1)) * 8;
+        Item m;
+        while (ring_take(bar.ring, turn, m, lost)) {
+            if (!tc_wait_warp(&bar.rows_empty[rt.at], rt.parity ^ 1, lost)) break;
+            for (int r0 = (warp - 10) * 64; r0 < (warp - 9) * 64; r0 += kLoads * kAtOnce) {
+                const int r1 = r0 + lane / kLanes;
+                const char* g = row_of(a.dout, m.q0 + m.row0 + r1, m.head) + 2 * d;
+                const char* o = row_of(a.out, m.q0 + m.row0 + r1, m.head) + 2 * d;
+                const int64_t step_g = 2 * kAtOnce * a.dout.ld, step_o = 2 * kAtOnce * a.out.ld;
+                uint4 u[kLoads], w[kLoads];
+#pragma unroll
+                for (int q = 0; q < kLoads; ++q) {
+                    u[q] = w[q] = make_uint4(0, 0, 0, 0);
+                    if (m.row0 + r1 + q * kAtOnce < m.nq && d < a.D) {
+                        u[q] = *reinterpret_cast<const uint4*>(g + q * step_g);
+                        w[q] = *reinterpret_cast<const uint4*>(o + q * step_o);
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < kLoads; ++q) {
+                    const uint32_t us[4] = {u[q].x, u[q].y, u[q].z, u[q].w};
+                    const uint32_t ws[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+                    float y = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        y = fmaf(bf16_hi(us[e]), bf16_hi(ws[e]),
+                                 fmaf(bf16_lo(us[e]), bf16_lo(ws[e]), y));
+#pragma unroll
+                    for (int k = 1; k < kLanes; k <<= 1) y += __shfl_xor_sync(0xffffffffu, y, k);
+                    const int r = r1 + q * kAtOnce;
+                    if (d == 0) {
+                        rows_s[rt.at * 128 + r] = y;
+                        if (m.row0 + r < m.nq)
+                            a.delta[(int64_t)m.head * a.Tq + m.q0 + m.row0 + r] = y;
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.rows_full[rt.at]);
+            rt.next();
+        }
     }
     tc_finish(lost, tmem, warp == 9);
 }
@@ -1080,7 +1133,7 @@ k_attn_tc_dkv(const __grid_constant__ Maps maps, const __grid_constant__ AttnArg
     GradBars& bar = *reinterpret_cast<GradBars*>(smem + S::kBars);
     float* rows_s = reinterpret_cast<float*>(smem + S::kRows);   // [stage][-lse log2e, -delta][128]
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const uint32_t tmem = grad_start<BLOCKS>(bar, maps, warp);
+    const uint32_t tmem = grad_start<BLOCKS>(bar, maps, warp, 9);
     volatile int* lost = &bar.lost;
     const int G = a.Hq / a.Hk;
     const int ksteps = (a.D + 15) / 16, width = ksteps * 16;
@@ -1473,7 +1526,7 @@ cudaError_t launch_attn_tc_dq(const AttnArgs& a, cudaStream_t s)
         static SmemRaisedOn raised;
         const int64_t tiles = tiles_bound(a.cu_q, a.Tq, a.B, kTcRows);
         const int64_t items = tiles * a.Hq;
-        return launch_tc(k_attn_tc_dq<n>, raised, GradShape<n>::kBytes, items < sms ? items : sms, 1,
+        return launch_tc(k_attn_tc_dq<n>, raised, DqShape<n>::kBytes, items < sms ? items : sms, 1,
                          kGradThreads, s, 0u, m, a, (int)tiles, items);
     });
 }
