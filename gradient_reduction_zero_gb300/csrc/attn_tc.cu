@@ -10,6 +10,11 @@
 // would lie in a tile beyond a sequence's end is not zero in memory: it is masked
 // where it is a column of scores, cleared in shared memory where a product
 // sums over it, and otherwise a row of its own that is not stored.
+//
+// Measured, one sequence of 8,192 tokens of 16 + 4 heads of 128 without a mask: forward 429 us
+// (1,281 TFLOP/s), queries' gradient 560 (1,473), keys' and values' 761 (1,446).  8 x 1,024
+// tokens of 25 heads of 64, causal: 49 us, and 165 us for both gradients.  Bound by the
+// chain of a tile: products, tensor memory to registers, exponentials, and back.
 #include <cmath>
 #include <type_traits>
 
