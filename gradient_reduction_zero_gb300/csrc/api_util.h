@@ -1,6 +1,7 @@
-// What the entry points of api.cpp and lm_api.cpp share: status codes and the
-// last-error message, checks of pointers and overlaps, and the launch with
-// its accounting and optional per-launch event timing.
+// What the entry points (api.cpp, lm_api.cpp, attn_api.cpp, tensors_api.cpp)
+// share: status codes and the last-error message, checks of pointers and
+// overlaps, and the launch with its accounting and optional per-launch event
+// timing.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) k_rope(const __grid_constant_
                     other[s][q] = mul2(partner<SWAP, V>(w[s], q), m[1]);
                 }
         }
-        for (int b0 = 0; b0 < per; b0 += kRopeAhead)
+        for (int b0 = 0; b0 < min(per, H); b0 += kRopeAhead)
 #pragma unroll
             for (int j = 0; j < kRopeAhead; ++j) {
                 const int b = b0 + j;
@@ -487,7 +487,7 @@ k_rope_grad(const __grid_constant__ RopeArgs a, int per)
             rd[j].load(p, head_row(a.dout[k], t, h0 + j, ES), j < n);
         }
         const Turns<V, NS> turns = turns_of<SWAP, V, NS>(p, a, frac, t);
-        for (int b0 = 0; b0 < per; b0 += kRopeGradAhead)
+        for (int b0 = 0; b0 < min(per, H); b0 += kRopeGradAhead)
 #pragma unroll
         for (int j = 0; j < kRopeGradAhead; ++j) {
             const int b = b0 + j;
@@ -628,13 +628,15 @@ cudaError_t by_vector(const RopeArgs& a, bool grad, F&& f)
 
 }  // namespace
 
-// Heads of an item, by sizes alone (the sums' order follows it): up to 16, fewer while
-// the items would leave most of the GPU without work.
-int heads_of_item(int64_t tokens, int H, int lanes, int64_t threads)
+// Heads of an item, by sizes alone (the sums' order follows it): up to `most`, fewer while
+// the items would leave most of the threads without work, and about equally many in each item
+// (25 heads as 4 x 7, not 16 + 9).
+int heads_of_item(int64_t tokens, int H, int lanes, int64_t threads, int most)
 {
-    int per = 16;
+    int per = most;
     while (per > 1 && tokens * ((H + per - 1) / per) * lanes < threads) per /= 2;
-    return per;
+    const int each = (H + per - 1) / per;
+    return each > 0 ? (H + each - 1) / each : 1;
 }
 
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s)
@@ -643,7 +645,7 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s)
     return by_vector(a, false, [&](auto dt, auto v, auto ns, auto swap) {
         const Cut c = make_cut<v>(a.D, a.R, a.interleaved);
         const int H = a.H[0] > a.H[1] ? a.H[0] : a.H[1];
-        const int per = heads_of_item(a.T, H, c.lanes, 152 * 768);
+        const int per = heads_of_item(a.T, H, c.lanes, 152 * 768, 16);
         const int64_t threads = a.T * ((H + per - 1) / per) * c.lanes;
         const int64_t need = (threads + kRopeThreads - 1) / kRopeThreads;
         const unsigned blocks = (unsigned)(need < kRopeBlocks ? need : kRopeBlocks);
@@ -658,7 +660,7 @@ cudaError_t launch_rope_grad(const RopeArgs& a, cudaStream_t s)
     return by_vector(a, true, [&](auto dt, auto v, auto ns, auto swap) {
         const Cut c = make_cut<v>(a.D, a.R, a.interleaved);
         const int H = a.H[0] > a.H[1] ? a.H[0] : a.H[1];
-        const int per = heads_of_item(rope_part_tokens(a.T), H, c.lanes, kRopeGradThreads);
+        const int per = heads_of_item(rope_part_tokens(a.T), H, c.lanes, kRopeGradThreads, 8);
         return launch_kernel(k_rope_grad<dt, v, ns, swap>, dim3((unsigned)rope_parts(a.T), 2),
                              dim3(kRopeGradThreads), 0, s, true, 0u, a, per);
     });
