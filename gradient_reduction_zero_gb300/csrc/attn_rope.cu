@@ -12,8 +12,8 @@
 // head.  A group of lanes takes one token and several of its heads, and
 // computes the token's sines and cosines once for all of them.
 //
-// Measured: 16,384 tokens of 32 + 8 heads of 128 in bf16 71 us (4.8 TB/s); the gradient of
-// 32,768 tokens of 25 + 25 heads of 64 177 us (3.6 TB/s).
+// Measured: 16,384 tokens of 32 + 8 heads of 128 in bf16 67 us (5.0 TB/s); the gradient of
+// 32,768 tokens of 25 + 25 heads of 64 159 us (4.0 TB/s).
 //
 // Angles: a frequency is taken as a fraction of a turn in 128-bit fixed point, whose
 // product with a 64-bit position wraps exactly: far positions lose nothing, where a
@@ -31,9 +31,11 @@ namespace dpz {
 namespace {
 
 // Threads of a block, rows that a lane has under way, and blocks that stay: what the registers
-// hold decides the speed (bytes in flight), not the arithmetic.  One row under way 82 us, four
-// 71; the gradient 177 us with two blocks of 256 threads and one row, 254 with one block
-// of 384 and two rows.
+// hold decides the speed (bytes in flight), not the arithmetic.  One row under way 87 us, four
+// 83 (67 with blocks that stay and heads shared out evenly); the gradient 159 us with two
+// blocks of 256 threads an SM and one row, 226 with three of vectors half as long and
+// two rows, and before the heads were shared out evenly 173 against 254 with one block of 384
+// and two rows.
 constexpr int kRopeThreads = 256, kRopeAhead = 4, kRopeBlocks = 304;
 constexpr int kRopeGradThreads = 256, kRopeGradAhead = 1;
 
