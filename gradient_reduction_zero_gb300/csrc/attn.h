@@ -115,9 +115,11 @@ __device__ __forceinline__ void seq_bounds(const void* cu, int itype, int64_t b,
     *n = (int)(e > a ? e - a : 0);
 }
 
+constexpr int kSortedSeqs = 32;
+
 // Tile number `tile` of all sequences' tiles of `per` rows, over the queries
-// (of_keys false) or the keys: by position in sequences of equal length, else by
-// sequence.  Called by whole warps with equal arguments: with offsets, 32
+// (of_keys false) or the keys: by position in sequences of equal length and in up to
+// kSortedSeqs packed ones, else by sequence.  Called by whole warps with equal arguments: with offsets, 32
 // sequences' numbers of tiles are summed at a time.  The number of tiles is at
 // most tiles_bound(), below 2^31.
 __device__ __forceinline__ Tile find_tile(const AttnArgs& a, int tile, int per, bool of_keys)
@@ -133,6 +135,27 @@ __device__ __forceinline__ Tile find_tile(const AttnArgs& a, int tile, int per, 
         if ((int64_t)at * per < len) {
             b = (int)((unsigned)tile - at * n);
             t.row0 = (int)at * per;
+        }
+    } else if (a.B <= kSortedSeqs) {
+        // a sequence to a lane; the tiles at one position of all that reach it, then the next
+        // position's, in steps over which the same sequences reach it
+        const int lane = threadIdx.x & 31;
+        int64_t first;
+        int n = 0, at = 0, left = tile;
+        if (lane < a.B) seq_bounds(cu, a.itype, lane, 0, T, &first, &n);
+        const int mine = (int)((unsigned)(n + per - 1) / (unsigned)per);
+        while (true) {
+            const unsigned reach = __ballot_sync(0xffffffffu, mine > at);
+            if (reach == 0) break;
+            const int many = __popc(reach);
+            const int until = __reduce_min_sync(0xffffffffu, mine > at ? mine : 0x7fffffff);
+            if (left < (until - at) * many) {
+                b = (int)__fns(reach, 0, left % many + 1);
+                t.row0 = (at + left / many) * per;
+                break;
+            }
+            left -= (until - at) * many;
+            at = until;
         }
     } else {
         const int lane = threadIdx.x & 31;

@@ -145,13 +145,15 @@ struct Item {
     int first;         // the first of them (forward)
 };
 
-// The block's item of a round.  Where items are in order of length (sequences of equal
-// length), there and back, so that the block with the longest item of one round has the shortest
-// of the next: 8 x 1,024 tokens of 32 + 8 heads of 128, gradients of keys and values,
-// 124 us against 150 round after round.  Packed sequences follow one another, and there and
-// back sorts nothing: 2,069 us against 1,935 for the gradient of nine of them.
-__device__ __forceinline__ int64_t item_of_round(int64_t round, bool sorted)
+// The block's item of a round.  Where items are in order of length (find_tile sorts sequences of
+// equal length and few packed ones), there and back, so that the block with the longest
+// item of one round has the shortest of the next: 8 x 1,024 tokens of 32 + 8 heads of 128,
+// gradients of keys and values, 124 us against 150 round after round.  Many packed sequences
+// follow one another, and there and back sorts nothing.  (Gradient of nine packed sequences of
+// 32 + 8 heads of 128: 1,732 us by position, 1,813 by sequence, 5 % more there and back.)
+__device__ __forceinline__ int64_t item_of_round(int64_t round, const AttnArgs& a)
 {
+    const bool sorted = a.cu_q == nullptr || a.B <= kSortedSeqs;
     const unsigned b = sorted && round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
     return round * gridDim.x + b;
 }
@@ -486,7 +488,7 @@ k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a,
         Item m{};
         // in parts: one item for the blocks of a cluster
         for (int64_t round = 0; round * (SPLIT ? 1 << 30 : gridDim.x) < items && going; ++round) {
-            const int64_t w = SPLIT ? blockIdx.x / parts : item_of_round(round, a.cu_q == nullptr);
+            const int64_t w = SPLIT ? blockIdx.x / parts : item_of_round(round, a);
             if (w >= items) continue;
             // the tiles at the end of a sequence see the most keys and go first
             const int tile = (int)(w / groups);
@@ -868,7 +870,7 @@ k_attn_tc_dq(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs
         bool going = true;
         Item m{};
         for (int64_t round = 0; round * gridDim.x < items && going; ++round) {
-            const int64_t w = item_of_round(round, a.cu_q == nullptr);
+            const int64_t w = item_of_round(round, a);
             if (w >= items) continue;
             // the tiles at the end of a sequence see the most keys and go first
             const int tile = (int)(w / a.Hq);
@@ -1152,7 +1154,7 @@ k_attn_tc_dkv(const __grid_constant__ Maps maps, const __grid_constant__ AttnArg
         bool going = true;
         Item m{};
         for (int64_t round = 0; round * gridDim.x < items && going; ++round) {
-            const int64_t w = item_of_round(round, a.cu_q == nullptr);
+            const int64_t w = item_of_round(round, a);
             if (w >= items) continue;
             // the first keys of a sequence are seen by the most queries: tiles in order
             const int tile = (int)(w / a.Hk);
